@@ -313,7 +313,7 @@ def _store(st):
         p = st["problem"]
         p.cache_store(st["k_new"], st["v_new"], st["k_cache"], st["v_cache"], st["table"], st["cu"],
                       st["used"], st["n"], st["total_q"], st["max_q"], st["max_k"])
-        p.cache_expand(st["k_cache"], st["v_cache"], st["table"], st["used"], st["n"], st["max_k"],
+        p.cache_expand(st["k_cache"], st["v_cache"], st["table"], st["used"], st["n"], st["max_q"],
                        st["k_out"], st["v_out"], st["out_table"], begin=st["begin"])
         return [st["k_out"], st["v_out"]]
     s, pos = _token_place(st)
