@@ -71,7 +71,10 @@ enum {
     UA_FLAG_ALIBI = 1u << 2,
     UA_FLAG_WINDOW = 1u << 3,
     UA_FLAG_SINKS = 1u << 4,
-    UA_FLAG_QQ_BIAS = 1u << 5
+    UA_FLAG_QQ_BIAS = 1u << 5,
+    /* Descriptor only: the problem may run ua_forward_weights (its score
+     * workspace is allocated at creation); never part of a call's flags. */
+    UA_FLAG_KEY_WEIGHTS = 1u << 6
 };
 
 /* Bits of the device error word. */
@@ -89,8 +92,17 @@ enum {
  * each; OCP e4m3: bias 7, subnormals, no infinities, 0x7f / 0xff NaN) with one
  * scale per tensor, K = code * k_scale, V = code * v_scale (gfx950 page,
  * section 7.3 "fp8 KV cache (bf16-Q + fp8-KV)").  The fp8 cache is read by
- * the DECODE_TC path only. */
-enum { UA_DTYPE_BF16 = 0, UA_DTYPE_FP8_E4M3 = 1 };
+ * the DECODE_TC path only.
+ *
+ * UA_DTYPE_FP4_E2M1: caches in 4 bits, uint8 [num_blocks, H_k, P] with
+ * P = b * (d / 2 + d / 16) bytes for one (block, KV head): first b rows of
+ * d / 2 bytes holding e2m1 codes (dim 2i in the low nibble of byte i, dim
+ * 2i + 1 in the high one; magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign
+ * bit), then b rows of d / 16 e4m3 scales, one per 16 consecutive dims.
+ * K = code * scale * k_scale, V = code * scale * v_scale; ua_cache_store
+ * writes this format, and a (block, KV head) is one contiguous, 16-byte
+ * aligned run.  Any d, b, g and S_q; needs path AUTO. */
+enum { UA_DTYPE_BF16 = 0, UA_DTYPE_FP8_E4M3 = 1, UA_DTYPE_FP4_E2M1 = 2 };
 
 /* Execution path (gfx950 spec section 6: a path whose query-tile grid fills
  * the device versus split-KV segments plus a reduction).
@@ -139,9 +151,10 @@ typedef struct ua_problem_desc {
     int32_t kv_dtype;           /* UA_DTYPE_BF16, or UA_DTYPE_FP8_E4M3 (needs d = 128 and
                                    path AUTO or DECODE_TC; a call whose shape the
                                    decode kernel does not take returns
-                                   UA_ERR_UNSUPPORTED) */
-    float k_scale;              /* fp8 caches: K = code * k_scale, > 0; else ignored */
-    float v_scale;              /* fp8 caches: V = code * v_scale, > 0; else ignored */
+                                   UA_ERR_UNSUPPORTED), or UA_DTYPE_FP4_E2M1 (needs
+                                   path AUTO) */
+    float k_scale;              /* fp8 / fp4 caches: factor of every K value, > 0; else ignored */
+    float v_scale;              /* fp8 / fp4 caches: factor of every V value, > 0; else ignored */
     int32_t split_partials;     /* UA_PARTIALS_F32 (0, the default) or UA_PARTIALS_BF16 */
 } ua_problem_desc;
 
@@ -337,6 +350,126 @@ ua_status ua_forward_noalloc(const ua_problem_desc *desc, const void *q, const v
                              int32_t max_seqlen_k, uint32_t flags, const float *sinks,
                              const float *alibi_slopes, void *out, int32_t *device_error,
                              void *stream);
+
+/*
+ * ---- the cache: writing, reading back, weighing and thinning it ----
+ * (Additions of this library; the pages leave the cache's writer open.)
+ *
+ * The calls below are asynchronous on `stream`, allocate nothing, launch
+ * nothing when they return an error, need the problem's device to be current
+ * (else UA_ERR_INVALID_ARG), and report malformed metadata through the
+ * problem's device error word like ua_forward.  Calls on one problem share
+ * its workspace: calls (or graph replays) that may overlap on the GPU need a
+ * problem each.
+ *
+ * ua_cache_store -- write the chunk's K and V rows into the paged caches: row
+ * i of sequence s goes to key position ctx + i (ctx = S_k - S_q, the place
+ * ua_forward expects it), block block_table[s][j / b], slot j % b.
+ *   k_new, v_new  bf16 [total_q, H_k, d], tokens new_stride elements apart
+ *                 (>= H_k * d, a multiple of 8; a slice of a fused QKV
+ *                 projection), 16-byte aligned
+ * By the problem's kv_dtype, with scale = k_scale or v_scale and
+ * y = x / scale rounded to fp32:
+ *   BF16      the bits of x;
+ *   FP8_E4M3  y rounded to nearest even, magnitudes above 448 (infinities
+ *             too) to 448, NaN to 0x7f;
+ *   FP4_E2M1  per 16 dims s = max|y| / 6 rounded to e4m3 (nearest even, at
+ *             most 448), codes y / s rounded to nearest even, at most 6, the
+ *             sign kept; s = 0 stores zero codes; a NaN among the 16 stores
+ *             s = 0x7f and zero codes, so that all 16 read back as NaN.  The
+ *             rounding is that of the exact quotients.
+ * Malformed sequences are skipped; rows whose block id is out of range are
+ * dropped (UA_DEVERR_BLOCK_ID).  No slot may be written by two rows of a call.
+ */
+ua_status ua_cache_store(ua_problem *p, const void *k_new, const void *v_new, int64_t new_stride,
+                         void *k_cache, void *v_cache, const int32_t *block_table,
+                         const int32_t *cu_seqlens_q, const int32_t *seqused_k, int32_t num_seqs,
+                         int64_t total_q, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                         void *stream);
+
+/*
+ * ua_cache_expand -- the values of the cached keys begin[s] <= j < S_k of
+ * every sequence (begin NULL: from 0), rounded once to bf16, into bf16 pages
+ * [out_num_blocks, b, H_k, d] at block out_block_table[s][j / b] (rows of
+ * out_table_stride ids), slot j % b.  A bf16 problem with these pages runs the
+ * prefill kernels over what a 4-bit or fp8 cache holds.  Exact when the scale
+ * is a power of two.
+ *   max_keys  host-side upper bound on S_k(s) - begin(s); a sequence above
+ *             it, or with begin outside [0, S_k], is skipped
+ *             (UA_DEVERR_BOUNDS)
+ * Rows of other keys are left as they are.  Keys whose source or destination
+ * block id is out of range are dropped (UA_DEVERR_BLOCK_ID).
+ */
+ua_status ua_cache_expand(ua_problem *p, const void *k_cache, const void *v_cache,
+                          const int32_t *block_table, const int32_t *seqused_k,
+                          const int32_t *begin, int32_t num_seqs, int32_t max_keys, void *k_out,
+                          void *v_out, const int32_t *out_block_table, int32_t out_table_stride,
+                          int64_t out_num_blocks, void *stream);
+
+/*
+ * ua_forward_weights -- ua_forward plus the accumulated attention weight of
+ * every cached key.  For a sequence with S_q >= 1 query rows, KV head k and
+ * key j < S_k
+ *
+ *     out_w[s][k][j] = decay * in_w[s][k][j] * [j < ctx]
+ *                      + sum over the rows i and the g query heads h of k of
+ *                        softmax(x_(i,h))_j
+ *
+ * (the sink's share of a row goes to no key; an empty row adds nothing; the
+ * chunk's own keys start from zero, whatever in_w holds).  Entries j >= S_k,
+ * and all entries of malformed sequences or of sequences without query rows,
+ * are left as they are.  Every sum has one order, so equal calls give equal
+ * bits.
+ *   weights_in   fp32 [num_seqs, H_k, weight_stride], or NULL for zeros (not
+ *                read when decay = 0)
+ *   weights_out  same layout; may be weights_in itself (else disjoint)
+ *   weight_stride >= max_seqlen_k
+ *   decay        finite and >= 0
+ * The problem must have been created with UA_FLAG_KEY_WEIGHTS, which
+ * allocates 4 * max_total_q * H_q * (max_blocks_per_seq * b, rounded up to
+ * 128) bytes for the scores: size max_total_q for the steps that are weighed
+ * (a decode batch, a prompt's last tokens).  Needs g <= 16 on bf16 and fp8
+ * caches, and path AUTO (else UA_ERR_UNSUPPORTED).
+ */
+ua_status ua_forward_weights(ua_problem *p, const void *q, const void *k_cache,
+                             const void *v_cache, const int32_t *block_table,
+                             const int32_t *cu_seqlens_q, const int32_t *seqused_k,
+                             int32_t num_seqs, int64_t total_q, int32_t max_seqlen_q,
+                             int32_t max_seqlen_k, uint32_t flags, const float *sinks,
+                             const float *alibi_slopes, const float *weights_in,
+                             float *weights_out, int64_t weight_stride, float decay, void *out,
+                             void *stream);
+
+/*
+ * ua_cache_evict -- keep at most `budget` keys of every (sequence, KV head):
+ * all of them when S_k <= budget, else the last `recent` keys and the
+ * budget - recent heaviest of the keys before those (ties: the lowest
+ * position; NaN weighs less than anything).  The kept keys move, in their
+ * order, to positions 0, 1, ... of dst_block_table, each KV head with its own
+ * choice; positions afterwards are ranks, not the original positions, so
+ * ALiBi and windows no longer mean distances.
+ *   dst_block_table  same layout as block_table.  NULL or block_table itself
+ *                    evicts in place; any other table must name blocks that
+ *                    block_table does not name (the sources stay as they are,
+ *                    so a prefix shared with another sequence survives).
+ *                    Within a table no block may be named twice, or in place
+ *                    be shared.
+ *   weights_in       fp32 [num_seqs, H_k, weight_stride], the weights
+ *   weights_out      the kept keys' weights at their new positions (entries
+ *                    past them are left as they are); may be weights_in
+ *   kept             int32 [num_seqs, H_k, budget]: the kept positions,
+ *                    ascending, then -1
+ *   seqused_out      int32 [num_seqs]: min(S_k, budget); may be seqused_k
+ *   budget >= 1, 0 <= recent <= budget, weight_stride >= max_seqlen_k
+ * A malformed length keeps nothing (kept -1, seqused_out 0, the cache and the
+ * weights as they were; UA_DEVERR_BOUNDS).  Keys whose source or destination
+ * block id is out of range are not moved (UA_DEVERR_BLOCK_ID).
+ */
+ua_status ua_cache_evict(ua_problem *p, void *k_cache, void *v_cache, const int32_t *block_table,
+                         const int32_t *dst_block_table, const int32_t *seqused_k,
+                         int32_t num_seqs, int32_t max_seqlen_k, const float *weights_in,
+                         float *weights_out, int64_t weight_stride, int32_t budget,
+                         int32_t recent, int32_t *kept, int32_t *seqused_out, void *stream);
 
 /* Free the workspace and the problem.  NULL is a no-op. */
 void ua_destroy(ua_problem *p);

@@ -18,6 +18,7 @@ UA_FLAG_ALIBI = 1 << 2
 UA_FLAG_WINDOW = 1 << 3
 UA_FLAG_SINKS = 1 << 4
 UA_FLAG_QQ_BIAS = 1 << 5
+UA_FLAG_KEY_WEIGHTS = 1 << 6
 UA_PARTIALS_F32 = 0
 UA_PARTIALS_BF16 = 1
 
@@ -29,6 +30,7 @@ UA_DEVERR_TIMEOUT = 1 << 4
 
 UA_DTYPE_BF16 = 0
 UA_DTYPE_FP8_E4M3 = 1
+UA_DTYPE_FP4_E2M1 = 2
 
 UA_PATH_AUTO = 0
 UA_PATH_SPLIT_KV = 1
@@ -101,6 +103,16 @@ def load_library():
     lib.ua_forward_topk.argtypes = [vp] * 7 + [i32, ctypes.c_int64, i32, i32, vp, vp, i32,
                                                ctypes.c_uint32, vp, vp, vp, vp]
     lib.ua_forward_topk.restype = ctypes.c_int
+    f32 = ctypes.c_float
+    lib.ua_forward_weights.argtypes = [vp] * 7 + [i32, i64, i32, i32, u32, vp, vp, vp, vp, i64, f32,
+                                                  vp, vp]
+    lib.ua_forward_weights.restype = ctypes.c_int
+    lib.ua_cache_store.argtypes = [vp, vp, vp, i64, vp, vp, vp, vp, vp, i32, i64, i32, i32, vp]
+    lib.ua_cache_store.restype = ctypes.c_int
+    lib.ua_cache_expand.argtypes = [vp] * 6 + [i32, i32, vp, vp, vp, i32, i64, vp]
+    lib.ua_cache_expand.restype = ctypes.c_int
+    lib.ua_cache_evict.argtypes = [vp] * 6 + [i32, i32, vp, vp, i64, i32, i32, vp, vp, vp]
+    lib.ua_cache_evict.restype = ctypes.c_int
     lib.ua_set_qq_bias.argtypes = [vp, vp, ctypes.c_int64, ctypes.c_int64]
     lib.ua_set_qq_bias.restype = ctypes.c_int
     lib.ua_debug_stall_data_waits.argtypes = [vp, i32, i64]
@@ -194,6 +206,68 @@ def ua_forward_topk(problem, q, k_cache, v_cache, block_table, cu_seqlens_q, seq
         _ptr(alibi_slopes), _ptr(out), _stream(stream))
 
 
+def ua_forward_weights(problem, q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k,
+                       num_seqs, total_q, max_seqlen_q, max_seqlen_k, flags, sinks, alibi_slopes,
+                       weights_in, weights_out, weight_stride, decay, out, stream=None):
+    """Enqueue a forward pass that also accumulates every cached key's attention
+    weight (fp32 [num_seqs, H_k, weight_stride]).  Returns the status."""
+    return load_library().ua_forward_weights(
+        problem, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(cu_seqlens_q),
+        _ptr(seqused_k), num_seqs, total_q, max_seqlen_q, max_seqlen_k, flags, _ptr(sinks),
+        _ptr(alibi_slopes), _ptr(weights_in), _ptr(weights_out), weight_stride, decay, _ptr(out),
+        _stream(stream))
+
+
+def ua_cache_store(problem, k_new, v_new, new_stride, k_cache, v_cache, block_table, cu_seqlens_q,
+                   seqused_k, num_seqs, total_q, max_seqlen_q, max_seqlen_k, stream=None):
+    """Enqueue the write of a chunk's K/V rows into the paged caches.  Returns
+    the status."""
+    return load_library().ua_cache_store(
+        problem, _ptr(k_new), _ptr(v_new), new_stride, _ptr(k_cache), _ptr(v_cache),
+        _ptr(block_table), _ptr(cu_seqlens_q), _ptr(seqused_k), num_seqs, total_q, max_seqlen_q,
+        max_seqlen_k, _stream(stream))
+
+
+def ua_cache_expand(problem, k_cache, v_cache, block_table, seqused_k, begin, num_seqs, max_keys,
+                    k_out, v_out, out_block_table, out_table_stride, out_num_blocks, stream=None):
+    """Enqueue the expansion of cached keys into bf16 pages.  Returns the status."""
+    return load_library().ua_cache_expand(
+        problem, _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(seqused_k), _ptr(begin),
+        num_seqs, max_keys, _ptr(k_out), _ptr(v_out), _ptr(out_block_table), out_table_stride,
+        out_num_blocks, _stream(stream))
+
+
+def ua_cache_evict(problem, k_cache, v_cache, block_table, dst_block_table, seqused_k, num_seqs,
+                   max_seqlen_k, weights_in, weights_out, weight_stride, budget, recent, kept,
+                   seqused_out, stream=None):
+    """Enqueue an eviction by key weights.  Returns the status."""
+    return load_library().ua_cache_evict(
+        problem, _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(dst_block_table),
+        _ptr(seqused_k), num_seqs, max_seqlen_k, _ptr(weights_in), _ptr(weights_out),
+        weight_stride, budget, recent, _ptr(kept), _ptr(seqused_out), _stream(stream))
+
+
+def cache_shape(num_blocks, num_kv_heads, head_size, block_size, kv_dtype=UA_DTYPE_BF16):
+    """Shape of one K or V cache: bf16 or uint8 [num_blocks, b, H_k, d], or for
+    the 4-bit format uint8 [num_blocks, H_k, bytes of a (block, KV head) page]."""
+    if kv_dtype == UA_DTYPE_FP4_E2M1:
+        return (num_blocks, num_kv_heads, block_size * (head_size // 2 + head_size // 16))
+    return (num_blocks, block_size, num_kv_heads, head_size)
+
+
+def _token_stride(t, name):
+    """Elements between the tokens of a [total, H_k, d] tensor whose rows are contiguous."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError("%s must be [total_q, H_k, d] with contiguous heads" % name)
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def _weight_stride(t, name):
+    if t.dim() != 3 or t.stride(2) != 1 or t.stride(0) != t.shape[1] * t.stride(1):
+        raise ValueError("%s must be [num_seqs, H_k, n] with evenly spaced rows" % name)
+    return t.stride(1)
+
+
 def ua_forward_host(problem, q_host, k_cache, v_cache, block_table_host, cu_seqlens_q_host,
                     seqused_k_host, num_seqs, total_q, max_seqlen_q, max_seqlen_k, flags,
                     sinks_host, alibi_host, out_host, stream=None):
@@ -265,6 +339,7 @@ class Problem:
         self.flags = flags
         self.head_size = head_size
         self.num_q_heads = num_q_heads
+        self.num_kv_heads = num_kv_heads
 
     @classmethod
     def for_workload(cls, w, max_total_q=None, max_num_seqs=None, extra_flags=0,
@@ -305,6 +380,67 @@ class Problem:
         if st != UA_OK:
             raise UAError(st, "ua_forward_topk")
         return out
+
+    def forward_weights(self, q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, num_seqs,
+                        total_q, max_seqlen_q, max_seqlen_k, flags, weights_in, weights_out,
+                        decay=1.0, sinks=None, alibi_slopes=None, out=None, stream=None):
+        """``forward`` that also writes decay * weights_in plus this call's
+        attention weights to ``weights_out`` (fp32 [num_seqs, H_k, n >= max_seqlen_k];
+        ``weights_in`` may be the same tensor, or None for zeros)."""
+        stride = _weight_stride(weights_out, "weights_out")
+        if weights_in is not None and _weight_stride(weights_in, "weights_in") != stride:
+            raise ValueError("weights_in and weights_out must share a row stride")
+        if out is None:
+            import torch
+            out = torch.empty_like(q)
+        st = ua_forward_weights(self.handle, q, k_cache, v_cache, block_table, cu_seqlens_q,
+                                seqused_k, num_seqs, total_q, max_seqlen_q, max_seqlen_k, flags,
+                                sinks, alibi_slopes, weights_in, weights_out, stride, decay, out,
+                                stream)
+        if st != UA_OK:
+            raise UAError(st, "ua_forward_weights")
+        return out
+
+    def cache_store(self, k_new, v_new, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k,
+                    num_seqs, total_q, max_seqlen_q, max_seqlen_k, stream=None):
+        """Write a chunk's rows (bf16 [total_q, H_k, d]; tokens may be strided)
+        to the positions ``forward`` expects them at."""
+        stride = _token_stride(k_new, "k_new")
+        if _token_stride(v_new, "v_new") != stride:
+            raise ValueError("k_new and v_new must share a token stride")
+        st = ua_cache_store(self.handle, k_new, v_new, stride, k_cache, v_cache, block_table,
+                            cu_seqlens_q, seqused_k, num_seqs, total_q, max_seqlen_q,
+                            max_seqlen_k, stream)
+        if st != UA_OK:
+            raise UAError(st, "ua_cache_store")
+
+    def cache_expand(self, k_cache, v_cache, block_table, seqused_k, num_seqs, max_keys, k_out,
+                     v_out, out_block_table, begin=None, stream=None):
+        """Expand the keys from ``begin`` (or 0) on into the bf16 pages
+        ``k_out`` / ``v_out`` [blocks, b, H_k, d]."""
+        if out_block_table.dim() != 2 or out_block_table.stride(1) != 1:
+            raise ValueError("out_block_table must be [num_seqs, n] with unit inner stride")
+        st = ua_cache_expand(self.handle, k_cache, v_cache, block_table, seqused_k, begin,
+                             num_seqs, max_keys, k_out, v_out, out_block_table,
+                             out_block_table.stride(0), k_out.shape[0], stream)
+        if st != UA_OK:
+            raise UAError(st, "ua_cache_expand")
+
+    def cache_evict(self, k_cache, v_cache, block_table, seqused_k, num_seqs, max_seqlen_k,
+                    weights_in, weights_out, budget, recent, kept, seqused_out,
+                    dst_block_table=None, stream=None):
+        """Keep ``budget`` keys of every (sequence, KV head) by weight, in place
+        or into ``dst_block_table``; ``kept`` int32 [num_seqs, H_k, budget]."""
+        stride = _weight_stride(weights_in, "weights_in")
+        if _weight_stride(weights_out, "weights_out") != stride:
+            raise ValueError("weights_in and weights_out must share a row stride")
+        if tuple(kept.shape) != (num_seqs, self.num_kv_heads, budget) or not kept.is_contiguous():
+            raise ValueError("kept must be a contiguous [num_seqs, H_k, budget]")
+        st = ua_cache_evict(self.handle, k_cache, v_cache, block_table, dst_block_table, seqused_k,
+                            num_seqs, max_seqlen_k, weights_in, weights_out, stride, budget,
+                            recent, kept, seqused_out, stream)
+        if st != UA_OK:
+            raise UAError(st, "ua_cache_evict")
 
     def forward_workload(self, w, out=None, stream=None):
         """Forward on a device-resident ``workloads.Workload`` (through

@@ -12,12 +12,16 @@
 #include <cstring>
 #include <mutex>
 
+#include "ua_cache.h"
 #include "ua_common.cuh"
 #include "ua_decode_tc.h"
+#include "ua_fp4.cuh"
+#include "ua_fp4.h"
 #include "ua_prefill.h"
 #include "ua_split.h"
 #include "ua_tmap.h"
 #include "ua_topk.h"
+#include "ua_weights.h"
 
 namespace {
 
@@ -47,6 +51,9 @@ struct ua_problem {
     int32_t* d_err = nullptr;
     float* d_ws = nullptr;
     size_t ws_bytes = 0;
+    // scores of ua_forward_weights (UA_FLAG_KEY_WEIGHTS problems only)
+    float* d_scores = nullptr;
+    size_t scores_elems = 0;
     // work list of the persistent prefill kernel: entries, then the
     // per-sequence prefix, then [entries, claim counter]
     void* d_work = nullptr;
@@ -107,7 +114,7 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
     if (!d || !out) return UA_ERR_INVALID_ARG;
     *out = nullptr;
     const uint32_t known = UA_FLAG_CAUSAL | UA_FLAG_SOFTCAP | UA_FLAG_ALIBI | UA_FLAG_WINDOW |
-                           UA_FLAG_SINKS | UA_FLAG_QQ_BIAS;
+                           UA_FLAG_SINKS | UA_FLAG_QQ_BIAS | UA_FLAG_KEY_WEIGHTS;
     if (d->num_q_heads <= 0 || d->num_kv_heads <= 0 || d->num_q_heads % d->num_kv_heads != 0)
         return UA_ERR_INVALID_ARG;
     if (d->num_blocks <= 0 || d->max_num_seqs <= 0 || d->max_blocks_per_seq <= 0 ||
@@ -120,11 +127,17 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
     if ((d->flags & UA_FLAG_WINDOW) && (d->window < 1 || !(d->flags & UA_FLAG_CAUSAL)))
         return UA_ERR_INVALID_ARG;
     if (d->dtype != UA_DTYPE_BF16) return UA_ERR_UNSUPPORTED;
-    if (d->kv_dtype != UA_DTYPE_BF16 && d->kv_dtype != UA_DTYPE_FP8_E4M3) return UA_ERR_INVALID_ARG;
+    if (d->kv_dtype != UA_DTYPE_BF16 && d->kv_dtype != UA_DTYPE_FP8_E4M3 &&
+        d->kv_dtype != UA_DTYPE_FP4_E2M1)
+        return UA_ERR_INVALID_ARG;
+    if (d->kv_dtype != UA_DTYPE_BF16 &&
+        (!(d->k_scale > 0.f) || !std::isfinite(d->k_scale) || !(d->v_scale > 0.f) ||
+         !std::isfinite(d->v_scale)))
+        return UA_ERR_INVALID_ARG;
+    // One kernel family reads a 4-bit cache, whatever the call's shape.
+    if (d->kv_dtype == UA_DTYPE_FP4_E2M1 && d->path != UA_PATH_AUTO)
+        return d->path > UA_PATH_DECODE_TC ? UA_ERR_INVALID_ARG : UA_ERR_UNSUPPORTED;
     if (d->kv_dtype == UA_DTYPE_FP8_E4M3) {
-        if (!(d->k_scale > 0.f) || !std::isfinite(d->k_scale) || !(d->v_scale > 0.f) ||
-            !std::isfinite(d->v_scale))
-            return UA_ERR_INVALID_ARG;
         // Only the decode tensor-core kernel reads an fp8 cache.
         if (d->head_size != 128) return UA_ERR_UNSUPPORTED;
         if (d->path != UA_PATH_AUTO && d->path != UA_PATH_DECODE_TC) return UA_ERR_UNSUPPORTED;
@@ -150,6 +163,13 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
     const size_t row_bytes = size_t(d->head_size + 2) * sizeof(float);
     const size_t want = size_t(d->max_total_q) * d->num_q_heads * row_bytes * 16;
     p->ws_bytes = std::min(want, kWorkspaceCap);
+    if (d->flags & UA_FLAG_KEY_WEIGHTS) {
+        // Key weights always go through partials: room for one segment of every
+        // row, and the rows' scores.
+        p->ws_bytes = std::max(p->ws_bytes, size_t(d->max_total_q) * d->num_q_heads * row_bytes);
+        const size_t keys = ((size_t)d->max_blocks_per_seq * d->block_size + 127) / 128 * 128;
+        p->scores_elems = size_t(d->max_total_q) * d->num_q_heads * keys;
+    }
     // Work-list entries: every call's (total_q / (2 ppt) + num_seqs) entries
     // without a KV split, and room for the splits the planner makes when the
     // grid is small (about 4 x 152 units per KV head x up to 64 segments).
@@ -159,10 +179,12 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
     const size_t work_bytes = (size_t)cap * sizeof(int2) + (size_t)(d->max_num_seqs + 1) * 4 + 16;
     if (cudaMalloc(&p->d_err, sizeof(int32_t)) != cudaSuccess ||
         cudaMalloc(&p->d_ws, p->ws_bytes) != cudaSuccess ||
-        cudaMalloc(&p->d_work, work_bytes) != cudaSuccess) {
+        cudaMalloc(&p->d_work, work_bytes) != cudaSuccess ||
+        (p->scores_elems && cudaMalloc(&p->d_scores, p->scores_elems * sizeof(float)) != cudaSuccess)) {
         cudaGetLastError();
         cudaFree(p->d_err);
         cudaFree(p->d_ws);
+        cudaFree(p->d_work);
         delete p;
         return UA_ERR_OUT_OF_MEMORY;
     }
@@ -172,6 +194,7 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
         cudaFree(p->d_err);
         cudaFree(p->d_ws);
         cudaFree(p->d_work);
+        cudaFree(p->d_scores);
         delete p;
         return UA_ERR_CUDA;
     }
@@ -184,6 +207,7 @@ void ua_destroy(ua_problem* p) {
     cudaFree(p->d_err);
     cudaFree(p->d_ws);
     cudaFree(p->d_work);
+    cudaFree(p->d_scores);
     cudaFree(p->st_q);
     cudaFree(p->st_out);
     cudaFree(p->st_bt);
@@ -250,7 +274,7 @@ ua_status prepare_call(ua_problem* p, const void* q, const void* k_cache, const 
     if (max_seqlen_q < 0 || max_seqlen_k < 0 || max_seqlen_q > max_seqlen_k ||
         (int64_t)max_seqlen_k > (int64_t)d.max_blocks_per_seq * d.block_size)
         return UA_ERR_INVALID_ARG;
-    if ((flags & ~d.flags) != 0) return UA_ERR_INVALID_ARG;
+    if ((flags & ~(d.flags & ~(uint32_t)UA_FLAG_KEY_WEIGHTS)) != 0) return UA_ERR_INVALID_ARG;
     if ((flags & UA_FLAG_WINDOW) && !(flags & UA_FLAG_CAUSAL)) return UA_ERR_INVALID_ARG;
     if (((flags & UA_FLAG_SINKS) != 0) != (sinks != nullptr)) return UA_ERR_INVALID_ARG;
     if (((flags & UA_FLAG_ALIBI) != 0) != (alibi_slopes != nullptr)) return UA_ERR_INVALID_ARG;
@@ -300,8 +324,8 @@ ua_status prepare_call(ua_problem* p, const void* q, const void* k_cache, const 
     fp.softcap = d.softcap;
     fp.window = d.window;
     fp.kv_fp8 = d.kv_dtype == UA_DTYPE_FP8_E4M3 ? 1 : 0;
-    fp.k_scale = fp.kv_fp8 ? d.k_scale : 1.f;
-    fp.v_scale = fp.kv_fp8 ? d.v_scale : 1.f;
+    fp.k_scale = d.kv_dtype != UA_DTYPE_BF16 ? d.k_scale : 1.f;
+    fp.v_scale = d.kv_dtype != UA_DTYPE_BF16 ? d.v_scale : 1.f;
     fp.part_bf16 = d.split_partials == UA_PARTIALS_BF16 ? 1 : 0;
     fp.work_list = static_cast<int2*>(p->d_work);
     fp.seq_prefix = reinterpret_cast<int32_t*>(fp.work_list + p->work_cap);
@@ -314,6 +338,100 @@ ua_status prepare_call(ua_problem* p, const void* q, const void* k_cache, const 
         fp.qq_stride = p->qq_stride;
     }
     return UA_OK;
+}
+
+// The cache's tensor maps with 16-slot boxes (re-encoded when the caches
+// change), and with boxes of b slots for the tensor-core kernels.
+ua_status encode_maps(ua_problem* p, const void* k_cache, const void* v_cache, bool block_boxes) {
+    const ua_problem_desc& d = p->desc;
+    if (k_cache != p->map_k_ptr || v_cache != p->map_v_ptr) {
+        if (!encode_cache_map(&p->map_k16, k_cache, d, 16) ||
+            !encode_cache_map(&p->map_v16, v_cache, d, 16)) {
+            p->map_k_ptr = p->map_v_ptr = nullptr;
+            std::snprintf(g_cuda_err, sizeof g_cuda_err, "cuTensorMapEncodeTiled failed");
+            return UA_ERR_CUDA;
+        }
+        p->map_k_ptr = k_cache;
+        p->map_v_ptr = v_cache;
+        p->map_p_rows = 0;
+    }
+    if (block_boxes && p->map_p_rows != d.block_size) {
+        if (!encode_cache_map(&p->map_kp, k_cache, d, d.block_size) ||
+            !encode_cache_map(&p->map_vp, v_cache, d, d.block_size)) {
+            std::snprintf(g_cuda_err, sizeof g_cuda_err, "cuTensorMapEncodeTiled failed");
+            p->map_p_rows = 0;
+            return UA_ERR_CUDA;
+        }
+        p->map_p_rows = d.block_size;
+    }
+    return UA_OK;
+}
+
+// The call's partials behind each other in the problem's workspace.
+void set_partials(const ua_problem* p, ua::FwdParams* fp, int splits, int chunk) {
+    fp->splits = splits;
+    fp->chunk = chunk;
+    fp->part_o = p->d_ws;
+    fp->part_ml = p->d_ws + (size_t)fp->total_q * p->desc.num_q_heads * splits * p->desc.head_size;
+}
+
+ua_status run_combine(const ua::FwdParams& fp, cudaStream_t st) {
+    const cudaError_t e = ua::launch_combine(fp, st);
+    if (e == cudaSuccess) return UA_OK;
+    note_cuda(e, "combine kernel launch");
+    return UA_ERR_CUDA;
+}
+
+// Attention over a 4-bit cache; with fp->scores set partials are always
+// written and combined.
+ua_status run_fp4(ua_problem* p, ua::FwdParams* fp, cudaStream_t st) {
+    ua::Fp4Plan plan;
+    if (!ua::plan_fp4(*fp, p->num_sms, p->ws_bytes, &plan)) return UA_ERR_UNSUPPORTED;
+    set_partials(p, fp, plan.splits, plan.chunk);
+    prof_mark(p, true, st);
+    cudaError_t e = ua::launch_fp4(plan, *fp, st);
+    prof_mark(p, false, st);
+    if (e != cudaSuccess) {
+        note_cuda(e, "fp4 kernel launch");
+        return UA_ERR_CUDA;
+    }
+    const bool combine = plan.splits > 1 || fp->scores;
+    p->last_launches = combine ? 2 : 1;
+    p->last_path = combine ? "fp4+combine" : "fp4";
+    return combine ? run_combine(*fp, st) : UA_OK;
+}
+
+// The problem's device is the current one (the cache operators launch on it).
+bool on_device(const ua_problem* p) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return dev == p->device;
+}
+
+bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
+
+ua::CacheParams cache_params(const ua_problem* p, const void* k_cache, const void* v_cache,
+                             const int32_t* block_table, const int32_t* seqused_k, int32_t num_seqs) {
+    const ua_problem_desc& d = p->desc;
+    ua::CacheParams c{};
+    c.k_cache = static_cast<uint8_t*>(const_cast<void*>(k_cache));
+    c.v_cache = static_cast<uint8_t*>(const_cast<void*>(v_cache));
+    c.block_table = block_table;
+    c.seqused_k = seqused_k;
+    c.err = p->d_err;
+    c.num_blocks = d.num_blocks;
+    c.num_seqs = num_seqs;
+    c.bt_stride = d.max_blocks_per_seq;
+    c.hk = d.num_kv_heads;
+    c.d = d.head_size;
+    c.b = d.block_size;
+    c.kv_dtype = d.kv_dtype;
+    c.k_scale = d.kv_dtype != UA_DTYPE_BF16 ? d.k_scale : 1.f;
+    c.v_scale = d.kv_dtype != UA_DTYPE_BF16 ? d.v_scale : 1.f;
+    return c;
 }
 
 }  // namespace
@@ -336,17 +454,9 @@ ua_status ua_forward(ua_problem* p, const void* q, const void* k_cache, const vo
     const int g = fp.g;
     max_seqlen_k = fp.max_seqlen_k;
 
-    if (k_cache != p->map_k_ptr || v_cache != p->map_v_ptr) {
-        if (!encode_cache_map(&p->map_k16, k_cache, d, 16) ||
-            !encode_cache_map(&p->map_v16, v_cache, d, 16)) {
-            p->map_k_ptr = p->map_v_ptr = nullptr;
-            std::snprintf(g_cuda_err, sizeof g_cuda_err, "cuTensorMapEncodeTiled failed");
-            return UA_ERR_CUDA;
-        }
-        p->map_k_ptr = k_cache;
-        p->map_v_ptr = v_cache;
-        p->map_p_rows = 0;
-    }
+    if (d.kv_dtype == UA_DTYPE_FP4_E2M1) return run_fp4(p, &fp, st);
+    rs = encode_maps(p, k_cache, v_cache, false);
+    if (rs != UA_OK) return rs;
 
     // ---- path choice ------------------------------------------------------
     const int64_t rows_per_kv = (int64_t)g * max_seqlen_q;
@@ -367,15 +477,8 @@ ua_status ua_forward(ua_problem* p, const void* q, const void* k_cache, const vo
     }
     if (use_dec || use_tc) {
         // Both tensor-core kernels read the caches through boxes of b slots.
-        if (p->map_p_rows != d.block_size) {
-            if (!encode_cache_map(&p->map_kp, k_cache, d, d.block_size) ||
-                !encode_cache_map(&p->map_vp, v_cache, d, d.block_size)) {
-                std::snprintf(g_cuda_err, sizeof g_cuda_err, "cuTensorMapEncodeTiled failed");
-                p->map_p_rows = 0;
-                return UA_ERR_CUDA;
-            }
-            p->map_p_rows = d.block_size;
-        }
+        rs = encode_maps(p, k_cache, v_cache, true);
+        if (rs != UA_OK) return rs;
     }
     if (use_dec) {
         ua::DecodePlan plan;
@@ -543,6 +646,178 @@ ua_status ua_forward_topk(ua_problem* p, const void* q, const void* k_cache, con
     }
     p->last_launches = plan.launches;
     p->last_path = plan.splits > 1 ? "topk_tc+combine" : "topk_tc";
+    return UA_OK;
+}
+
+ua_status ua_forward_weights(ua_problem* p, const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_table, const int32_t* cu_seqlens_q,
+                             const int32_t* seqused_k, int32_t num_seqs, int64_t total_q,
+                             int32_t max_seqlen_q, int32_t max_seqlen_k, uint32_t flags,
+                             const float* sinks, const float* alibi_slopes, const float* weights_in,
+                             float* weights_out, int64_t weight_stride, float decay, void* out,
+                             void* stream) {
+    ua::FwdParams fp;
+    bool skip = false;
+    ua_status rs = prepare_call(p, q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k,
+                                num_seqs, total_q, max_seqlen_q, max_seqlen_k, flags, sinks,
+                                alibi_slopes, out, &fp, &skip);
+    if (rs != UA_OK) return rs;
+    const ua_problem_desc& d = p->desc;
+    if (!(d.flags & UA_FLAG_KEY_WEIGHTS) || !(decay >= 0.f) || !std::isfinite(decay) ||
+        weight_stride < max_seqlen_k || !on_device(p))
+        return UA_ERR_INVALID_ARG;
+    if (skip) return UA_OK;
+    if (!weights_out || (reinterpret_cast<uintptr_t>(weights_out) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(weights_in) & 3u) != 0)
+        return UA_ERR_INVALID_ARG;
+    if (d.path != UA_PATH_AUTO) return UA_ERR_UNSUPPORTED;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    fp.scores = p->d_scores;
+    fp.score_stride = ((int64_t)fp.max_seqlen_k + 127) / 128 * 128;
+    if (d.kv_dtype == UA_DTYPE_FP4_E2M1) {
+        rs = run_fp4(p, &fp, st);
+        if (rs != UA_OK) return rs;
+        p->last_path = "fp4+combine+weights";
+    } else {
+        if (!ua::decode_tc_shape_ok(fp)) return UA_ERR_UNSUPPORTED;
+        rs = encode_maps(p, k_cache, v_cache, true);
+        if (rs != UA_OK) return rs;
+        ua::DecodePlan plan;
+        ua::plan_decode_tc(fp, p->num_sms, p->ws_bytes, &plan);
+        if ((int64_t)plan.splits * plan.row_tiles > 0x7fffffffLL) return UA_ERR_UNSUPPORTED;
+        set_partials(p, &fp, plan.splits, plan.chunk);
+        prof_mark(p, true, st);
+        const cudaError_t e = ua::launch_decode_tc(plan, p->map_kp, p->map_vp, fp, st);
+        prof_mark(p, false, st);
+        if (e != cudaSuccess) {
+            note_cuda(e, "decode kernel launch");
+            return UA_ERR_CUDA;
+        }
+        rs = run_combine(fp, st);
+        if (rs != UA_OK) return rs;
+        p->last_path = "decode_tc+combine+weights";
+    }
+    const cudaError_t e = ua::launch_weights(fp, weights_in, weights_out, weight_stride, decay, st);
+    if (e != cudaSuccess) {
+        note_cuda(e, "weights kernel launch");
+        return UA_ERR_CUDA;
+    }
+    p->last_launches = 3;
+    return UA_OK;
+}
+
+ua_status ua_cache_store(ua_problem* p, const void* k_new, const void* v_new, int64_t new_stride,
+                         void* k_cache, void* v_cache, const int32_t* block_table,
+                         const int32_t* cu_seqlens_q, const int32_t* seqused_k, int32_t num_seqs,
+                         int64_t total_q, int32_t max_seqlen_q, int32_t max_seqlen_k, void* stream) {
+    if (!p) return UA_ERR_INVALID_ARG;
+    p->last_launches = 0;
+    p->last_path = "none";
+    const ua_problem_desc& d = p->desc;
+    if (num_seqs < 0 || num_seqs > d.max_num_seqs || total_q < 0 || total_q > d.max_total_q ||
+        max_seqlen_q < 0 || max_seqlen_k < max_seqlen_q ||
+        (int64_t)max_seqlen_k > (int64_t)d.max_blocks_per_seq * d.block_size ||
+        new_stride < (int64_t)d.num_kv_heads * d.head_size || new_stride % 8 != 0 || !on_device(p))
+        return UA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return UA_OK;
+    if (num_seqs > 65535) return UA_ERR_UNSUPPORTED;
+    if (!k_new || !v_new || !k_cache || !v_cache || !block_table || !cu_seqlens_q || !seqused_k ||
+        !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache))
+        return UA_ERR_INVALID_ARG;
+    ua::StoreParams sp{};
+    sp.c = cache_params(p, k_cache, v_cache, block_table, seqused_k, num_seqs);
+    sp.k_new = static_cast<const __nv_bfloat16*>(k_new);
+    sp.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    sp.cu_seqlens_q = cu_seqlens_q;
+    sp.stride = new_stride;
+    sp.total_q = total_q;
+    sp.max_seqlen_q = max_seqlen_q;
+    sp.max_seqlen_k = max_seqlen_k;
+    const cudaError_t e = ua::launch_store(sp, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+        note_cuda(e, "store kernel launch");
+        return UA_ERR_CUDA;
+    }
+    p->last_launches = 1;
+    p->last_path = "store";
+    return UA_OK;
+}
+
+ua_status ua_cache_expand(ua_problem* p, const void* k_cache, const void* v_cache,
+                          const int32_t* block_table, const int32_t* seqused_k, const int32_t* begin,
+                          int32_t num_seqs, int32_t max_keys, void* k_out, void* v_out,
+                          const int32_t* out_block_table, int32_t out_table_stride,
+                          int64_t out_num_blocks, void* stream) {
+    if (!p) return UA_ERR_INVALID_ARG;
+    p->last_launches = 0;
+    p->last_path = "none";
+    const ua_problem_desc& d = p->desc;
+    if (num_seqs < 0 || num_seqs > d.max_num_seqs || max_keys < 0 || out_table_stride < 1 ||
+        out_num_blocks < 1 || !on_device(p))
+        return UA_ERR_INVALID_ARG;
+    if (num_seqs == 0 || max_keys == 0) return UA_OK;
+    if (num_seqs > 65535 || out_num_blocks > (int64_t(1) << 31) - 1) return UA_ERR_UNSUPPORTED;
+    if (!k_cache || !v_cache || !block_table || !seqused_k || !k_out || !v_out || !out_block_table ||
+        !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out))
+        return UA_ERR_INVALID_ARG;
+    ua::ExpandParams ep{};
+    ep.c = cache_params(p, k_cache, v_cache, block_table, seqused_k, num_seqs);
+    ep.begin = begin;
+    ep.k_out = static_cast<__nv_bfloat16*>(k_out);
+    ep.v_out = static_cast<__nv_bfloat16*>(v_out);
+    ep.out_table = out_block_table;
+    ep.out_blocks = out_num_blocks;
+    ep.out_stride = out_table_stride;
+    ep.max_keys = max_keys;
+    const cudaError_t e = ua::launch_expand(ep, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+        note_cuda(e, "expand kernel launch");
+        return UA_ERR_CUDA;
+    }
+    p->last_launches = 1;
+    p->last_path = "expand";
+    return UA_OK;
+}
+
+ua_status ua_cache_evict(ua_problem* p, void* k_cache, void* v_cache, const int32_t* block_table,
+                         const int32_t* dst_block_table, const int32_t* seqused_k, int32_t num_seqs,
+                         int32_t max_seqlen_k, const float* weights_in, float* weights_out,
+                         int64_t weight_stride, int32_t budget, int32_t recent, int32_t* kept,
+                         int32_t* seqused_out, void* stream) {
+    if (!p) return UA_ERR_INVALID_ARG;
+    p->last_launches = 0;
+    p->last_path = "none";
+    const ua_problem_desc& d = p->desc;
+    if (num_seqs < 0 || num_seqs > d.max_num_seqs || max_seqlen_k < 0 ||
+        (int64_t)max_seqlen_k > (int64_t)d.max_blocks_per_seq * d.block_size || budget < 1 ||
+        recent < 0 || recent > budget || weight_stride < max_seqlen_k || !on_device(p))
+        return UA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return UA_OK;
+    if (num_seqs > 65535 || d.num_kv_heads > 32767) return UA_ERR_UNSUPPORTED;
+    if (!k_cache || !v_cache || !block_table || !seqused_k || !weights_in || !weights_out || !kept ||
+        !seqused_out || !aligned16(k_cache) || !aligned16(v_cache) ||
+        (reinterpret_cast<uintptr_t>(weights_in) & 3u) != 0 ||
+        (reinterpret_cast<uintptr_t>(weights_out) & 3u) != 0)
+        return UA_ERR_INVALID_ARG;
+    ua::EvictParams ep{};
+    ep.c = cache_params(p, k_cache, v_cache, block_table, seqused_k, num_seqs);
+    ep.in_place = !dst_block_table || dst_block_table == block_table;
+    ep.dst_table = ep.in_place ? block_table : dst_block_table;
+    ep.w_in = weights_in;
+    ep.w_out = weights_out;
+    ep.kept = kept;
+    ep.seqused_out = seqused_out;
+    ep.w_stride = weight_stride;
+    ep.max_seqlen_k = max_seqlen_k;
+    ep.budget = budget;
+    ep.recent = recent;
+    const cudaError_t e = ua::launch_evict(ep, p->num_sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+        note_cuda(e, "evict kernel launch");
+        return UA_ERR_CUDA;
+    }
+    p->last_launches = 2;
+    p->last_path = ep.in_place ? "evict_in_place" : "evict";
     return UA_OK;
 }
 

@@ -40,7 +40,7 @@ struct FwdParams {
     int32_t chunk;                 // keys per segment (multiple of 64)
     int32_t row_tiles;             // row tiles per (sequence, kv head)
     int32_t kv_fp8;                // caches hold e4m3 codes
-    float k_scale, v_scale;        // fp8 caches: K = code * k_scale, V = code * v_scale
+    float k_scale, v_scale;        // fp8 / fp4 caches: factors of K and V (1 for bf16)
     int64_t qq_stride;             // row stride of qq_bias
     int32_t part_bf16;             // part_o holds bf16 (same element indexing) instead of fp32
     const int32_t* topk_idx;       // [total_q, topk_stride] key positions per query token, or null
@@ -58,6 +58,10 @@ struct FwdParams {
     // bounded by stall_ns, so the bounded-wait abort path runs.
     int32_t stall;
     int64_t stall_ns;
+    // Key weights: every row's scores in log2 units, masks applied, element
+    // (row, key) at row * score_stride + key; null outside ua_forward_weights.
+    float* scores;
+    int64_t score_stride;
 };
 
 // Per-sequence metadata check.  Returns UA_DEVERR_* bits (0 = well formed) and

@@ -109,7 +109,11 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t& lo, uint32
 // F8: K and V caches hold e4m3 codes (gfx950 page, section 7.3): the MMAs run
 // in f16 (every e4m3 value is exact in f16, and so is a bf16 Q of moderate
 // magnitude), k_scale is folded into tau and v_scale into the output scale.
-template <int D, int NSK, int NSV, int NR, bool PLAIN, bool F8>
+// EMIT (key weights): the grid also covers row tiles of floor(16 / g) positions,
+// every row's scores are stored for the key-weight kernel, partials are written
+// even for one segment, and the row sums add fp32 exponentials (the weights are
+// fp32 results; the f16 exponentials of the P.V operand are 2^-11 off each).
+template <int D, int NSK, int NSV, int NR, bool PLAIN, bool F8, bool EMIT>
 __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreadsD, F8 ? 2 : 1)   // two CTAs per SM
 decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
@@ -122,23 +126,31 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int lane = threadIdx.x & 31;
     const int s = blockIdx.z;
     const int hkv = blockIdx.y;
-    const int seg = blockIdx.x;
-    const bool split = p.splits > 1;
+    const int seg = EMIT ? blockIdx.x % p.splits : blockIdx.x;
+    const bool split = EMIT || p.splits > 1;
     const int g = p.g;
 
     int sq, sk;
     int64_t q0;
     const uint32_t st = seq_status(p, s, sq, sk, q0);
-    if (st && hkv == 0 && seg == 0 && threadIdx.x == 0) atomicOr(p.err, (int)st);
+    if (st && hkv == 0 && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, (int)st);
     if (st & UA_DEVERR_CU_SEQLENS) return;
-    const int nrows = min(g * sq, kN);   // the planner guarantees g * S_q <= 16
+    const int ctx = sk - sq;
+    int i0 = 0;                          // the tile's first position in the chunk
+    if constexpr (EMIT) {
+        const int64_t first = (int64_t)(blockIdx.x / p.splits) * (kN / g);
+        if (first >= sq) return;
+        i0 = (int)first;
+        q0 += i0;
+        sq = min(sq - i0, kN / g);
+    }
+    const int nrows = min(g * sq, kN);   // without EMIT the planner guarantees g * S_q <= 16
     if (nrows <= 0) return;
     if (seg >= (split ? seq_segments(p, st, sk) : 1)) return;
-    const int ctx = sk - sq;
     const bool causal = (p.flags & UA_FLAG_CAUSAL) != 0;
     const bool window = (p.flags & UA_FLAG_WINDOW) != 0;
-    int k_end = causal ? min(sk, sq - 1 + ctx + 1) : sk;
-    int k_beg = window ? max(0, ctx - p.window + 1) : 0;
+    int k_end = causal ? min(sk, i0 + sq - 1 + ctx + 1) : sk;
+    int k_beg = window ? max(0, i0 + ctx - p.window + 1) : 0;
     if (split) {
         k_beg = max(k_beg, seg * p.chunk);
         k_end = min(k_end, seg * p.chunk + p.chunk);
@@ -495,7 +507,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int r = 0; r < NR; ++r) {
             m[r] = -INFINITY;
             l[r] = 0.f;
-            const int i = r / g;
+            const int i = i0 + r / g;
             rhi[r] = r < nrows ? (causal ? min(i + ctx, sk - 1) : sk - 1) : -1;
             rlo[r] = window ? max(0, i + ctx - p.window + 1) : 0;
             rslope[r] = (!PLAIN && alibi && r < nrows) ? __ldg(p.alibi + hkv * g + r % g) : 0.f;
@@ -523,10 +535,18 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         // Query section of row r (position r / g); keys past
                         // the row's last visible key read nothing.
                         if (qq && key >= ctx && key <= rhi[r])
-                            tt += __ldg(p.qq_bias + (int64_t)(r / g) * p.qq_stride + (key - ctx));
+                            tt += __ldg(p.qq_bias + (int64_t)(i0 + r / g) * p.qq_stride + (key - ctx));
                         v = tt * kLog2e;
                     }
                     x[r] = (key >= rlo[r] && key <= rhi[r]) ? v : -INFINITY;
+                }
+                if constexpr (EMIT) {
+                    if (key < sk) {
+#pragma unroll
+                        for (int r = 0; r < NR; ++r)
+                            if (r < nrows)
+                                p.scores[((q0 + r / g) * p.hq + hkv * g + r % g) * p.score_stride + key] = x[r];
+                    }
                 }
             } else {
 #pragma unroll
@@ -575,8 +595,8 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     "cvt.f32.f16 %1, hi;\n\t}"
                     : "=f"(p0), "=f"(p1)
                     : "r"(e));
-                l[r] = l[r] * alpha[r] + p0;
-                l[r + 1] = l[r + 1] * alpha[r + 1] + p1;
+                l[r] = l[r] * alpha[r] + (EMIT ? fast_exp2(a0) : p0);
+                l[r + 1] = l[r + 1] * alpha[r + 1] + (EMIT ? fast_exp2(a1) : p1);
                 pb[r / 2] = F8 ? e : pack_bf16x2(p0, p1);   // the P.V MMA's element type
             }
             // P^T buffer (j & 1) was read by the P.V of tile j - 2; rescaling O
@@ -695,7 +715,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
 bool decode_tc_shape_ok(const FwdParams& p) {
     const bool d_ok = p.kv_fp8 ? p.d == 128 : (p.d == 64 || p.d == 128 || p.d == 256);
-    return d_ok && p.g >= 1 && p.g <= kN && (int64_t)p.g * p.max_seqlen_q <= kN;
+    return d_ok && p.g >= 1 && p.g <= kN && (p.scores || (int64_t)p.g * p.max_seqlen_q <= kN);
 }
 
 void plan_decode_tc(const FwdParams& p, int num_sms, size_t workspace_bytes, DecodePlan* plan) {
@@ -704,20 +724,24 @@ void plan_decode_tc(const FwdParams& p, int num_sms, size_t workspace_bytes, Dec
     // Segments of whole 128-key tiles, at least 8 tiles each, aiming at about
     // four waves of the two CTAs an SM holds (measured on the 64-sequence
     // decode batch: 3-4 segments per (sequence, KV head) beat 2 and 5+).
-    const int64_t base = (int64_t)p.hk * p.num_seqs;
+    if (p.scores) {                      // row tiles of floor(16 / g) positions
+        const int per = kN / p.g;
+        plan->row_tiles = (p.max_seqlen_q + per - 1) / per;
+    }
+    const int64_t base = (int64_t)p.hk * p.num_seqs * plan->row_tiles;
     const int64_t want = (8LL * num_sms + base - 1) / base;
     const int64_t by_len = std::max<int64_t>(1, p.max_seqlen_k / (8 * kBN));
     int splits = (int)std::min<int64_t>(std::min<int64_t>(want, by_len), 64);
     const size_t per_split = (size_t)p.total_q * p.hq * (p.d + 2) * sizeof(float);
     splits = (int)std::min<size_t>((size_t)splits, per_split ? workspace_bytes / per_split : 1);
     if (splits < 1) splits = 1;
-    if (splits > 1) {
+    if (splits > 1 || p.scores) {        // with scores even one segment goes through the combine
         const int per = (p.max_seqlen_k + splits - 1) / splits;
         plan->chunk = (per + kBN - 1) / kBN * kBN;
         splits = (p.max_seqlen_k + plan->chunk - 1) / plan->chunk;
     }
     plan->splits = splits;
-    plan->launches = splits > 1 ? 2 : 1;
+    plan->launches = splits > 1 || p.scores ? 2 : 1;
 }
 
 namespace {
@@ -728,15 +752,18 @@ cudaError_t launch_decode_t(const CUtensorMap& tq, const CUtensorMap& tm_k, cons
     using C = DCfg<D, NSK, NSV, F8>;
     const bool plain = (p.flags & (UA_FLAG_SOFTCAP | UA_FLAG_ALIBI | UA_FLAG_QQ_BIAS)) == 0;
     const int rows = p.g * p.max_seqlen_q;
-    auto kern = rows <= 4 ? (plain ? decode_tc_kernel<D, NSK, NSV, 4, true, F8>
-                                   : decode_tc_kernel<D, NSK, NSV, 4, false, F8>)
-              : rows <= 8 ? (plain ? decode_tc_kernel<D, NSK, NSV, 8, true, F8>
-                                   : decode_tc_kernel<D, NSK, NSV, 8, false, F8>)
-                          : (plain ? decode_tc_kernel<D, NSK, NSV, 16, true, F8>
-                                   : decode_tc_kernel<D, NSK, NSV, 16, false, F8>);
+    auto kern = rows <= 4 ? (plain ? decode_tc_kernel<D, NSK, NSV, 4, true, F8, false>
+                                   : decode_tc_kernel<D, NSK, NSV, 4, false, F8, false>)
+              : rows <= 8 ? (plain ? decode_tc_kernel<D, NSK, NSV, 8, true, F8, false>
+                                   : decode_tc_kernel<D, NSK, NSV, 8, false, F8, false>)
+                          : (plain ? decode_tc_kernel<D, NSK, NSV, 16, true, F8, false>
+                                   : decode_tc_kernel<D, NSK, NSV, 16, false, F8, false>);
+    if (p.scores)
+        kern = rows <= 4 ? decode_tc_kernel<D, NSK, NSV, 4, false, F8, true>
+                         : decode_tc_kernel<D, NSK, NSV, 16, false, F8, true>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    dim3 grid((unsigned)plan.splits, (unsigned)p.hk, (unsigned)p.num_seqs);
+    dim3 grid((unsigned)(plan.splits * plan.row_tiles), (unsigned)p.hk, (unsigned)p.num_seqs);
     kern<<<grid, F8 ? kThreadsF8 : kThreadsD, C::kSmem, stream>>>(tq, tm_k, tm_v, p);
     return cudaGetLastError();
 }
