@@ -54,6 +54,8 @@ struct ua_problem {
     // scores of ua_forward_weights (UA_FLAG_KEY_WEIGHTS problems only)
     float* d_scores = nullptr;
     size_t scores_elems = 0;
+    // pieces of every row of a call on a 4-bit cache (fp4 problems only)
+    int32_t* d_pieces = nullptr;
     // work list of the persistent prefill kernel: entries, then the
     // per-sequence prefix, then [entries, claim counter]
     void* d_work = nullptr;
@@ -170,6 +172,15 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
         const size_t keys = ((size_t)d->max_blocks_per_seq * d->block_size + 127) / 128 * 128;
         p->scores_elems = size_t(d->max_total_q) * d->num_q_heads * keys;
     }
+    size_t piece_bytes = 0;
+    if (d->kv_dtype == UA_DTYPE_FP4_E2M1) {
+        // A row may have as many pieces as warps share its keys: slots under the
+        // cap, two at least, and the rows' statistics.
+        const size_t slot = ua::fp4_workspace_bytes(d->max_total_q * d->num_q_heads, d->head_size);
+        p->ws_bytes = std::max(std::min(slot * 512, kWorkspaceCap), slot * 2) +
+                      size_t(d->max_total_q) * d->num_q_heads * 2 * sizeof(float) + 16;
+        piece_bytes = size_t(d->max_total_q) * d->num_q_heads * sizeof(int32_t);
+    }
     // Work-list entries: every call's (total_q / (2 ppt) + num_seqs) entries
     // without a KV split, and room for the splits the planner makes when the
     // grid is small (about 4 x 152 units per KV head x up to 64 segments).
@@ -180,21 +191,25 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
     if (cudaMalloc(&p->d_err, sizeof(int32_t)) != cudaSuccess ||
         cudaMalloc(&p->d_ws, p->ws_bytes) != cudaSuccess ||
         cudaMalloc(&p->d_work, work_bytes) != cudaSuccess ||
+        (piece_bytes && cudaMalloc(&p->d_pieces, piece_bytes) != cudaSuccess) ||
         (p->scores_elems && cudaMalloc(&p->d_scores, p->scores_elems * sizeof(float)) != cudaSuccess)) {
         cudaGetLastError();
         cudaFree(p->d_err);
         cudaFree(p->d_ws);
         cudaFree(p->d_work);
+        cudaFree(p->d_pieces);
         delete p;
         return UA_ERR_OUT_OF_MEMORY;
     }
     e = cudaMemset(p->d_err, 0, sizeof(int32_t));
+    if (e == cudaSuccess && piece_bytes) e = cudaMemset(p->d_pieces, 0, piece_bytes);
     if (e != cudaSuccess) {
         note_cuda(e, "ua_problem_create");
         cudaFree(p->d_err);
         cudaFree(p->d_ws);
         cudaFree(p->d_work);
         cudaFree(p->d_scores);
+        cudaFree(p->d_pieces);
         delete p;
         return UA_ERR_CUDA;
     }
@@ -208,6 +223,7 @@ void ua_destroy(ua_problem* p) {
     cudaFree(p->d_ws);
     cudaFree(p->d_work);
     cudaFree(p->d_scores);
+    cudaFree(p->d_pieces);
     cudaFree(p->st_q);
     cudaFree(p->st_out);
     cudaFree(p->st_bt);
@@ -382,12 +398,19 @@ ua_status run_combine(const ua::FwdParams& fp, cudaStream_t st) {
     return UA_ERR_CUDA;
 }
 
-// Attention over a 4-bit cache; with fp->scores set partials are always
-// written and combined.
+// Attention over a 4-bit cache.  With fp->scores the rows' final (m, l) go to
+// the front of the workspace, laid out like the partials of one segment.
 ua_status run_fp4(ua_problem* p, ua::FwdParams* fp, cudaStream_t st) {
+    const size_t rows = (size_t)fp->total_q * p->desc.num_q_heads;
+    const size_t stats = fp->scores ? rows * 2 : 0;
     ua::Fp4Plan plan;
-    if (!ua::plan_fp4(*fp, p->num_sms, p->ws_bytes, &plan)) return UA_ERR_UNSUPPORTED;
-    set_partials(p, fp, plan.splits, plan.chunk);
+    if (!ua::plan_fp4(*fp, p->num_sms, p->ws_bytes - stats * sizeof(float) - 16, &plan)) return UA_ERR_UNSUPPORTED;
+    fp->splits = plan.splits;
+    fp->chunk = plan.chunk;
+    fp->part_ml = p->d_ws;
+    fp->part_o = p->d_ws + (stats + 3) / 4 * 4;
+    fp->piece_ml = fp->part_o + rows * plan.splits * p->desc.head_size;
+    fp->row_pieces = p->d_pieces;
     prof_mark(p, true, st);
     cudaError_t e = ua::launch_fp4(plan, *fp, st);
     prof_mark(p, false, st);
@@ -395,10 +418,11 @@ ua_status run_fp4(ua_problem* p, ua::FwdParams* fp, cudaStream_t st) {
         note_cuda(e, "fp4 kernel launch");
         return UA_ERR_CUDA;
     }
-    const bool combine = plan.splits > 1 || fp->scores;
-    p->last_launches = combine ? 2 : 1;
-    p->last_path = combine ? "fp4+combine" : "fp4";
-    return combine ? run_combine(*fp, st) : UA_OK;
+    fp->splits = 1;                      // what part_ml holds, for the key-weight kernel
+    fp->chunk = 1 << 30;
+    p->last_launches = 2;
+    p->last_path = "fp4+merge";
+    return UA_OK;
 }
 
 // The problem's device is the current one (the cache operators launch on it).
@@ -677,7 +701,7 @@ ua_status ua_forward_weights(ua_problem* p, const void* q, const void* k_cache, 
     if (d.kv_dtype == UA_DTYPE_FP4_E2M1) {
         rs = run_fp4(p, &fp, st);
         if (rs != UA_OK) return rs;
-        p->last_path = "fp4+combine+weights";
+        p->last_path = "fp4+merge+weights";
     } else {
         if (!ua::decode_tc_shape_ok(fp)) return UA_ERR_UNSUPPORTED;
         rs = encode_maps(p, k_cache, v_cache, true);

@@ -62,6 +62,10 @@ struct FwdParams {
     // (row, key) at row * score_stride + key; null outside ua_forward_weights.
     float* scores;
     int64_t score_stride;
+    // 4-bit caches: (m, l) of every piece of a row (beside its o in part_o), and
+    // every row's number of pieces (0 between calls).
+    float* piece_ml;               // [total_q * hq, splits, 2]
+    int32_t* row_pieces;           // [total_q * hq]
 };
 
 // Per-sequence metadata check.  Returns UA_DEVERR_* bits (0 = well formed) and

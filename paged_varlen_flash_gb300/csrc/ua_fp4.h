@@ -6,19 +6,22 @@
 namespace ua {
 
 struct Fp4Plan {
-    int rows = 16;      // packed rows per tile (8 or 16)
-    int splits = 1;     // KV segments per (sequence, kv head, row tile)
-    int chunk = 0;      // keys per segment (a multiple of 128)
-    int row_tiles = 1;  // row tiles per (sequence, kv head)
-    int launches = 0;   // kernels enqueued per call (the combine among them)
+    int rows = 16;   // packed rows per tile (8 or 16)
+    int ctas = 1;    // CTAs; each warp has an equal share of the batch's keys
+    int splits = 2;  // partial slots per row: the most pieces a job may be cut into
+    int chunk = 1;   // smallest share, in steps of 32 keys
 };
 
-// False when the call's grid does not fit.
+// Bytes of one partial slot for `rows` output rows; a problem's workspace
+// holds at least two.
+size_t fp4_workspace_bytes(int64_t rows, int d);
+
+// False when the call does not fit.
 bool plan_fp4(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4Plan* plan);
 
-// Enqueue the kernel (p.splits / p.chunk / p.row_tiles / partial pointers set
-// from the plan).  With p.scores set every row's scores are stored as well and
-// partials are written even for one segment.
+// Enqueue the kernel and the merge of cut jobs (p.splits / p.chunk from the plan;
+// p.part_o, p.piece_ml and p.row_pieces the problem's workspace).  With p.scores set every
+// row's scores and its final (m, l), the latter in p.part_ml, are stored as well.
 cudaError_t launch_fp4(const Fp4Plan& plan, const FwdParams& p, cudaStream_t stream);
 
 }  // namespace ua
