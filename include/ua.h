@@ -374,10 +374,11 @@ ua_status ua_forward_noalloc(const ua_problem_desc *desc, const void *q, const v
  *   FP8_E4M3  y rounded to nearest even, magnitudes above 448 (infinities
  *             too) to 448, NaN to 0x7f;
  *   FP4_E2M1  per 16 dims s = max|y| / 6 rounded to e4m3 (nearest even, at
- *             most 448), codes y / s rounded to nearest even, at most 6, the
- *             sign kept; s = 0 stores zero codes; a NaN among the 16 stores
- *             s = 0x7f and zero codes, so that all 16 read back as NaN.  The
- *             rounding is that of the exact quotients.
+ *             most 448), codes y / s rounded to nearest even, at most 6 (a
+ *             negative value that rounds to 0 stores the code of 0); s = 0
+ *             stores zero codes; a NaN among the 16 stores s = 0x7f and zero
+ *             codes, so that all 16 read back as NaN.  The rounding is that of
+ *             the exact quotients.
  * Malformed sequences are skipped; rows whose block id is out of range are
  * dropped (UA_DEVERR_BLOCK_ID).  No slot may be written by two rows of a call.
  */

@@ -111,8 +111,8 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t& lo, uint32
 // magnitude), k_scale is folded into tau and v_scale into the output scale.
 // EMIT (key weights): the grid also covers row tiles of floor(16 / g) positions,
 // every row's scores are stored for the key-weight kernel, partials are written
-// even for one segment, and the row sums add fp32 exponentials (the weights are
-// fp32 results; the f16 exponentials of the P.V operand are 2^-11 off each).
+// even for one segment, and the exponentials are fp32 (the weights are fp32
+// results; f16 exponentials are 2^-11 off each, and their arguments too).
 template <int D, int NSK, int NSV, int NR, bool PLAIN, bool F8, bool EMIT>
 __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreadsD, F8 ? 2 : 1)   // two CTAs per SM
 decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -587,17 +587,26 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int r = 0; r < NR; r += 2) {
                 const float a0 = x[r] - (m[r] == -INFINITY ? 0.f : m[r]);
                 const float a1 = x[r + 1] - (m[r + 1] == -INFINITY ? 0.f : m[r + 1]);
-                uint32_t h, e;
-                asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(a1), "f"(a0));
-                asm("ex2.approx.f16x2 %0, %1;" : "=r"(e) : "r"(h));
                 float p0, p1;
-                asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\t"
-                    "cvt.f32.f16 %1, hi;\n\t}"
-                    : "=f"(p0), "=f"(p1)
-                    : "r"(e));
-                l[r] = l[r] * alpha[r] + (EMIT ? fast_exp2(a0) : p0);
-                l[r + 1] = l[r + 1] * alpha[r + 1] + (EMIT ? fast_exp2(a1) : p1);
-                pb[r / 2] = F8 ? e : pack_bf16x2(p0, p1);   // the P.V MMA's element type
+                if constexpr (EMIT) {
+                    p0 = fast_exp2(a0);
+                    p1 = fast_exp2(a1);
+                    if constexpr (F8)
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pb[r / 2]) : "f"(p1), "f"(p0));
+                    else
+                        pb[r / 2] = pack_bf16x2(p0, p1);
+                } else {
+                    uint32_t h, e;
+                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(a1), "f"(a0));
+                    asm("ex2.approx.f16x2 %0, %1;" : "=r"(e) : "r"(h));
+                    asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\t"
+                        "cvt.f32.f16 %1, hi;\n\t}"
+                        : "=f"(p0), "=f"(p1)
+                        : "r"(e));
+                    pb[r / 2] = F8 ? e : pack_bf16x2(p0, p1);   // the P.V MMA's element type
+                }
+                l[r] = l[r] * alpha[r] + p0;
+                l[r + 1] = l[r + 1] * alpha[r + 1] + p1;
             }
             // P^T buffer (j & 1) was read by the P.V of tile j - 2; rescaling O
             // needs the P.V of tile j - 1.

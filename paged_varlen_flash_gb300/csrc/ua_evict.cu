@@ -2,15 +2,20 @@
 // head) the `budget` kept keys are found (select_kernel) and their cache rows
 // moved to the front of the destination table (move_kernel).
 //
-// Select: one CTA per (sequence, KV head).  A weight's bits, flipped so that
-// unsigned order is float order, are searched for the m-th largest of the n
-// candidates by three radix passes (11 + 11 + 10 bits) over a shared-memory
-// histogram; one pass in key order then writes the kept positions, taking keys
-// above the threshold, the first `need` of those equal to it, and the recent
-// tail.  Reading the weights four times costs L2 reads only (32 KB for 8192
-// keys).  Move: rows in chunks of rank order; a kept key's new position is never
-// behind its old one, so an in-place CTA that has read a whole chunk before it
-// writes any of it overwrites nothing unread.
+// Select: a cluster of 1, 2, 4 or 8 CTAs per (sequence, KV head), each with a
+// run of the keys (up to 8192 of them stay in registers, eight per thread; a
+// longer run, past 65536 keys, is read again in every pass).  A weight's bits, flipped so that unsigned order is float order,
+// are searched for the m-th largest of the n candidates by three radix passes
+// (11 + 11 + 10 bits) over shared-memory histograms that the cluster's CTAs read
+// from one another; one pass in key order then writes the kept positions,
+// taking keys above the threshold, the first `need` of those equal to it, and
+// the recent tail.
+//
+// Move: a CTA takes a run of 256 ranks, a warp 32 neighbouring ones, looks its
+// rows' pages up once (lane = rank) and copies them in 16-byte pieces, eight
+// loads per thread in flight before the first store.  A kept key's new position is never
+// behind its old one, so in place a CTA that walks the ranks in order and has
+// read a whole round before it writes any of it overwrites nothing unread.
 #include <algorithm>
 #include <cstdint>
 
@@ -22,9 +27,12 @@ namespace ua {
 namespace {
 
 constexpr int kSel = 1024;      // threads of select_kernel
+constexpr int kKeep = 8;        // weights a thread keeps in registers
+constexpr int kSelKeys = kKeep * kSel;   // keys a cluster's CTA should have
 constexpr int kBins = 2048;
 constexpr int kMove = 256;      // threads of move_kernel
-constexpr int kBatch = 4;       // 16-byte pieces a move thread holds at a time
+constexpr int kHold = 8;        // 16-byte pieces a move thread holds at a time
+constexpr int kRanks = kMove;   // ranks of a CTA's round: 32 per warp
 
 // Order-preserving bits: NaN first (0), -0 with +0, +inf last.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -42,115 +50,195 @@ __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t v, int lane) {
     return v;
 }
 
+// A 32-bit word of the same shared-memory variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_word(const uint32_t* local, uint32_t rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(local), rank)) : "memory");
+    return v;
+}
+
+template <int CL>
+__device__ __forceinline__ void team_sync() {
+    if constexpr (CL == 1) __syncthreads();
+    else cluster_sync_all();
+}
+
+template <int CL>
 __global__ void __launch_bounds__(kSel) select_kernel(const EvictParams p) {
-    __shared__ uint32_t hist[kBins];
+    __shared__ uint32_t hist[2][kBins];       // a pass's counts; the next pass's are cleared meanwhile
     __shared__ uint32_t wsum[32], wsum2[32];
     __shared__ uint32_t found[2];
-    const int h = blockIdx.x, s = blockIdx.y;
+    __shared__ uint32_t mine[2];              // this CTA's keys above and equal to the threshold
+    const uint32_t rank = CL == 1 ? 0u : cluster_ctarank();
+    const int h = blockIdx.x / CL, s = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const CacheParams& c = p.c;
     const int sk = __ldg(c.seqused_k + s);
     const int64_t head = (int64_t)s * c.hk + h;
     int32_t* kept = p.kept + head * p.budget;
     const bool bad = sk < 0 || sk > p.max_seqlen_k || (int64_t)sk > (int64_t)c.bt_stride * c.b;
-    if (bad && h == 0 && tid == 0) atomicOr(c.err, (int)UA_DEVERR_BOUNDS);
+    if (bad && h == 0 && rank == 0 && tid == 0) atomicOr(c.err, (int)UA_DEVERR_BOUNDS);
     const int count = bad ? 0 : min(sk, p.budget);
-    for (int64_t r = (int64_t)count + tid; r < p.budget; r += kSel) kept[r] = -1;
+    const int64_t step = kSel * CL, first = (int64_t)rank * kSel + tid;
+    for (int64_t r = count + first; r < p.budget; r += step) kept[r] = -1;
     const float* wi = p.w_in + head * p.w_stride;
     float* wo = p.w_out + head * p.w_stride;
     if (bad || sk <= p.budget) {
-        for (int j = tid; j < count; j += kSel) {
-            kept[j] = j;
+        for (int64_t j = first; j < count; j += step) {
+            kept[j] = (int32_t)j;
             if (wo != wi) wo[j] = wi[j];
         }
-        return;
+        return;                               // the whole cluster does
     }
     const int n = sk - p.recent;              // candidates
-    uint32_t m = (uint32_t)(p.budget - p.recent);
-    uint32_t prefix = 0;                      // found high bits of the threshold
-    uint32_t need = 0;                        // keys equal to the threshold to take
-    if (m > 0) {
-        need = m;
-#pragma unroll 1
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const int bits = pass == 2 ? 10 : 11;
-            for (int i = tid; i < kBins; i += kSel) hist[i] = 0;
-            __syncthreads();
-            for (int j = tid; j < n; j += kSel) {
-                const uint32_t k = weight_key(wi[j]);
-                if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
-            }
-            __syncthreads();
-            // Bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t.
-            const uint32_t c0 = hist[kBins - 1 - 2 * tid], c1 = hist[kBins - 2 - 2 * tid];
-            const uint32_t incl = warp_incl_scan(c0 + c1, lane);
-            if (lane == 31) wsum[warp] = incl;
-            __syncthreads();
-            if (warp == 0) wsum2[lane] = warp_incl_scan(wsum[lane], lane);
-            __syncthreads();
-            const uint32_t before = (warp ? wsum2[warp - 1] : 0u) + incl - (c0 + c1);   // keys in higher bins
-            if (before < need && before + c0 + c1 >= need) {
-                const bool first = before + c0 >= need;
-                found[0] = (uint32_t)(kBins - 1 - 2 * tid - (first ? 0 : 1));
-                found[1] = need - before - (first ? 0u : c0);
-            }
-            __syncthreads();
-            prefix = (prefix << bits) | found[0];
-            need = found[1];
-            __syncthreads();
+    const uint32_t m = (uint32_t)(p.budget - p.recent);
+    // This CTA's run of them, a multiple of the threads long.
+    const int run = (n + CL * kSel - 1) / (CL * kSel) * kSel;
+    const int lo = min(n, (int)rank * run), hi = min(n, lo + run);
+    uint32_t thr = 0;                         // found high bits of the threshold
+    uint32_t need = m;                        // keys equal to the threshold to take
+    const bool cached = run <= kSelKeys;
+    float v[kKeep];                           // weights of keys j0 + q * kSel + tid
+    auto load = [&](int j0) {
+#pragma unroll
+        for (int q = 0; q < kKeep; ++q) {
+            const int j = j0 + q * kSel + tid;
+            v[q] = j < hi ? wi[j] : 0.f;
         }
+    };
+    if (cached) load(lo);
+    for (int i = tid; i < kBins; i += kSel) hist[0][i] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int pass = 0; pass < 3 && m > 0; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const int bits = pass == 2 ? 10 : 11;
+        uint32_t* cur = hist[pass & 1];
+        for (int j0 = lo; j0 < hi; j0 += kSelKeys) {
+            if (!cached) load(j0);
+#pragma unroll
+            for (int q = 0; q < kKeep; ++q) {
+                const uint32_t k = weight_key(v[q]);
+                if (j0 + q * kSel + tid < hi && (pass == 0 || (k >> (shift + bits)) == thr))
+                    atomicAdd(&cur[(k >> shift) & ((1u << bits) - 1)], 1u);
+            }
+        }
+        team_sync<CL>();
+        // Bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t, summed
+        // over the cluster.
+        uint32_t c0 = 0, c1 = 0;
+#pragma unroll
+        for (int q = 0; q < CL; ++q) {
+            c0 += CL == 1 ? cur[kBins - 1 - 2 * tid] : cluster_word(cur + kBins - 1 - 2 * tid, q);
+            c1 += CL == 1 ? cur[kBins - 2 - 2 * tid] : cluster_word(cur + kBins - 2 - 2 * tid, q);
+        }
+        for (int i = tid; i < kBins; i += kSel) hist[(pass + 1) & 1][i] = 0;
+        const uint32_t incl = warp_incl_scan(c0 + c1, lane);
+        if (lane == 31) wsum[warp] = incl;
+        __syncthreads();
+        if (warp == 0) wsum2[lane] = warp_incl_scan(wsum[lane], lane);
+        __syncthreads();
+        const uint32_t before = (warp ? wsum2[warp - 1] : 0u) + incl - (c0 + c1);   // keys in higher bins
+        if (before < need && before + c0 + c1 >= need) {
+            const bool top = before + c0 >= need;
+            found[0] = (uint32_t)(kBins - 1 - 2 * tid - (top ? 0 : 1));
+            found[1] = need - before - (top ? 0u : c0);
+        }
+        // Nobody clears or counts into a histogram that another CTA still reads:
+        // `cur` is cleared two passes on, after the next pass's cluster barrier.
+        __syncthreads();
+        thr = (thr << bits) | found[0];
+        need = found[1];
     }
     // Kept positions in key order: rank = (keys above) + min(equal ones, need).
-    const uint32_t thr = prefix;
-    uint32_t above0 = 0, equal0 = 0;          // before this chunk
-    for (int j0 = 0; m > 0 && j0 < n; j0 += kSel) {
-        const int j = j0 + tid;
-        float w = 0.f;
-        bool above = false, equal = false;
-        if (j < n) {
-            w = wi[j];
-            const uint32_t k = weight_key(w);
-            above = k > thr;
-            equal = k == thr;
-        }
-        const unsigned ba = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
-        if (lane == 0) {
-            wsum[warp] = __popc(ba);
-            wsum2[warp] = __popc(be);
-        }
-        __syncthreads();
-        uint32_t na = 0, ne = 0, ta = 0, te = 0;
-        for (int k = 0; k < 32; ++k) {
-            if (k == warp) {
-                na = ta;
-                ne = te;
+    uint32_t above0 = 0, equal0 = 0;          // before this CTA's run, then before the chunk
+    if (CL > 1 && m > 0) {
+        uint32_t na = 0, ne = 0;
+        for (int j0 = lo; j0 < hi; j0 += kSelKeys) {
+            if (!cached) load(j0);
+#pragma unroll
+            for (int q = 0; q < kKeep; ++q) {
+                const uint32_t k = weight_key(v[q]);
+                const bool in = j0 + q * kSel + tid < hi;
+                na += in && k > thr;
+                ne += in && k == thr;
             }
-            ta += wsum[k];
-            te += wsum2[k];
         }
-        const unsigned lt = (1u << lane) - 1;
-        const uint32_t ra = above0 + na + __popc(ba & lt), re = equal0 + ne + __popc(be & lt);
-        if (above || (equal && re < need)) {
-            const uint32_t rank = ra + min(re, need);
-            kept[rank] = j;
-            wo[rank] = w;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            na += __shfl_xor_sync(0xffffffffu, na, o);
+            ne += __shfl_xor_sync(0xffffffffu, ne, o);
         }
-        above0 += ta;
-        equal0 += te;
+        if (tid < 2) mine[tid] = 0;
         __syncthreads();
+        if (lane == 0) {
+            atomicAdd(&mine[0], na);
+            atomicAdd(&mine[1], ne);
+        }
     }
-    // The recent tail; in place a chunk is read before it is written.
-    for (int j0 = n; j0 < sk; j0 += kSel) {
-        const int j = j0 + tid;
-        const float w = j < sk ? wi[j] : 0.f;
-        __syncthreads();
-        if (j < sk) {
-            kept[m + (uint32_t)(j - n)] = j;
-            wo[m + (uint32_t)(j - n)] = w;
+    // From here on weights_out may overwrite weights_in; cached weights are in
+    // every thread's hands by now.
+    team_sync<CL>();
+    if constexpr (CL > 1) {
+        for (uint32_t q = 0; m > 0 && q < rank; ++q) {
+            above0 += cluster_word(&mine[0], q);
+            equal0 += cluster_word(&mine[1], q);
         }
-        __syncthreads();
     }
+    // A CTA writes at or below its own keys, possibly in an earlier CTA's run:
+    // where weights are moved in place and read again, the CTAs take turns.
+    const bool turns = CL > 1 && wo == wi && !cached;
+    for (int turn = 0; turn < (turns ? CL : 1); ++turn) {
+        if (!turns || turn == (int)rank) {
+            for (int j0 = lo; m > 0 && j0 < hi; j0 += kSelKeys) {
+                if (!cached) load(j0);
+#pragma unroll
+                for (int q = 0; q < kKeep; ++q) {
+                    if (j0 + q * kSel >= hi) break;
+                    const int j = j0 + q * kSel + tid;
+                    const uint32_t k = weight_key(v[q]);
+                    const bool above = j < hi && k > thr, equal = j < hi && k == thr;
+                    const unsigned ba = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
+                    if (lane == 0) wsum[warp] = (uint32_t)__popc(ba) << 16 | __popc(be);
+                    __syncthreads();
+                    // Every warp scans the 32 packed counts (at most 1024 each).
+                    const uint32_t incl = warp_incl_scan(wsum[lane], lane);
+                    const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
+                    const uint32_t before = __shfl_sync(0xffffffffu, incl, warp) - wsum[warp];
+                    const unsigned lt = (1u << lane) - 1;
+                    const uint32_t ra = above0 + (before >> 16) + __popc(ba & lt);
+                    const uint32_t re = equal0 + (before & 0xffffu) + __popc(be & lt);
+                    if (above || (equal && re < need)) {
+                        const uint32_t to = ra + min(re, need);
+                        kept[to] = j;
+                        wo[to] = v[q];
+                    }
+                    above0 += all >> 16;
+                    equal0 += all & 0xffffu;
+                    __syncthreads();
+                }
+            }
+            if (rank == CL - 1) {
+                // The recent tail; in place a chunk is read before it is written.
+                for (int j0 = n; j0 < sk; j0 += kSel) {
+                    const int j = j0 + tid;
+                    const float w = j < sk ? wi[j] : 0.f;
+                    __syncthreads();
+                    if (j < sk) {
+                        kept[m + (uint32_t)(j - n)] = j;
+                        wo[m + (uint32_t)(j - n)] = w;
+                    }
+                    __syncthreads();
+                }
+            }
+        }
+        if (turns) {
+            __threadfence();
+            cluster_sync_all();
+        }
+    }
+    // No CTA ends while another may still read its shared memory.
+    if (CL > 1 && !turns) cluster_sync_all();
 }
 
 // Pieces of a row, 16 bytes each; a 4-bit row ends with a piece of d / 16
@@ -165,86 +253,117 @@ __device__ __forceinline__ uint8_t* piece_at(const CacheParams& c, uint8_t* cach
     return cache + ((block * c.b + slot) * c.hk + h) * rb + x * 16;
 }
 
-// grid: x = rank chunks (out of place; 1 in place) x piece slices, y = K / V of
-// each KV head, z = sequence.
-__global__ void __launch_bounds__(kMove) move_kernel(const EvictParams p, int pieces, int slice, int chunk) {
+// grid: x = rank runs (1 in place) x piece slices x (K, V), y = KV head, z =
+// sequence.  A warp has 32 neighbouring ranks of its CTA's 256; slices of `slice`
+// pieces of a row go to different CTAs.
+__global__ void __launch_bounds__(kMove, 3) move_kernel(const EvictParams p, int pieces, int slice) {
     const CacheParams& c = p.c;
     const int slices = (pieces + slice - 1) / slice;
-    const int sl = blockIdx.x % slices, ch = blockIdx.x / slices;
-    const int h = blockIdx.y >> 1;
-    const bool v = blockIdx.y & 1;
-    const int s = blockIdx.z;
+    const bool v = blockIdx.x & 1;
+    const int sl = (blockIdx.x >> 1) % slices, run = (blockIdx.x >> 1) / slices;
+    const int h = blockIdx.y, s = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t* kept = p.kept + ((int64_t)s * c.hk + h) * p.budget;
-    const int32_t* st = c.block_table + (int64_t)s * c.bt_stride;
-    const int32_t* dt = p.dst_table + (int64_t)s * c.bt_stride;
+    const int32_t* src_table = c.block_table + (int64_t)s * c.bt_stride;
+    const int32_t* dst_table = p.dst_table + (int64_t)s * c.bt_stride;
     uint8_t* cache = v ? c.v_cache : c.k_cache;
     const int x0 = sl * slice, nx = min(slice, pieces - x0);
-    const int rows = kMove / slice * kBatch;                 // ranks per round
-    const int lane_row = threadIdx.x / slice, lane_x = threadIdx.x % slice;
-    const int small = c.kv_dtype == UA_DTYPE_FP4_E2M1 && x0 + lane_x == pieces - 1 ? c.d / 16 : 16;
-    const int r_end = (int)min((int64_t)p.budget, ((int64_t)ch + 1) * chunk);
-    if (h == 0 && !v && sl == 0) {
-        // New length: one past the last kept rank (every sequence has one such
-        // rank, or none and length 0).
-        for (int r = ch * chunk + threadIdx.x; r < r_end; r += kMove)
-            if (kept[r] >= 0 && (r + 1 == p.budget || kept[r + 1] < 0)) p.seqused_out[s] = r + 1;
-        if (ch == 0 && threadIdx.x == 0 && kept[0] < 0) p.seqused_out[s] = 0;
-    }
-    for (int r0 = ch * chunk; r0 < r_end; r0 += rows) {
-        if (kept[r0] < 0) return;
-        uint4 hold[kBatch];
-        uint8_t* to[kBatch];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int r = r0 + lane_row + k * (kMove / slice);
-            to[k] = nullptr;
-            if (lane_row >= kMove / slice || lane_x >= nx || r >= r_end) continue;
-            const int j = kept[r];
-            if (j < 0 || (p.in_place && j == r)) continue;
-            const int32_t sb = __ldg(st + j / c.b), db = __ldg(dt + r / c.b);
-            if (sb < 0 || (int64_t)sb >= c.num_blocks || db < 0 || (int64_t)db >= c.num_blocks) {
-                atomicOr(c.err, (int)UA_DEVERR_BLOCK_ID);
-                continue;
+    const uint32_t nx_inv = 0xffffffffu / (uint32_t)nx + 1u;   // e / nx = umulhi(e, nx_inv) for e < 2^16, nx > 1
+    const int b_log2 = 31 - __clz(c.b);
+    const bool fp4 = c.kv_dtype == UA_DTYPE_FP4_E2M1;
+    for (int64_t r0 = (int64_t)run * kRanks; r0 < p.budget; r0 += kRanks) {
+        if (__ldg(kept + r0) < 0) break;
+        // Lane = rank: the row's old and new place; j < 0: nothing to move.
+        const int64_t r = r0 + warp * 32 + lane;
+        int32_t j = r < p.budget ? __ldg(kept + r) : -1, sb = -1, db = -1;
+        if (j >= 0) {
+            if (h == 0 && !v && sl == 0 && (r + 1 == p.budget || __ldg(kept + r + 1) < 0)) p.seqused_out[s] = (int)r + 1;
+            if (p.in_place && j == r) {
+                j = -1;                       // already there
+            } else {
+                sb = __ldg(src_table + (j >> b_log2));
+                db = __ldg(dst_table + (r >> b_log2));
+                if (sb < 0 || (int64_t)sb >= c.num_blocks || db < 0 || (int64_t)db >= c.num_blocks) {
+                    atomicOr(c.err, (int)UA_DEVERR_BLOCK_ID);
+                    j = -1;
+                }
             }
-            const uint8_t* src = piece_at(c, cache, sb, j % c.b, h, x0 + lane_x);
-            to[k] = piece_at(c, cache, db, r % c.b, h, x0 + lane_x);
-            if (small == 16) hold[k] = *reinterpret_cast<const uint4*>(src);
-            else if (small == 8) *reinterpret_cast<uint2*>(&hold[k]) = *reinterpret_cast<const uint2*>(src);
-            else hold[k].x = *reinterpret_cast<const uint32_t*>(src);
         }
-        if (p.in_place) __syncthreads();
+        // The warp's pieces, row by row, kHold per lane at a time (one turn in
+        // place: the launcher's slices see to that).
+        for (int i0 = 0; i0 < 32 * nx; i0 += 32 * kHold) {
+            uint4 hold[kHold];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            if (!to[k]) continue;
-            if (small == 16) *reinterpret_cast<uint4*>(to[k]) = hold[k];
-            else if (small == 8) *reinterpret_cast<uint2*>(to[k]) = make_uint2(hold[k].x, hold[k].y);
-            else *reinterpret_cast<uint32_t*>(to[k]) = hold[k].x;
+            for (int k = 0; k < kHold; ++k) {
+                const int e = i0 + k * 32 + lane;
+                const int row = nx == 1 ? e : (int)__umulhi((uint32_t)e, nx_inv), x = x0 + e - row * nx;
+                const int jj = __shfl_sync(0xffffffffu, j, row & 31), bb = __shfl_sync(0xffffffffu, sb, row & 31);
+                if (row >= 32 || jj < 0) continue;
+                const uint8_t* src = piece_at(c, cache, bb, jj & (c.b - 1), h, x);
+                if (!fp4 || x < pieces - 1 || c.d == 256) hold[k] = *reinterpret_cast<const uint4*>(src);
+                else if (c.d == 128) *reinterpret_cast<uint2*>(&hold[k]) = *reinterpret_cast<const uint2*>(src);
+                else hold[k].x = *reinterpret_cast<const uint32_t*>(src);
+            }
+            if (p.in_place) __syncthreads();
+#pragma unroll
+            for (int k = 0; k < kHold; ++k) {
+                const int e = i0 + k * 32 + lane;
+                const int row = nx == 1 ? e : (int)__umulhi((uint32_t)e, nx_inv), x = x0 + e - row * nx;
+                const int jj = __shfl_sync(0xffffffffu, j, row & 31), dd = __shfl_sync(0xffffffffu, db, row & 31);
+                if (row >= 32 || jj < 0) continue;
+                uint8_t* to = piece_at(c, cache, dd, (int)(r0 + warp * 32 + row) & (c.b - 1), h, x);
+                if (!fp4 || x < pieces - 1 || c.d == 256) *reinterpret_cast<uint4*>(to) = hold[k];
+                else if (c.d == 128) *reinterpret_cast<uint2*>(to) = make_uint2(hold[k].x, hold[k].y);
+                else *reinterpret_cast<uint32_t*>(to) = hold[k].x;
+            }
         }
+        if (!p.in_place) break;               // one round per run
     }
+    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0 && __ldg(kept) < 0) p.seqused_out[s] = 0;
+}
+
+template <int CL>
+cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = CL;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(p.c.hk * CL), (unsigned)p.c.num_seqs);
+    cfg.blockDim = dim3(kSel);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = CL > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, select_kernel<CL>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream) {
     const CacheParams& c = p.c;
-    select_kernel<<<dim3((unsigned)c.hk, (unsigned)c.num_seqs), kSel, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const int ctas = (p.max_seqlen_k + kSelKeys - 1) / kSelKeys;
+    cudaError_t e = ctas <= 1   ? launch_select<1>(p, stream)
+                    : ctas <= 2 ? launch_select<2>(p, stream)
+                    : ctas <= 4 ? launch_select<4>(p, stream)
+                                : launch_select<8>(p, stream);
     if (e != cudaSuccess) return e;
     const int pieces = c.kv_dtype == UA_DTYPE_FP4_E2M1 ? c.d / 32 + 1
                      : c.kv_dtype == UA_DTYPE_BF16     ? c.d / 8
                                                        : c.d / 16;
-    // In place one CTA walks all ranks of its slice; slices down to two pieces
-    // keep the SMs busy when there are few (sequence, KV head) pairs.
+    // In place one CTA walks all ranks of its slice: a slice's pieces fit one
+    // turn of loads, and slices go down to two pieces where there are few
+    // (sequence, KV head) pairs.
     int slice = pieces;
     const int64_t base = (int64_t)c.hk * 2 * c.num_seqs;
-    if (p.in_place)
+    if (p.in_place) {
+        slice = std::min(slice, kHold);
         while (slice > 2 && base * ((pieces + slice - 1) / slice) < 2LL * num_sms) slice = (slice + 1) / 2;
+    }
     const int slices = (pieces + slice - 1) / slice;
-    const int n = std::max(1, std::min(p.budget, p.max_seqlen_k));
-    const int chunk = p.in_place ? p.budget : kMove / slice * kBatch;
-    const int64_t chunks = p.in_place ? 1 : (n + (int64_t)chunk - 1) / chunk;
-    move_kernel<<<dim3((unsigned)(chunks * slices), (unsigned)(c.hk * 2), (unsigned)c.num_seqs), kMove, 0, stream>>>(
-        p, pieces, slice, chunk);
+    const int64_t n = std::max(1, std::min(p.budget, p.max_seqlen_k));
+    const int64_t runs = p.in_place ? 1 : (n + kRanks - 1) / kRanks;
+    dim3 grid((unsigned)(runs * slices * 2), (unsigned)c.hk, (unsigned)c.num_seqs);
+    move_kernel<<<grid, kMove, 0, stream>>>(p, pieces, slice);
     return cudaGetLastError();
 }
 

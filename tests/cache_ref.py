@@ -48,7 +48,7 @@ def quantise_fp4(x, tensor_scale):
         s = np.where(nan, 0.0, E4M3[np.where(nan, 0, s8)])[..., None]
         ratio = np.where(s > 0, np.abs(y) / np.where(s > 0, s, 1.0), 0.0)
         code = nearest(np.minimum(np.where(np.isnan(ratio), 0.0, ratio), 6.0), E2M1)
-    code = np.where(s > 0, code + 8 * np.signbit(y), 0)
+    code = np.where((s > 0) & (code > 0), code + 8 * np.signbit(y), 0)
     return code.reshape(x.shape).astype(np.uint8), s8.astype(np.uint8)
 
 

@@ -33,7 +33,7 @@ def test_fp4_rounds_midpoints_to_even_codes():
     x = np.array([[6.0, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, -0.25, -5.0, 0.2, 0.3, 0, -0.0, 4.9, 5.1]])
     codes, s8 = R.quantise_fp4(x, 1.0)
     assert s8.tolist() == [[0x38]]
-    assert codes[0].tolist() == [7, 0, 2, 2, 4, 4, 6, 6, 8, 14, 0, 1, 0, 8, 6, 7]
+    assert codes[0].tolist() == [7, 0, 2, 2, 4, 4, 6, 6, 0, 14, 0, 1, 0, 0, 6, 7]
 
 
 def test_fp4_special_groups():
