@@ -55,7 +55,7 @@ struct ua_problem {
     float* d_scores = nullptr;
     size_t scores_elems = 0;
     // pieces of every row of a call on a 4-bit cache (fp4 problems only)
-    int32_t* d_pieces = nullptr;
+    int4* d_pieces = nullptr;
     // work list of the persistent prefill kernel: entries, then the
     // per-sequence prefix, then [entries, claim counter]
     void* d_work = nullptr;
@@ -179,7 +179,7 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
         const size_t slot = ua::fp4_workspace_bytes(d->max_total_q * d->num_q_heads, d->head_size);
         p->ws_bytes = std::max(std::min(slot * 512, kWorkspaceCap), slot * 2) +
                       size_t(d->max_total_q) * d->num_q_heads * 2 * sizeof(float) + 16;
-        piece_bytes = size_t(d->max_total_q) * d->num_q_heads * sizeof(int32_t);
+        piece_bytes = size_t(d->max_total_q) * d->num_q_heads * sizeof(int4);
     }
     // Work-list entries: every call's (total_q / (2 ppt) + num_seqs) entries
     // without a KV split, and room for the splits the planner makes when the

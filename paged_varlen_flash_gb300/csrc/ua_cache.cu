@@ -74,7 +74,7 @@ struct Fp4Group {
 // Any tensor scale: a magnitude's code is the number of midpoints below it; the
 // midpoints times s are exact in fp32, and one that is met rounds to the even
 // code.
-__device__ __noinline__ Fp4Group quantise_any(const Group& x, float scale) {
+__device__ __forceinline__ Fp4Group quantise_any(const Group& x, float scale) {
     float y[16];
     float amax = 0.f;
     bool nan = false;
@@ -159,7 +159,8 @@ __device__ __forceinline__ Place place_of(int e, int group_log2, int rows, uint3
     return {e & ((1 << group_log2) - 1), rest - x * rows, x >> 1, (x & 1) != 0};
 }
 
-template <int KV>
+// POW2: both tensor scales are powers of two (k_inv, v_inv their inverses).
+template <int KV, bool POW2>
 __global__ void __launch_bounds__(kThreads) store_kernel(const StoreParams p, int tokens, float k_inv, float v_inv) {
     const CacheParams& c = p.c;
     const int s = blockIdx.y;
@@ -221,8 +222,9 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const StoreParams p, in
                 *reinterpret_cast<uint4*>(cache + row_at(c, id[k], slot, at.h) + at.grp * 16) =
                     make_uint4(w[0], w[1], w[2], w[3]);
             } else {
-                const float inv = at.v ? v_inv : k_inv;        // 0: not a power of two
-                const Fp4Group r = inv != 0.f ? quantise_pow2(x[k], inv) : quantise_any(x[k], scale);
+                Fp4Group r;
+                if constexpr (POW2) r = quantise_pow2(x[k], at.v ? v_inv : k_inv);
+                else r = quantise_any(x[k], scale);
                 uint8_t* page = cache + ((int64_t)id[k] * c.hk + at.h) * fp4_page_bytes(c.b, c.d);
                 *reinterpret_cast<uint2*>(page + slot * (c.d / 2) + at.grp * 8) = make_uint2(r.codes[0], r.codes[1]);
                 page[c.b * (c.d / 2) + slot * groups + at.grp] = (uint8_t)r.s8;
@@ -334,10 +336,12 @@ int rows_per_cta(const CacheParams& c) {
 cudaError_t launch_store(const StoreParams& p, cudaStream_t stream) {
     const int tokens = rows_per_cta(p.c);
     dim3 grid((unsigned)((p.max_seqlen_q + (int64_t)tokens - 1) / tokens), (unsigned)p.c.num_seqs);
-    auto kern = p.c.kv_dtype == UA_DTYPE_BF16       ? store_kernel<UA_DTYPE_BF16>
-                : p.c.kv_dtype == UA_DTYPE_FP8_E4M3 ? store_kernel<UA_DTYPE_FP8_E4M3>
-                                                    : store_kernel<UA_DTYPE_FP4_E2M1>;
-    kern<<<grid, kThreads, 0, stream>>>(p, tokens, exact_inverse(p.c.k_scale), exact_inverse(p.c.v_scale));
+    const float k_inv = exact_inverse(p.c.k_scale), v_inv = exact_inverse(p.c.v_scale);
+    auto kern = p.c.kv_dtype == UA_DTYPE_BF16       ? store_kernel<UA_DTYPE_BF16, false>
+                : p.c.kv_dtype == UA_DTYPE_FP8_E4M3 ? store_kernel<UA_DTYPE_FP8_E4M3, false>
+                : k_inv != 0.f && v_inv != 0.f      ? store_kernel<UA_DTYPE_FP4_E2M1, true>
+                                                    : store_kernel<UA_DTYPE_FP4_E2M1, false>;
+    kern<<<grid, kThreads, 0, stream>>>(p, tokens, k_inv, v_inv);
     return cudaGetLastError();
 }
 

@@ -63,9 +63,9 @@ struct FwdParams {
     float* scores;
     int64_t score_stride;
     // 4-bit caches: (m, l) of every piece of a row (beside its o in part_o), and
-    // every row's number of pieces (0 between calls).
+    // every row's number of pieces, once per 64 dims (0 between calls).
     float* piece_ml;               // [total_q * hq, splits, 2]
-    int32_t* row_pieces;           // [total_q * hq]
+    int4* row_pieces;              // [total_q * hq]
 };
 
 // Per-sequence metadata check.  Returns UA_DEVERR_* bits (0 = well formed) and

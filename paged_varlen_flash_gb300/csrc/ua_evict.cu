@@ -3,7 +3,7 @@
 // moved to the front of the destination table (move_kernel).
 //
 // Select: a cluster of 1, 2, 4 or 8 CTAs per (sequence, KV head), each with a
-// run of the keys (up to 8192 of them stay in registers, eight per thread; a
+// run of the keys (up to 8192 of them stay in registers; a
 // longer run, past 65536 keys, is read again in every pass).  A weight's bits, flipped so that unsigned order is float order,
 // are searched for the m-th largest of the n candidates by three radix passes
 // (11 + 11 + 10 bits) over shared-memory histograms that the cluster's CTAs read
@@ -26,9 +26,7 @@
 namespace ua {
 namespace {
 
-constexpr int kSel = 1024;      // threads of select_kernel
-constexpr int kKeep = 8;        // weights a thread keeps in registers
-constexpr int kSelKeys = kKeep * kSel;   // keys a cluster's CTA should have
+constexpr int kSelKeys = 8192;  // keys a cluster's CTA should have, kept in registers
 constexpr int kBins = 2048;
 constexpr int kMove = 256;      // threads of move_kernel
 constexpr int kHold = 8;        // 16-byte pieces a move thread holds at a time
@@ -63,10 +61,18 @@ __device__ __forceinline__ void team_sync() {
     else cluster_sync_all();
 }
 
+// Threads: 512 where a CTA works alone (three to four of them share an SM),
+// 1024 in a cluster (few CTAs, each should be quick).
 template <int CL>
-__global__ void __launch_bounds__(kSel) select_kernel(const EvictParams p) {
+constexpr int kSelThreads = CL == 1 ? 512 : 1024;
+
+template <int CL>
+__global__ void __launch_bounds__(kSelThreads<CL>) select_kernel(const EvictParams p) {
+    constexpr int kSel = kSelThreads<CL>;
+    constexpr int kKeep = kSelKeys / kSel;    // weights a thread keeps in registers
+    constexpr int kPerBin = kBins / kSel;
     __shared__ uint32_t hist[2][kBins];       // a pass's counts; the next pass's are cleared meanwhile
-    __shared__ uint32_t wsum[32], wsum2[32];
+    __shared__ uint32_t wsum[kSel / 32], counts[kKeep * (kSel / 32) + 1];
     __shared__ uint32_t found[2];
     __shared__ uint32_t mine[2];              // this CTA's keys above and equal to the threshold
     const uint32_t rank = CL == 1 ? 0u : cluster_ctarank();
@@ -124,25 +130,36 @@ __global__ void __launch_bounds__(kSel) select_kernel(const EvictParams p) {
             }
         }
         team_sync<CL>();
-        // Bins from the top: thread t holds bins 2047 - 2t and 2046 - 2t, summed
-        // over the cluster.
-        uint32_t c0 = 0, c1 = 0;
+        // Bins from the top, summed over the cluster: thread t holds kPerBin of
+        // them from bin 2047 - kPerBin * t down.
+        uint32_t cnt[kPerBin] = {}, sum = 0;
 #pragma unroll
-        for (int q = 0; q < CL; ++q) {
-            c0 += CL == 1 ? cur[kBins - 1 - 2 * tid] : cluster_word(cur + kBins - 1 - 2 * tid, q);
-            c1 += CL == 1 ? cur[kBins - 2 - 2 * tid] : cluster_word(cur + kBins - 2 - 2 * tid, q);
-        }
+        for (int q = 0; q < CL; ++q)
+#pragma unroll
+            for (int e = 0; e < kPerBin; ++e) {
+                const uint32_t* bin = cur + kBins - 1 - kPerBin * tid - e;
+                if constexpr (CL == 1) cnt[e] += *bin;
+                else cnt[e] += cluster_word(bin, q);
+            }
+#pragma unroll
+        for (int e = 0; e < kPerBin; ++e) sum += cnt[e];
         for (int i = tid; i < kBins; i += kSel) hist[(pass + 1) & 1][i] = 0;
-        const uint32_t incl = warp_incl_scan(c0 + c1, lane);
+        const uint32_t incl = warp_incl_scan(sum, lane);
         if (lane == 31) wsum[warp] = incl;
         __syncthreads();
-        if (warp == 0) wsum2[lane] = warp_incl_scan(wsum[lane], lane);
-        __syncthreads();
-        const uint32_t before = (warp ? wsum2[warp - 1] : 0u) + incl - (c0 + c1);   // keys in higher bins
-        if (before < need && before + c0 + c1 >= need) {
-            const bool top = before + c0 >= need;
-            found[0] = (uint32_t)(kBins - 1 - 2 * tid - (top ? 0 : 1));
-            found[1] = need - before - (top ? 0u : c0);
+        // Keys in higher bins; every warp scans the warps' sums.
+        const uint32_t warps = warp_incl_scan(lane < kSel / 32 ? wsum[lane] : 0u, lane);
+        uint32_t before = __shfl_sync(0xffffffffu, warps, warp) - wsum[warp] + incl - sum;
+        if (before < need && before + sum >= need) {
+#pragma unroll
+            for (int e = 0; e < kPerBin; ++e) {
+                if (before < need && before + cnt[e] >= need) {
+                    found[0] = (uint32_t)(kBins - 1 - kPerBin * tid - e);
+                    found[1] = need - before;
+                    break;
+                }
+                before += cnt[e];
+            }
         }
         // Nobody clears or counts into a histogram that another CTA still reads:
         // `cur` is cleared two passes on, after the next pass's cluster barrier.
@@ -192,19 +209,38 @@ __global__ void __launch_bounds__(kSel) select_kernel(const EvictParams p) {
         if (!turns || turn == (int)rank) {
             for (int j0 = lo; m > 0 && j0 < hi; j0 += kSelKeys) {
                 if (!cached) load(j0);
+                // Counts of every (row of kSel keys, warp), scanned by warp 0 in
+                // key order; equal and above packed in one word (8192 at most).
 #pragma unroll
                 for (int q = 0; q < kKeep; ++q) {
-                    if (j0 + q * kSel >= hi) break;
+                    const uint32_t k = weight_key(v[q]);
+                    const bool in = j0 + q * kSel + tid < hi;
+                    const unsigned ba = __ballot_sync(0xffffffffu, in && k > thr);
+                    const unsigned be = __ballot_sync(0xffffffffu, in && k == thr);
+                    if (lane == 0) counts[q * (kSel / 32) + warp] = (uint32_t)__popc(ba) << 16 | __popc(be);
+                }
+                __syncthreads();
+                if (warp == 0) {
+                    constexpr int kEach = kKeep * (kSel / 32) / 32;
+                    uint32_t c0[kEach], sum = 0;
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) {
+                        c0[e] = sum;
+                        sum += counts[lane * kEach + e];
+                    }
+                    const uint32_t incl = warp_incl_scan(sum, lane);
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) counts[lane * kEach + e] = incl - sum + c0[e];
+                    if (lane == 31) counts[kKeep * (kSel / 32)] = incl;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int q = 0; q < kKeep; ++q) {
                     const int j = j0 + q * kSel + tid;
                     const uint32_t k = weight_key(v[q]);
                     const bool above = j < hi && k > thr, equal = j < hi && k == thr;
                     const unsigned ba = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
-                    if (lane == 0) wsum[warp] = (uint32_t)__popc(ba) << 16 | __popc(be);
-                    __syncthreads();
-                    // Every warp scans the 32 packed counts (at most 1024 each).
-                    const uint32_t incl = warp_incl_scan(wsum[lane], lane);
-                    const uint32_t all = __shfl_sync(0xffffffffu, incl, 31);
-                    const uint32_t before = __shfl_sync(0xffffffffu, incl, warp) - wsum[warp];
+                    const uint32_t before = counts[q * (kSel / 32) + warp];
                     const unsigned lt = (1u << lane) - 1;
                     const uint32_t ra = above0 + (before >> 16) + __popc(ba & lt);
                     const uint32_t re = equal0 + (before & 0xffffu) + __popc(be & lt);
@@ -213,10 +249,11 @@ __global__ void __launch_bounds__(kSel) select_kernel(const EvictParams p) {
                         kept[to] = j;
                         wo[to] = v[q];
                     }
-                    above0 += all >> 16;
-                    equal0 += all & 0xffffu;
-                    __syncthreads();
                 }
+                const uint32_t all = counts[kKeep * (kSel / 32)];
+                above0 += all >> 16;
+                equal0 += all & 0xffffu;
+                __syncthreads();
             }
             if (rank == CL - 1) {
                 // The recent tail; in place a chunk is read before it is written.
@@ -330,7 +367,7 @@ cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.c.hk * CL), (unsigned)p.c.num_seqs);
-    cfg.blockDim = dim3(kSel);
+    cfg.blockDim = dim3(kSelThreads<CL>);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = CL > 1 ? 1 : 0;

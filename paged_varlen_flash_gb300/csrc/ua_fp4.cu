@@ -53,7 +53,7 @@ constexpr int kStep = 32;       // keys per ring stage
 constexpr int kDepth = 2;       // ring stages per warp
 constexpr int kSub = 4;         // sequences per thread and round of the work split
 constexpr int kRound = kW * 32 * kSub;
-constexpr int kTeamRows = 4096; // up to here merge_kernel gives a row a whole CTA
+constexpr int kTeamRows = 1024; // up to here merge_kernel gives a row whole CTAs
 constexpr float kLazy4 = 8.0f;  // re-anchor when a step's max exceeds m by this (log2)
 
 template <int D, int NT>
@@ -390,7 +390,12 @@ fp4_kernel(const FwdParams p) {
             bulk_load(smem_u32(dst), cache + (int64_t)id * p.hk * page_bytes + half, copy_bytes, bar);
         }
     };
-    // Take the next piece, steps [pos, ...) of one job, and start its copies.
+    // Tile row r: position i_first + (h_first + r) / g, head (h_first + r) mod g.
+    auto pos_of = [&](int r) { return i_first + (int)((unsigned)(h_first + r) / (unsigned)g); };
+    auto head_of = [&](int r) { return hkv * g + (int)((unsigned)(h_first + r) % (unsigned)g); };
+    auto out_row = [&](int r) { return (q0 + pos_of(r)) * p.hq + head_of(r); };
+    // Take the next piece, steps [pos, ...) of one job: start its copies, lay out
+    // its Q (the last piece's steps are done with theirs).
     auto take = [&]() {
         while (pos - seq_base >= (uint32_t)sw.steps * sw.tiles * p.hk) {
             seq_base += (uint32_t)sw.steps * sw.tiles * p.hk;
@@ -421,35 +426,37 @@ fp4_kernel(const FwdParams p) {
                 (b == 64 && run ? b * C::kCodeRow : 0);
         pos = end;
         id_next = block_of(0);
+        // Q (eight lanes a row) is fetched while the block ids are on their way,
+        // where the registers allow it beside the last piece's o.
+        constexpr int kPer = D / 8, kIter = C::kRows / 4;
+        constexpr bool kEarly = NT * D <= 256;
+        uint4 w[kEarly ? kIter : 1][kPer / 8];
+        auto load_q = [&](int r, uint4 (&x)[kPer / 8]) {
+#pragma unroll
+            for (int c = 0; c < kPer / 8; ++c)
+                x[c] = r < nrows ? __ldg(reinterpret_cast<const uint4*>(p.q + out_row(r) * D + (lane & 7) * kPer) + c)
+                                 : make_uint4(0, 0, 0, 0);
+        };
+        if constexpr (kEarly) {
+#pragma unroll
+            for (int i = 0; i < kIter; ++i) load_q(4 * i + (lane >> 3), w[i]);
+        }
 #pragma unroll
         for (int i = 0; i < kDepth; ++i) issue(i);
-    };
-    // Tile row r: position i_first + (h_first + r) / g, head (h_first + r) mod g.
-    auto pos_of = [&](int r) { return i_first + (int)((unsigned)(h_first + r) / (unsigned)g); };
-    auto head_of = [&](int r) { return hkv * g + (int)((unsigned)(h_first + r) % (unsigned)g); };
-    auto out_row = [&](int r) { return (q0 + pos_of(r)) * p.hq + head_of(r); };
-
-    take();
-    for (;;) {
-        // ---- Q: f16 in fragment order, each row scaled by a power of two so
-        // that its largest magnitude lies in [1, 2) (f16 covers 2^-24 below
-        // that; the factor goes into the row's score scale).  Eight lanes a row.
-        for (int r = lane >> 3; r < C::kRows; r += 4) {
-            constexpr int kPer = D / 8;
-            const int e0 = (lane & 7) * kPer;
-            uint4 w[kPer / 8];
+        // Q as f16 in fragment order, each row scaled by a power of two so that
+        // its largest magnitude lies in [1, 2) (f16 covers 2^-24 below that; the
+        // factor goes into the row's score scale).
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+            const int r = 4 * i + (lane >> 3), e0 = (lane & 7) * kPer;
+            uint4 (&x)[kPer / 8] = w[kEarly ? i : 0];
+            if constexpr (!kEarly) load_q(r, x);
             uint32_t amax = 0;
 #pragma unroll
-            for (int c = 0; c < kPer / 8; ++c) {
-                w[c] = r < nrows ? __ldg(reinterpret_cast<const uint4*>(p.q + out_row(r) * D + e0) + c)
-                                 : make_uint4(0, 0, 0, 0);
-                const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    amax = max(amax, v[k] & 0x7fffu);
-                    amax = max(amax, (v[k] >> 16) & 0x7fffu);
-                }
-            }
+            for (int c = 0; c < kPer / 8; ++c)
+                amax = __vmaxu2(amax, __vmaxu2(__vmaxu2(x[c].x & 0x7fff7fffu, x[c].y & 0x7fff7fffu),
+                                               __vmaxu2(x[c].z & 0x7fff7fffu, x[c].w & 0x7fff7fffu)));
+            amax = max(amax & 0xffffu, amax >> 16);
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
@@ -461,7 +468,7 @@ fp4_kernel(const FwdParams p) {
             if ((lane & 7) == 0) q_scale[r] = __int_as_float((127 + e) << 23);
 #pragma unroll
             for (int c = 0; c < kPer / 8; ++c) {
-                const uint32_t v[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+                const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
                 for (int k = 0; k < 4; k += 2) {
                     int step, tt, half;
@@ -473,7 +480,10 @@ fp4_kernel(const FwdParams p) {
             }
         }
         __syncwarp();
+    };
 
+    take();
+    for (;;) {
         // ---- per-lane row constants: rows 8 n + 2t + c (mu: m, or 0 while m is
         // -inf).  Rows that do not exist see what the last row sees: their
         // results are never stored, and tile-wide tests stay simple.
@@ -502,6 +512,14 @@ fp4_kernel(const FwdParams p) {
         full_hi = min(full_hi, __shfl_xor_sync(0xffffffffu, full_hi, 1));
         full_hi = min(full_hi, __shfl_xor_sync(0xffffffffu, full_hi, 2));
 
+        float* scores[NT][2];            // EMIT: the rows' scores at the lane's first key
+        if constexpr (EMIT) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    scores[j][c] = p.scores + out_row(min(8 * j + 2 * t + c, nrows - 1)) * p.score_stride + rho(u);
+        }
         float o[C::kKS][NT][4];
 #pragma unroll
         for (int i = 0; i < C::kKS; ++i)
@@ -612,7 +630,7 @@ fp4_kernel(const FwdParams p) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         if (8 * j + 2 * t + c >= nrows) continue;
-                        float* dst = p.scores + out_row(8 * j + 2 * t + c) * p.score_stride + key0 + rho(u);
+                        float* dst = scores[j][c] + key0;
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             if (key0 + rho(u) + 8 * k < sk) dst[8 * k] = sacc[k >> 1][j][c + 2 * (k & 1)];
@@ -742,7 +760,7 @@ fp4_kernel(const FwdParams p) {
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
                 if (8 * j + 2 * t + c >= e_rows) continue;
                 const int64_t row = e_row[j][c];
-                if (e_piece == 0 && u == 0) p.row_pieces[row] = e_pieces;
+                if (e_piece == 0 && u == 0) p.row_pieces[row] = make_int4(e_pieces, e_pieces, e_pieces, e_pieces);
                 if (e_pieces == 1) {
                     if (EMIT && u == 0) *reinterpret_cast<float2*>(p.part_ml + row * 2) = make_float2(m[j][c], v);
                     const float f = row_factor(p, e_head[j][c], m[j][c], v);
@@ -772,53 +790,74 @@ fp4_kernel(const FwdParams p) {
 }
 
 // Joins the pieces of the rows that have more than one, in piece order, and
-// leaves row_pieces at 0.  TEAM: a CTA per row, each warp a quarter of its pieces
-// (few rows, cut into many pieces); else a warp per row.  Eight pieces' loads
-// are in flight at a time.
+// leaves row_pieces at 0.  TEAM: a CTA of eight warps per row and 64 dims, each
+// warp an eighth of the pieces (few rows, cut into many pieces: 150 at most on
+// the four-request batch at d = 256, joined in 5 us); else a warp per row.
+// kAhead pieces' loads are in flight at a time, and their statistics with them:
+// the running maximum is re-anchored once per batch.
+constexpr int kAhead = 8;
+
 template <int D, bool EMIT, bool TEAM>
-__global__ void __launch_bounds__(kW * 32) merge_kernel(const FwdParams p) {
-    constexpr int kPer = D / 32;             // dims per lane
-    __shared__ float2 s_ml[kW];
-    __shared__ float s_o[TEAM ? kW : 1][D];
+__global__ void __launch_bounds__(256) merge_kernel(const FwdParams p) {
+    constexpr int kPer = TEAM ? 2 : D / 32;  // dims per lane
+    constexpr int kParts = TEAM ? D / 64 : 1;
+    __shared__ float2 s_ml[8];
+    __shared__ float2 s_o[TEAM ? 8 : 1][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row = TEAM ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * kW + warp;
+    const int64_t row = TEAM ? (int64_t)blockIdx.x / kParts : (int64_t)blockIdx.x * 8 + warp;
+    const int part = TEAM ? blockIdx.x % kParts : 0;
     griddep_wait();
     if (row >= p.total_q * p.hq) return;
-    const int n = p.row_pieces[row];
-    if (TEAM) __syncthreads();
-    else __syncwarp();
-    if (n == 0) return;
-    if (TEAM ? threadIdx.x == 0 : lane == 0) p.row_pieces[row] = 0;
-    if (n == 1) return;
-    const int per = TEAM ? (n + kW - 1) / kW : n;
+    // Each part of a row has its own copy of the count to read and clear.
+    int n;
+    if constexpr (TEAM) {
+        int* count = reinterpret_cast<int*>(p.row_pieces + row) + part;
+        n = *count;
+        __syncthreads();
+        if (threadIdx.x == 0) *count = 0;
+    } else {
+        n = p.row_pieces[row].x;
+        __syncwarp();
+        if (lane == 0) p.row_pieces[row] = make_int4(0, 0, 0, 0);
+    }
+    if (n <= 1) return;
+    const int per = TEAM ? (n + 7) / 8 : n;
     const int k0 = TEAM ? min(n, warp * per) : 0, k1 = min(n, k0 + per);
     const float2* st = reinterpret_cast<const float2*>(p.piece_ml) + row * p.splits;
+    const int64_t o0 = row * p.splits * D + part * 64 + lane * kPer;
     float M = -INFINITY, L = 0.f, acc[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-    for (int k = k0 + lane; k < k1; k += 32) M = fmaxf(M, st[k].x);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     auto join = [&](auto bf16_parts) {
         constexpr bool kBf16 = decltype(bf16_parts)::value;
-        for (int kk = k0; kk < k1; kk += 8) {
-            float2 v[8];
-            uint32_t x[8][kBf16 ? kPer / 2 : kPer];
+        constexpr int kWords = kBf16 ? kPer / 2 : kPer;
+        for (int kk = k0; kk < k1; kk += kAhead) {
+            float2 v[kAhead];
+            uint32_t x[kAhead][kWords];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < kAhead; ++q) {
                 const int k = min(kk + q, k1 - 1);
                 v[q] = st[k];
-                const int64_t at = (row * p.splits + k) * D + lane * kPer;
-                const uint32_t* src = kBf16 ? reinterpret_cast<const uint32_t*>(
-                                                  reinterpret_cast<const __nv_bfloat16*>(p.part_o) + at)
-                                            : reinterpret_cast<const uint32_t*>(p.part_o + at);
+                const uint32_t* src =
+                    kBf16 ? reinterpret_cast<const uint32_t*>(reinterpret_cast<const __nv_bfloat16*>(p.part_o) + o0 +
+                                                              (int64_t)k * D)
+                          : reinterpret_cast<const uint32_t*>(p.part_o + o0 + (int64_t)k * D);
 #pragma unroll
-                for (int e = 0; e < (kBf16 ? kPer / 2 : kPer); ++e) x[q][e] = src[e];
+                for (int e = 0; e < kWords; ++e) x[q][e] = src[e];
             }
+            float top = M;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < kAhead; ++q) top = fmaxf(top, v[q].x);
+            if (top == -INFINITY) continue;              // pieces the row sees no key of
+            const float back = fast_exp2(M - top);
+            M = top;
+            L *= back;
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[e] *= back;
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
                 if (kk + q >= k1) break;
-                const float a = fast_exp2(v[q].x - M);   // 0 for a piece the row sees no key of
+                const float a = fast_exp2(v[q].x - M);
                 L = fmaf(a, v[q].y, L);
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) {
@@ -828,34 +867,31 @@ __global__ void __launch_bounds__(kW * 32) merge_kernel(const FwdParams p) {
             }
         }
     };
-    if (M != -INFINITY) {
-        if (p.part_bf16) join(std::true_type{});
-        else join(std::false_type{});
-    }
+    if (p.part_bf16) join(std::true_type{});
+    else join(std::false_type{});
     if constexpr (TEAM) {
         if (lane == 0) s_ml[warp] = make_float2(M, L);
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) s_o[warp][lane * kPer + e] = acc[e];
+        s_o[warp][lane] = make_float2(acc[0], acc[1]);
         __syncthreads();
         if (warp) return;
-        M = fmaxf(fmaxf(s_ml[0].x, s_ml[1].x), fmaxf(s_ml[2].x, s_ml[3].x));
-        L = 0.f;
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+        for (int q = 1; q < 8; ++q) M = fmaxf(M, s_ml[q].x);
+        L = acc[0] = acc[1] = 0.f;
         if (M != -INFINITY)
 #pragma unroll
-            for (int q = 0; q < kW; ++q) {
+            for (int q = 0; q < 8; ++q) {
                 const float a = fast_exp2(s_ml[q].x - M);
                 L = fmaf(a, s_ml[q].y, L);
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) acc[e] = fmaf(a, s_o[q][lane * kPer + e], acc[e]);
+                acc[0] = fmaf(a, s_o[q][lane].x, acc[0]);
+                acc[1] = fmaf(a, s_o[q][lane].y, acc[1]);
             }
     }
-    if (EMIT && lane == 0) *reinterpret_cast<float2*>(p.part_ml + row * 2) = make_float2(M, L);
+    if (EMIT && lane == 0 && part == 0) *reinterpret_cast<float2*>(p.part_ml + row * 2) = make_float2(M, L);
     const float f = row_factor(p, (int)(row % p.hq), M, L);
 #pragma unroll
     for (int e = 0; e < kPer; e += 2)
-        *reinterpret_cast<uint32_t*>(p.out + row * D + lane * kPer + e) = pack_bf16x2(acc[e] * f, acc[e + 1] * f);
+        *reinterpret_cast<uint32_t*>(p.out + row * D + part * 64 + lane * kPer + e) =
+            pack_bf16x2(acc[e] * f, acc[e + 1] * f);
 }
 
 template <int D, int NT, bool GEN, bool EMIT>
@@ -875,8 +911,8 @@ cudaError_t launch_t(const Fp4Plan& plan, const FwdParams& p, cudaStream_t strea
     cudaLaunchConfig_t cfg{};
     const int64_t rows = p.total_q * p.hq;
     const bool team = rows <= kTeamRows;
-    cfg.gridDim = dim3((unsigned)(team ? rows : (rows + kW - 1) / kW));
-    cfg.blockDim = dim3(kW * 32);
+    cfg.gridDim = dim3((unsigned)(team ? rows * (D / 64) : (rows + 7) / 8));
+    cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
@@ -888,10 +924,10 @@ cudaError_t launch_d(const Fp4Plan& plan, const FwdParams& p, cudaStream_t strea
     const bool gen = (p.flags & (UA_FLAG_SOFTCAP | UA_FLAG_ALIBI | UA_FLAG_QQ_BIAS)) != 0;
     const bool emit = p.scores != nullptr;
     if (plan.rows == 8) {
-        if (emit) return launch_t<D, 1, true, true>(plan, p, stream);
+        if (emit) return gen ? launch_t<D, 1, true, true>(plan, p, stream) : launch_t<D, 1, false, true>(plan, p, stream);
         return gen ? launch_t<D, 1, true, false>(plan, p, stream) : launch_t<D, 1, false, false>(plan, p, stream);
     }
-    if (emit) return launch_t<D, 2, true, true>(plan, p, stream);
+    if (emit) return gen ? launch_t<D, 2, true, true>(plan, p, stream) : launch_t<D, 2, false, true>(plan, p, stream);
     return gen ? launch_t<D, 2, true, false>(plan, p, stream) : launch_t<D, 2, false, false>(plan, p, stream);
 }
 
