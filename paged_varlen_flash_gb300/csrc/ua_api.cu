@@ -402,6 +402,21 @@ ua_status run_combine(const ua::FwdParams& fp, cudaStream_t st) {
 // the front of the workspace, laid out like the partials of one segment.
 ua_status run_fp4(ua_problem* p, ua::FwdParams* fp, cudaStream_t st) {
     const size_t rows = (size_t)fp->total_q * p->desc.num_q_heads;
+    ua::Fp4RowsPlan tiles;
+    if (ua::plan_fp4_rows(*fp, p->num_sms, p->ws_bytes, &tiles)) {
+        set_partials(p, fp, tiles.splits, tiles.chunk);
+        prof_mark(p, true, st);
+        const cudaError_t e = ua::launch_fp4_rows(tiles, *fp, st);
+        prof_mark(p, false, st);
+        if (e != cudaSuccess) {
+            note_cuda(e, "fp4 rows kernel launch");
+            return UA_ERR_CUDA;
+        }
+        const bool combine = tiles.splits > 1 || fp->scores;
+        p->last_launches = combine ? 2 : 1;
+        p->last_path = combine ? "fp4_rows+combine" : "fp4_rows";
+        return combine ? run_combine(*fp, st) : UA_OK;
+    }
     const size_t stats = fp->scores ? rows * 2 : 0;
     ua::Fp4Plan plan;
     if (!ua::plan_fp4(*fp, p->num_sms, p->ws_bytes - stats * sizeof(float) - 16, &plan)) return UA_ERR_UNSUPPORTED;
@@ -701,7 +716,8 @@ ua_status ua_forward_weights(ua_problem* p, const void* q, const void* k_cache, 
     if (d.kv_dtype == UA_DTYPE_FP4_E2M1) {
         rs = run_fp4(p, &fp, st);
         if (rs != UA_OK) return rs;
-        p->last_path = "fp4+merge+weights";
+        p->last_path = std::strncmp(p->last_path, "fp4_rows", 8) == 0 ? "fp4_rows+combine+weights"
+                                                                      : "fp4+merge+weights";
     } else {
         if (!ua::decode_tc_shape_ok(fp)) return UA_ERR_UNSUPPORTED;
         rs = encode_maps(p, k_cache, v_cache, true);

@@ -1,4 +1,4 @@
-// ua_fp4.h -- launcher of the attention kernel over 4-bit (e2m1) caches (internal).
+// ua_fp4.h -- launchers of the attention kernels over 4-bit (e2m1) caches (internal).
 #pragma once
 
 #include "ua_common.cuh"
@@ -23,5 +23,23 @@ bool plan_fp4(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4Plan* 
 // p.part_o, p.piece_ml and p.row_pieces the problem's workspace).  With p.scores set every
 // row's scores and its final (m, l), the latter in p.part_ml, are stored as well.
 cudaError_t launch_fp4(const Fp4Plan& plan, const FwdParams& p, cudaStream_t stream);
+
+// Calls with at least this many packed rows per KV head go to the tcgen05
+// kernel (tiles of 128 rows), the others to the register-operand one.
+constexpr int kFp4RowsMin = 33;
+
+struct Fp4RowsPlan {
+    int tiles = 1;   // row tiles per (sequence, kv head)
+    int splits = 1;  // KV segments of each
+    int chunk = 0;   // keys per segment (a multiple of 128)
+};
+
+// False when the call does not suit the tcgen05 kernel.
+bool plan_fp4_rows(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4RowsPlan* plan);
+
+// Enqueue it (p.splits / p.chunk / partial pointers set from the plan).  With
+// p.scores set every row's scores are stored as well and partials are written
+// even for one segment.
+cudaError_t launch_fp4_rows(const Fp4RowsPlan& plan, const FwdParams& p, cudaStream_t stream);
 
 }  // namespace ua

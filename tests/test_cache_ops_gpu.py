@@ -260,6 +260,12 @@ ATTEND = [
     (5, 5, 256, 16, (1, 30), (40, 31), dict(window=9, alibi=True, sinks=True)),
     (8, 2, 64, 64, (2, 2), (300, 2), dict(causal=False)),
     (12, 4, 128, 16, (1,), (5000,), {}),
+    (16, 2, 256, 64, (20, 1, 37), (150, 700, 37), {}),
+    (16, 2, 256, 16, (9,), (1400,), dict(softcap=30.0, window=300, sinks=True)),
+    (4, 4, 64, 32, (200, 0, 129), (300, 7, 129), dict(alibi=True, sinks=True)),
+    (8, 2, 128, 16, (300, 33), (300, 900), dict(window=70)),
+    (10, 2, 128, 64, (64, 26), (1300, 26), dict(softcap=10.0)),
+    (8, 1, 128, 32, (17, 6), (2100, 129), dict(causal=False)),
 ]
 
 
@@ -282,10 +288,11 @@ def test_attention_over_4_bits(case, partials):
         check_out(bt, got, s, o, a, mag, softcap, extra, bf16_p=partials == ua.UA_PARTIALS_BF16)
 
 
-def test_query_magnitudes_far_outside_f16():
-    bt = Batch(80, "fp4", 4, 2, 128, 16, (1, 1), (100, 37))
-    bt.q[0] *= 2.0 ** 60
-    bt.q[1] *= 2.0 ** -70
+@pytest.mark.parametrize("nq", [1, 20])
+def test_query_magnitudes_far_outside_f16(nq):
+    bt = Batch(80, "fp4", 4, 2, 128, 16, (nq, nq), (100, 37))
+    bt.q[:nq] *= 2.0 ** 60
+    bt.q[nq:] *= 2.0 ** -70
     bt.qb, bt.q = bits(bt.q)
     bt.scale = 2.0 ** -62
     p = bt.device().problem()
@@ -307,10 +314,11 @@ def test_4bit_rows_without_keys_and_infinite_sinks():
         check_out(bt, got, s, o, a, mag)
 
 
-def test_nan_in_places_no_row_sees_stays_out():
+@pytest.mark.parametrize("nq", [1, 10])
+def test_nan_in_places_no_row_sees_stays_out(nq):
     """NaN keys before every row's window, and after the end, reach nothing."""
-    bt = Batch(82, "fp4", 8, 2, 128, 64, (1, 1), (100, 130))
-    for s, upto in ((0, 60), (1, 90)):
+    bt = Batch(82, "fp4", 8, 2, 128, 64, (nq, nq), (100, 130))
+    for s, upto in ((0, 61 - nq), (1, 91 - nq)):
         for j in range(upto):
             blk = int(bt.table[s, j // 64])
             n = 64 * 64
@@ -321,15 +329,16 @@ def test_nan_in_places_no_row_sees_stays_out():
     got = p.forward(*bt.args(), flags).double().cpu().numpy()
     for s in range(2):
         keys, vals = (c.rows(bt.table[s], bt.sk[s]) for c in (bt.kc, bt.vc))
-        lo = bt.sk[s] - 40
-        o, a, _, mag = R.attention(bt.q[s:s + 1], keys[lo:], vals[lo:], bt.scale)
+        lo = bt.sk[s] - 39 - nq
+        o, a, _, mag = R.attention(bt.q[s * nq:(s + 1) * nq], keys[lo:], vals[lo:], bt.scale, window=40)
         check_out(bt, got, s, o, a, mag)
 
 
-def test_4bit_qq_bias():
-    bt = Batch(83, "fp4", 8, 2, 128, 16, (3, 20), (90, 20)).device()
+@pytest.mark.parametrize("g,sq", [(4, (3, 20)), (4, (3, 4)), (1, (3, 2)), (2, (50, 17))])
+def test_4bit_qq_bias(g, sq):
+    bt = Batch(83, "fp4", 2 * g, 2, 128, 16, sq, (90, 20)).device()
     flags = ua.UA_FLAG_CAUSAL | ua.UA_FLAG_QQ_BIAS
-    qq = bt.rng.normal(size=(20, 24)).astype(np.float32)
+    qq = bt.rng.normal(size=(max(sq), max(sq) + 4)).astype(np.float32)
     p = bt.problem(flags)
     p.set_qq_bias(torch.from_numpy(qq).cuda())
     got = p.forward(*bt.args(), flags).double().cpu().numpy()
@@ -338,27 +347,29 @@ def test_4bit_qq_bias():
         check_out(bt, got, s, o, a, mag, extra=5.0)
 
 
-def test_4bit_bad_blocks_and_lengths_are_reported():
-    bt = Batch(84, "fp4", 4, 2, 128, 16, (1, 1, 1), (40, 40, 40))
+@pytest.mark.parametrize("nq", [1, 40])
+def test_4bit_bad_blocks_and_lengths_are_reported(nq):
+    bt = Batch(84, "fp4", 4, 2, 128, 16, (nq, nq, nq), (40, 40, 40))
     bt.table[0, 1] = bt.blocks + 9
     p = bt.device().problem()
     bt.d_sk[2] = 0                                  # S_k < S_q
     got = p.forward(*bt.args(), ua.UA_FLAG_CAUSAL).double().cpu().numpy()
     assert p.check_device_error() == ua.UA_DEVERR_BLOCK_ID | ua.UA_DEVERR_CONTEXT
-    assert np.all(got[2] == 0) and np.all(np.isfinite(got))
+    assert np.all(got[2 * nq:] == 0) and np.all(np.isfinite(got))
     # The bad block's keys read as zeros.
     keys, vals = [np.zeros((40, 2, 128)) for _ in range(2)]
     for j in list(range(16)) + list(range(32, 40)):
         keys[j] = bt.kc.row(int(bt.table[0, j // 16]), j % 16)
         vals[j] = bt.vc.row(int(bt.table[0, j // 16]), j % 16)
-    o, a, _, mag = R.attention(bt.q[:1], keys, vals, bt.scale)
+    o, a, _, mag = R.attention(bt.q[:nq], keys, vals, bt.scale)
     check_out(bt, got, 0, o, a, mag)
     o, a, _, mag = bt.reference(1)
     check_out(bt, got, 1, o, a, mag)
 
 
-def test_4bit_bounded_wait_gives_up_and_recovers():
-    bt = Batch(85, "fp4", 8, 2, 128, 16, (1, 1), (600, 300)).device()
+@pytest.mark.parametrize("sq", [(1, 1), (40, 9)])
+def test_4bit_bounded_wait_gives_up_and_recovers(sq):
+    bt = Batch(85, "fp4", 8, 2, 128, 16, sq, (600, 300)).device()
     p = bt.problem()
     assert ua.binding.ua_debug_stall_data_waits(p.handle, 1) == 0
     p.forward(*bt.args(), ua.UA_FLAG_CAUSAL)
@@ -404,6 +415,9 @@ WEIGHTS = [
     ("fp4", 16, 1, 256, 64, (2, 3), (200, 3), 0.0, dict(alibi=True)),
     ("fp4", 40, 2, 128, 16, (1, 2), (90, 33), 1.0, {}),
     ("bf16", 8, 2, 128, 16, (2, 2), (60, 2), 1.0, dict(causal=False)),
+    ("fp4", 8, 2, 128, 32, (32, 8, 0, 33), (700, 8, 5, 140), 0.9, {}),
+    ("fp4", 16, 2, 256, 16, (10, 5), (300, 130), 1.0, dict(window=40, sinks=True)),
+    ("fp4", 4, 2, 64, 64, (140, 1), (140, 260), 0.0, dict(softcap=20.0, alibi=True)),
 ]
 
 
