@@ -6,21 +6,21 @@
 // scales from the pages, write f16 tiles (code x scale is exact in f16) in the
 // 128-byte-swizzled layout a TMA copy of a 16-bit cache would have, and the
 // products are the prefill kernels': S = Q K^T and O += P V, tcgen05.mma with
-// M = 128 rows, P in tensor memory over its own S tile.  Per 128-key tile at
-// d = 128 the tensor pipe needs 1,024 cycles, the converters about 370 issue
-// slots per SM sub-partition and the softmax about 600, so the three run side
-// by side near the MMAs' pace.
+// M = 128 rows, P in tensor memory over its own S tile.
 //
 // One CTA per (KV segment, tile of floor(128 / g) positions, KV head, sequence),
-// heaviest tile first.  Roles (12 warps):
-//   warps 0-3   softmax and epilogue: thread r owns row r (tensor-memory lane r)
-//               and all 128 key columns of an S tile;
-//   warps 4-7   converters: Q once (f16, each row scaled by a power of two into
-//               [1, 2)), then K and V tiles; the next tile's codes are in
-//               registers before the current one's stage is free;
-//   warp 8      MMA issuer and tensor-memory owner: S(j + 1) goes out before it
+// heaviest tile first.  Roles (14 warps):
+//   warps 0-3   softmax and epilogue: thread r owns row r (tensor-memory lane r);
+//               two passes over the tile's columns, 32 at a time (maximum, then
+//               P), so the code stays small: four roles share each scheduler's
+//               instruction cache, and a fully unrolled row cost 2-3 times as
+//               many cycles per instruction;
+//   warps 4-7   convert the K tiles, warps 8-11 the V tiles, both together Q
+//               before (f16, each row scaled by a power of two into [1, 2));
+//   warp 12     MMA issuer and tensor-memory owner: S(j + 1) goes out before it
 //               waits for P(j), so the tensor pipe works through the softmax;
-//   warps 9-11  complete the warpgroup that gives up registers.
+//   warp 13     bulk copies of the pages into a ring of 4-bit tiles.
+// Key tiles are 128 keys, at d = 256 64 (shared memory).
 // Tensor memory: S(0), S(1) in columns [0, 256), O in [256, 256 + d).
 #include <algorithm>
 #include <cstdint>
@@ -37,46 +37,52 @@ namespace {
 
 using namespace pf;
 
-constexpr int kBN = 128;           // keys per tile
-constexpr int kThreadsR = 384;
-constexpr int kWarpMmaR = 8;
-// 128 x (224 + 168 + 112) registers are the 384 x 168 of the launch.
-constexpr uint32_t kRegsSoftmaxR = 224;
-constexpr uint32_t kRegsIssueR = 112;
+constexpr int kThreadsR = 448;
+constexpr int kWarpMmaR = 12;
+constexpr int kWarpCopyR = 13;
 
 template <int D>
 struct RCfg {
-    static constexpr int kStages = D == 256 ? 1 : 2;    // K and V tiles in shared memory
+    static constexpr int kBN = D == 256 ? 64 : 128;     // keys per tile
+    static constexpr int kStages = D == 256 ? 1 : 2;    // f16 K and V tiles
+    static constexpr int kRing = D == 64 ? 4 : 3;       // 4-bit K and V tiles
     static constexpr int kPanels = D / 64;
-    static constexpr int kPanel = kBN * 128;            // 128 rows x 64 dims, f16
+    static constexpr int kQPanel = kRows * 128;         // 128 rows x 64 dims, f16
+    static constexpr int kPanel = kBN * 128;            // kBN keys x 64 dims, f16
     static constexpr int kTile = kPanels * kPanel;
+    static constexpr int kRaw = kBN * (D / 2 + D / 16); // codes, then scales
     static constexpr int kOffQ = 0;
-    static constexpr int kOffK = kTile;
+    static constexpr int kOffK = kPanels * kQPanel;
     static constexpr int kOffV = kOffK + kStages * kTile;
-    static constexpr int kOffScale = kOffV + kStages * kTile;   // Q's row scales
+    static constexpr int kOffRawK = kOffV + kStages * kTile;
+    static constexpr int kOffRawV = kOffRawK + kRing * kRaw;
+    static constexpr int kOffScale = kOffRawV + kRing * kRaw;   // Q's row scales
     static constexpr int kOffBar = kOffScale + kRows * 4;
-    // q_full, k_full, v_full, k_empty, v_empty [kStages], s_full[2], p_full[2],
-    // o_done[2], drain, never
-    static constexpr int kNumBars = 1 + 4 * kStages + 8;
+    // q_full, {k, v} x {full, empty} [kStages], {k, v} x {raw full, raw empty}
+    // [kRing], s_full[2], p_full[2], o_done[2], drain, never
+    static constexpr int kNumBars = 1 + 4 * kStages + 4 * kRing + 8;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kSmem = kOffMisc + 16 + 1024;
-    static constexpr int kTmemO = 2 * kBN;
+    static constexpr int kTmemO = 256;
     static constexpr int kChunks = D / 32;              // 16-byte runs of codes per key
     static constexpr int kEach = kBN * kChunks / 128;   // of them per converter thread and tile
     static_assert(kSmem <= 232448, "shared memory budget");
+    static_assert(kRaw % 16 == 0, "bulk copy alignment");
 };
 
-// One tile's codes of a converter thread: run i is chunk (128 i + t) mod kChunks
-// of key (128 i + t) / kChunks.
-template <int D>
-struct Codes {
-    uint4 c[RCfg<D>::kEach];
-    uint32_t s[RCfg<D>::kEach];    // two e4m3 scales
-};
+// Contiguous copy global -> shared (16-byte aligned, a multiple of 16 bytes),
+// completion signalled on `bar`.
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
 
 template <int D, bool GEN, bool EMIT>
 __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams p) {
     using C = RCfg<D>;
+    constexpr int kBN = C::kBN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -133,11 +139,12 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
 
     uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     const uint32_t q_full = smem_u32(bar_mem);
-    const uint32_t k_full0 = smem_u32(bar_mem + 1);
-    const uint32_t v_full0 = k_full0 + 8 * C::kStages;
-    const uint32_t k_empty0 = v_full0 + 8 * C::kStages;
-    const uint32_t v_empty0 = k_empty0 + 8 * C::kStages;
-    const uint32_t s_full0 = v_empty0 + 8 * C::kStages;
+    constexpr int kS = 8 * C::kStages, kR = 8 * C::kRing;
+    const uint32_t k_full0 = smem_u32(bar_mem + 1), v_full0 = k_full0 + kS;
+    const uint32_t k_empty0 = v_full0 + kS, v_empty0 = k_empty0 + kS;
+    const uint32_t rk_full0 = v_empty0 + kS, rv_full0 = rk_full0 + kR;
+    const uint32_t rk_empty0 = rv_full0 + kR, rv_empty0 = rk_empty0 + kR;
+    const uint32_t s_full0 = rv_empty0 + kR;
     const uint32_t p_full0 = s_full0 + 16;
     const uint32_t o_done0 = s_full0 + 32;
     const uint32_t drain = s_full0 + 48;
@@ -147,12 +154,18 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
     float* q_scale = reinterpret_cast<float*>(smem + C::kOffScale);
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 128);
+        mbar_init(q_full, 256);
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(k_full0 + 8 * i, 128);     // the converters
             mbar_init(v_full0 + 8 * i, 128);
             mbar_init(k_empty0 + 8 * i, 1);
             mbar_init(v_empty0 + 8 * i, 1);
+        }
+        for (int i = 0; i < C::kRing; ++i) {
+            mbar_init(rk_full0 + 8 * i, 1);
+            mbar_init(rv_full0 + 8 * i, 1);
+            mbar_init(rk_empty0 + 8 * i, 128);
+            mbar_init(rv_empty0 + 8 * i, 128);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full0 + 8 * i, 1);
@@ -176,8 +189,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
         return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, p.err));
     };
 
-    if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsIssueR));
+    if (warp >= 12) {
         if (warp == kWarpMmaR) {
             // ------------------------------ MMA issuer ------------------------------
             constexpr uint32_t idesc_qk = tc::idesc_f16_f32(kRows, kBN, false, false);
@@ -197,9 +209,10 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                     const uint32_t kst = smem_u32(smem + C::kOffK) + stg * C::kTile;
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const int off = (k >> 2) * C::kPanel + (k & 3) * 32;
-                        tc::mma_bf16(tmem + (j & 1) * kBN, tc::smem_desc_sw128(sQ + off, 16, 1024),
-                                     tc::smem_desc_sw128(kst + off, 16, 1024), idesc_qk, k > 0 ? 1u : 0u);
+                        const int pn = k >> 2, off = (k & 3) * 32;
+                        tc::mma_bf16(tmem + (j & 1) * 128, tc::smem_desc_sw128(sQ + pn * C::kQPanel + off, 16, 1024),
+                                     tc::smem_desc_sw128(kst + pn * C::kPanel + off, 16, 1024), idesc_qk,
+                                     k > 0 ? 1u : 0u);
                     }
                     tc::commit(s_full0 + 8 * (j & 1));
                     tc::commit(k_empty0 + 8 * stg);
@@ -224,7 +237,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                         for (int h = 0; h < D / kNV; ++h)
                             // A = P from tensor memory (16 keys = 8 columns), B = V
                             // MN-major, two 64-dim panels.
-                            tc::mma_bf16_ts(tmem + C::kTmemO + h * kNV, tmem + (j & 1) * kBN + k * 8,
+                            tc::mma_bf16_ts(tmem + C::kTmemO + h * kNV, tmem + (j & 1) * 128 + k * 8,
                                             tc::smem_desc_sw128(vst + h * 2 * C::kPanel + k * 16 * 128, C::kPanel, 1024),
                                             idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
                     tc::commit(o_done0 + 8 * (j & 1));
@@ -238,120 +251,152 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                 __syncwarp();
                 mbar_wait_bounded(drain, 0);
             }
+        } else {
+            // ------------------------------ bulk copies ------------------------------
+            // Pages are contiguous (codes, then scales); a tile is whole pages
+            // (or, of a 64-key page at d = 256, one).  Lane = (page, operand);
+            // codes and scales go to the tile's two parts.  Block ids are
+            // fetched one tile ahead.
+            const int b_log2 = 31 - __clz(p.b), page = lane >> 1, op = lane & 1;
+            const int pages = kBN >> b_log2, nblk = (sk + p.b - 1) >> b_log2;
+            const int64_t page_bytes = fp4_page_bytes(p.b, D);
+            const uint8_t* cache = static_cast<const uint8_t*>(op ? p.v_cache : p.k_cache) + hkv * page_bytes;
+            const int32_t* bt = p.block_table + (int64_t)s * p.bt_stride;
+            const uint32_t code_bytes = (uint32_t)p.b * (D / 2), scale_bytes = (uint32_t)p.b * (D / 16);
+            const uint32_t full0 = op ? rv_full0 : rk_full0, empty0 = op ? rv_empty0 : rk_empty0;
+            uint8_t* ring = smem + (op ? C::kOffRawV : C::kOffRawK);
+            auto id_of = [&](int j) -> int32_t {       // -2: no such page
+                const int blk = ((t_begin + j) * kBN >> b_log2) + page;
+                return j < n && page < pages && blk < nblk ? __ldg(bt + blk) : -2;
+            };
+            int32_t id_next = id_of(0);
+            int issued = 0;
+            for (int j = 0; j < n; ++j) {
+                const int slot = j % C::kRing;
+                const int32_t id = id_next;
+                id_next = id_of(j + 1);
+                if (j >= C::kRing && !wwait(empty0 + 8 * slot, ((j / C::kRing) + 1) & 1)) break;
+                const bool good = id >= 0 && (int64_t)id < p.num_blocks;
+                const unsigned mask = __ballot_sync(0xffffffffu, good);
+                uint8_t* codes = ring + slot * C::kRaw + page * code_bytes;
+                uint8_t* scales = ring + slot * C::kRaw + kBN * (D / 2) + page * scale_bytes;
+                if (page < pages && !good) {
+                    // A bad block's keys, and those past the last block, are
+                    // zeros (scale 0; codes are always finite).  The slot is
+                    // later overwritten by copies, hence the proxy fence.
+                    if (id != -2) atomicOr(p.err, (int)UA_DEVERR_BLOCK_ID);
+                    for (uint32_t e = 0; e < scale_bytes; e += 4) *reinterpret_cast<uint32_t*>(scales + e) = 0;
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane < 2)
+                    mbar_arrive_expect_tx(full0 + 8 * slot, (uint32_t)__popc(mask & (op ? 0xaaaaaaaau : 0x55555555u)) *
+                                                                (code_bytes + scale_bytes));
+                __syncwarp();
+                if (good) {
+                    const uint8_t* src = cache + (int64_t)id * p.hk * page_bytes;
+                    bulk_copy(smem_u32(codes), src, code_bytes, full0 + 8 * slot);
+                    bulk_copy(smem_u32(scales), src + code_bytes, scale_bytes, full0 + 8 * slot);
+                }
+                issued = j + 1;
+            }
+            if (*abort_flag)
+                // Let every copy this warp issued land before the CTA ends.
+                for (int j = max(0, issued - C::kRing); j < issued; ++j)
+                    mbar_wait_bounded(full0 + 8 * (j % C::kRing), (j / C::kRing) & 1);
+            __syncwarp();
         }
     } else if (warp >= 4) {
         // -------------------------------- converters --------------------------------
-        const int t = threadIdx.x - 128;
-        const int b_log2 = 31 - __clz(p.b);
-        const int nblk = (sk + p.b - 1) >> b_log2;
-        const int32_t* bt = p.block_table + (int64_t)s * p.bt_stride;
-        const int64_t page_bytes = fp4_page_bytes(p.b, D);
-        auto key_of = [&](int j, int i) { return (t_begin + j) * kBN + (i * 128 + t) / C::kChunks; };
-        const int chunk = t % C::kChunks;       // the same in every run: 128 is a multiple of kChunks
-        // Block id of each run's key; -1: no key.
-        int32_t id[C::kEach];
-        auto fetch_ids = [&](int j) {
+        const bool is_v = warp >= 8;
+        const int t = threadIdx.x & 127;
+        // Q: eight threads a row, 32 rows per pass, several passes' loads together.
+        constexpr int kPer = D / 8, kPass = D == 256 ? 2 : 4;
+#pragma unroll 1
+        for (int pass = 0; pass < 4; pass += kPass) {
+            uint4 x[kPass][kPer / 8];
+            const int r_0 = pass * 32 + ((threadIdx.x - 128) >> 3), e0 = (t & 7) * kPer;
 #pragma unroll
-            for (int i = 0; i < C::kEach; ++i) {
-                const int blk = key_of(j, i) >> b_log2;
-                id[i] = j < n && blk < nblk ? __ldg(bt + blk) : -1;
-                if (j < n && blk < nblk && (id[i] < 0 || (int64_t)id[i] >= p.num_blocks)) {
-                    atomicOr(p.err, (int)UA_DEVERR_BLOCK_ID);
-                    id[i] = -1;                 // a bad block: its keys read as zeros
+            for (int a = 0; a < kPass; ++a) {
+                const int r = r_0 + 32 * a, i = first + r / g;
+                const bool real = r < g * ppt && i <= last;
+#pragma unroll
+                for (int c = 0; c < kPer / 8; ++c)
+                    x[a][c] = real ? __ldg(reinterpret_cast<const uint4*>(
+                                         p.q + ((q0 + i) * p.hq + hkv * g + r % g) * D + e0) + c)
+                                   : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int a = 0; a < kPass; ++a) {
+                const int r = r_0 + 32 * a;
+                uint32_t amax = 0;
+#pragma unroll
+                for (int c = 0; c < kPer / 8; ++c)
+                    amax = __vmaxu2(amax, __vmaxu2(__vmaxu2(x[a][c].x & 0x7fff7fffu, x[a][c].y & 0x7fff7fffu),
+                                                   __vmaxu2(x[a][c].z & 0x7fff7fffu, x[a][c].w & 0x7fff7fffu)));
+                amax = max(amax & 0xffffu, amax >> 16);
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
+                const int ef = (int)(amax >> 7);
+                const int e = (amax == 0 || ef == 255) ? 0 : min(max(ef, 1), 253) - 127;
+                const float down = __int_as_float((127 - e) << 23);
+                if ((t & 7) == 0) q_scale[r] = __int_as_float((127 + e) << 23);
+#pragma unroll
+                for (int c = 0; c < kPer / 8; ++c) {
+                    const uint32_t v[4] = {x[a][c].x, x[a][c].y, x[a][c].z, x[a][c].w};
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+                            : "=r"(h[k]) : "f"(bf16_hi(v[k]) * down), "f"(bf16_lo(v[k]) * down));
+                    const int dim = e0 + c * 8;
+                    *reinterpret_cast<uint4*>(smem + C::kOffQ + (dim >> 6) * C::kQPanel + r * 128 +
+                                              ((((dim & 63) >> 3) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
             }
-        };
-        auto load = [&](const void* cache, int j, bool visible_only, Codes<D>& x) {
-#pragma unroll
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
+        const uint32_t full0 = is_v ? v_full0 : k_full0, empty0 = is_v ? v_empty0 : k_empty0;
+        const uint32_t raw_full0 = is_v ? rv_full0 : rk_full0, raw_empty0 = is_v ? rv_empty0 : rk_empty0;
+        uint8_t* tiles_mem = smem + (is_v ? C::kOffV : C::kOffK);
+        const uint8_t* raw_mem = smem + (is_v ? C::kOffRawV : C::kOffRawK);
+        // Run i of a thread: 16-byte chunk t mod kChunks of key 128 i / kChunks + t / kChunks.
+        const int chunk = t % C::kChunks, k0 = t / C::kChunks;
+        for (int j = 0; j < n; ++j) {
+            const int stg = j % C::kStages, slot = j % C::kRing;
+            if (!wwait(raw_full0 + 8 * slot, (j / C::kRing) & 1)) break;
+            if (j >= C::kStages && !wwait(empty0 + 8 * stg, ((j / C::kStages) + 1) & 1)) break;
+            const uint8_t* raw = raw_mem + slot * C::kRaw;
+            uint8_t* tile_mem = tiles_mem + stg * C::kTile + (chunk >> 1) * C::kPanel;
+            // Keys no row of the tile sees are zeros in V: whatever their slots
+            // hold must not reach O (0 * NaN is NaN).
+            const int key0 = (t_begin + j) * kBN;
+            const bool edge = is_v && (key0 < vis_beg || key0 + kBN > vis_end);
+#pragma unroll 2
             for (int i = 0; i < C::kEach; ++i) {
-                const int key = key_of(j, i), slot = key & (p.b - 1);
-                x.c[i] = make_uint4(0, 0, 0, 0);
-                x.s[i] = 0;
-                // Keys no row of the tile sees are zeros in V: whatever their
-                // slots hold must not reach O (0 * NaN is NaN).
-                if (id[i] < 0 || (visible_only && (key < vis_beg || key >= vis_end))) continue;
-                const uint8_t* page = static_cast<const uint8_t*>(cache) + ((int64_t)id[i] * p.hk + hkv) * page_bytes;
-                x.c[i] = __ldg(reinterpret_cast<const uint4*>(page + slot * (D / 2)) + chunk);
-                x.s[i] = __ldg(reinterpret_cast<const uint16_t*>(page + p.b * (D / 2) + slot * (D / 16)) + chunk);
-            }
-        };
-        // Dims 32 chunk .. + 31 of the run's key: panel chunk / 2, four 16-byte
-        // units, 128-byte swizzled.
-        auto convert = [&](const Codes<D>& x, int j, uint8_t* tile_mem) {
-#pragma unroll
-            for (int i = 0; i < C::kEach; ++i) {
-                const int k = key_of(j, i) & (kBN - 1);
-                uint8_t* row = tile_mem + (chunk >> 1) * C::kPanel + k * 128;
-                const uint32_t sc = e4m3x2_to_f16(x.s[i]), s0 = splat_lo(sc), s1 = splat_hi(sc);
-                const uint32_t w[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
+                const int k = k0 + i * (128 / C::kChunks);
+                const uint4 c = *reinterpret_cast<const uint4*>(raw + k * (D / 2) + chunk * 16);
+                uint32_t s8 = *reinterpret_cast<const uint16_t*>(raw + kBN * (D / 2) + k * (D / 16) + chunk * 2);
+                if (edge && (key0 + k < vis_beg || key0 + k >= vis_end)) s8 = 0;
+                const uint32_t sc = e4m3x2_to_f16(s8), s0 = splat_lo(sc), s1 = splat_hi(sc);
+                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                // Dims 32 chunk .. + 31: four 16-byte units of the row, swizzled.
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t h[4];
                     e2m1x8_to_f16(w[q], h);
                     const uint32_t f = q < 2 ? s0 : s1;
-                    *reinterpret_cast<uint4*>(row + ((((chunk & 1) * 4 + q) ^ (k & 7)) << 4)) =
+                    *reinterpret_cast<uint4*>(tile_mem + k * 128 + ((((chunk & 1) * 4 + q) ^ (k & 7)) << 4)) =
                         make_uint4(mul_f16x2(h[0], f), mul_f16x2(h[1], f), mul_f16x2(h[2], f), mul_f16x2(h[3], f));
                 }
             }
-        };
-        Codes<D> kx, vx;
-        fetch_ids(0);
-        load(p.k_cache, 0, false, kx);
-        load(p.v_cache, 0, true, vx);
-        fetch_ids(1);
-        // Q: eight threads a row, 16 rows at a time.
-        for (int r = t >> 3; r < kRows; r += 16) {
-            constexpr int kPer = D / 8;
-            const int i = first + r / g, e0 = (t & 7) * kPer;
-            const bool real = r < g * ppt && i <= last;
-            uint4 x[kPer / 8];
-            uint32_t amax = 0;
-#pragma unroll
-            for (int c = 0; c < kPer / 8; ++c) {
-                x[c] = real ? __ldg(reinterpret_cast<const uint4*>(
-                                  p.q + ((q0 + i) * p.hq + hkv * g + r % g) * D + e0) + c)
-                            : make_uint4(0, 0, 0, 0);
-                amax = __vmaxu2(amax, __vmaxu2(__vmaxu2(x[c].x & 0x7fff7fffu, x[c].y & 0x7fff7fffu),
-                                               __vmaxu2(x[c].z & 0x7fff7fffu, x[c].w & 0x7fff7fffu)));
-            }
-            amax = max(amax & 0xffffu, amax >> 16);
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
-            const int ef = (int)(amax >> 7);
-            const int e = (amax == 0 || ef == 255) ? 0 : min(max(ef, 1), 253) - 127;
-            const float down = __int_as_float((127 - e) << 23);
-            if ((t & 7) == 0) q_scale[r] = __int_as_float((127 + e) << 23);
-#pragma unroll
-            for (int c = 0; c < kPer / 8; ++c) {
-                const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-                uint32_t h[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h[k]) : "f"(bf16_hi(v[k]) * down), "f"(bf16_lo(v[k]) * down));
-                const int dim = e0 + c * 8;
-                *reinterpret_cast<uint4*>(smem + C::kOffQ + (dim >> 6) * C::kPanel + r * 128 +
-                                          ((((dim & 63) >> 3) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(q_full);
-        for (int j = 0; j < n; ++j) {
-            const int stg = j % C::kStages;
-            if (j >= C::kStages && !wwait(k_empty0 + 8 * stg, ((j / C::kStages) + 1) & 1)) break;
-            convert(kx, j, smem + C::kOffK + stg * C::kTile);
             fence_proxy_async_smem();
-            mbar_arrive(k_full0 + 8 * stg);
-            load(p.k_cache, j + 1, false, kx);   // past the last tile every id is -1
-            if (j >= C::kStages && !wwait(v_empty0 + 8 * stg, ((j / C::kStages) + 1) & 1)) break;
-            convert(vx, j, smem + C::kOffV + stg * C::kTile);
-            fence_proxy_async_smem();
-            mbar_arrive(v_full0 + 8 * stg);
-            load(p.v_cache, j + 1, true, vx);
-            fetch_ids(j + 2);
+            mbar_arrive(full0 + 8 * stg);
+            mbar_arrive(raw_empty0 + 8 * slot);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmaxR));
         // ------------------------------ softmax, epilogue ------------------------------
         const int r = threadIdx.x;
         const int pos = first + r / g;
@@ -375,79 +420,84 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
         for (int j = 0; ok && j < n; ++j) {
             if (!(ok = wwait(s_full0 + 8 * (j & 1), (j >> 1) & 1))) break;
             const int key0 = (t_begin + j) * kBN;
-            const uint32_t s_col = trow + (j & 1) * kBN;
+            const uint32_t s_col = trow + (j & 1) * 128;
+            const bool edge = key0 < full_lo || key0 + kBN - 1 > full_hi;
             bool reanchor = false;
             float alpha = 1.f;
             if (live) {
-                uint32_t sr[kBN / 32][32];
                 tc::fence_after_sync();
-#pragma unroll
-                for (int c = 0; c < kBN / 32; ++c) tc::ld32(s_col + c * 32, sr[c]);
-                tc::wait_ld();
-#pragma unroll
-                for (int c = 0; c < kBN / 32; ++c)
+                // x of 32 columns, log2 units, masked.
+                auto scores = [&](int c, uint32_t (&x)[32]) {
+                    tc::ld32(s_col + c * 32, x);
+                    tc::wait_ld();
+                    const int key = key0 + c * 32;
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        float x = __uint_as_float(sr[c][e]) * fac;
+                        float v = __uint_as_float(x[e]) * fac;
                         if constexpr (GEN) {
-                            const int key = key0 + c * 32 + e;
-                            if (softcap) x = p.softcap * tanh_from_exp2(x / p.softcap);
-                            if (alibi) x += slope * (float)(key - ctx);
-                            if (qq && valid && key >= ctx && key <= hi)
-                                x += __ldg(p.qq_bias + (int64_t)pos * p.qq_stride + (key - ctx));
-                            x *= kLog2e;
+                            if (softcap) v = p.softcap * tanh_from_exp2(v / p.softcap);
+                            if (alibi) v += slope * (float)(key + e - ctx);
+                            if (qq && valid && key + e >= ctx && key + e <= hi)
+                                v += __ldg(p.qq_bias + (int64_t)pos * p.qq_stride + (key + e - ctx));
+                            v *= kLog2e;
                         }
-                        sr[c][e] = __float_as_uint(x);
+                        x[e] = __float_as_uint(v);
                     }
-                if (key0 < full_lo || key0 + kBN - 1 > full_hi) {
+                    if (edge) {
 #pragma unroll
-                    for (int c = 0; c < kBN / 32; ++c)
+                        for (int e = 0; e < 32; ++e)
+                            if (key + e < lo || key + e > hi) x[e] = __float_as_uint(-INFINITY);
+                    }
+                    // The second pass reads the finished scores back.
+                    if constexpr (GEN) tc::st32(s_col + c * 32, x);
+                };
+                float top = -INFINITY;
+#pragma unroll 1
+                for (int c = 0; c < kBN / 32; ++c) {
+                    uint32_t x[32];
+                    scores(c, x);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int key = key0 + c * 32 + e;
-                            if (key < lo || key > hi) sr[c][e] = __float_as_uint(-INFINITY);
-                        }
+                    for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                        for (int a = 0; a < 4; ++a)
+                            mx[a] = fmax3(mx[a], __uint_as_float(x[e + 2 * a]), __uint_as_float(x[e + 2 * a + 1]));
+                    top = fmax3(top, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 }
-                if (EMIT && valid) {
-                    // 128 consecutive floats a thread (the row stride is a
-                    // multiple of 128), whole sectors by 32-byte stores.
-                    float* dst = p.scores + row * p.score_stride + key0;
-#pragma unroll
-                    for (int c = 0; c < kBN / 32; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + c * 32 + e),
-                                         "r"(sr[c][e]), "r"(sr[c][e + 1]), "r"(sr[c][e + 2]), "r"(sr[c][e + 3]),
-                                         "r"(sr[c][e + 4]), "r"(sr[c][e + 5]), "r"(sr[c][e + 6]), "r"(sr[c][e + 7])
-                                         : "memory");
-                }
-                float mx[8];
-#pragma unroll
-                for (int a = 0; a < 8; ++a) mx[a] = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < kBN / 32; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; e += 16)
-#pragma unroll
-                        for (int a = 0; a < 8; ++a)
-                            mx[a] = fmax3(mx[a], __uint_as_float(sr[c][e + 2 * a]), __uint_as_float(sr[c][e + 2 * a + 1]));
-                const float top = fmax3(fmax3(mx[0], mx[1], mx[2]), fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+                if constexpr (GEN) tc::wait_st();
                 reanchor = top > m + kLazy;
                 if (reanchor) {
                     alpha = fast_exp2(m - top);
                     m = top;
                 }
-                // P = 2^(x - m): fp32 into the row sum, f16 over the first 64
-                // columns of S (every S value of this row has been read).
+                // P = 2^(x - m): fp32 into the row sum, f16 over columns of S
+                // that have been read (16 of P for 32 of S).
                 const float mu = m == -INFINITY ? 0.f : m;
                 float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < kBN / 32; ++c) {
-                    uint32_t pk[16];
+                    uint32_t x[32], pk[16];
+                    if constexpr (GEN) {
+                        tc::ld32(s_col + c * 32, x);
+                        tc::wait_ld();
+                    } else {
+                        scores(c, x);
+                    }
+                    if (EMIT && valid) {
+                        // 32 consecutive floats a thread (the row stride is a
+                        // multiple of 128), whole sectors by 32-byte stores.
+                        float* dst = p.scores + row * p.score_stride + key0 + c * 32;
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + e),
+                                         "r"(x[e]), "r"(x[e + 1]), "r"(x[e + 2]), "r"(x[e + 3]), "r"(x[e + 4]),
+                                         "r"(x[e + 5]), "r"(x[e + 6]), "r"(x[e + 7])
+                                         : "memory");
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float p0 = fast_exp2(__uint_as_float(sr[c][e]) - mu);
-                        const float p1 = fast_exp2(__uint_as_float(sr[c][e + 1]) - mu);
+                        const float p0 = fast_exp2(__uint_as_float(x[e]) - mu);
+                        const float p1 = fast_exp2(__uint_as_float(x[e + 1]) - mu);
                         sum[(e >> 1) & 3] += p0 + p1;
                         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[e / 2]) : "f"(p1), "f"(p0));
                     }
@@ -556,15 +606,15 @@ bool plan_fp4_rows(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4R
     if (p.g > kRows || (int64_t)p.g * p.max_seqlen_q < kFp4RowsMin) return false;
     const int ppt = kRows / p.g;
     const int64_t tiles = (p.max_seqlen_q + ppt - 1) / ppt;
-    // Segments of at least four key tiles, as many as give two CTAs per SM.
+    // Segments of at least 512 keys, as many as give two CTAs per SM.
     const int64_t base = (int64_t)p.hk * p.num_seqs * tiles;
     const int64_t want = (2LL * num_sms + base - 1) / base;
-    const int64_t by_len = std::max<int64_t>(1, p.max_seqlen_k / (4 * kBN));
+    const int64_t by_len = std::max<int64_t>(1, p.max_seqlen_k / 512);
     int64_t splits = std::min<int64_t>(std::min<int64_t>(want, by_len), 64);
     const size_t per_split = fp4_workspace_bytes(p.total_q * p.hq, p.d);
     splits = std::max<int64_t>(1, std::min<int64_t>(splits, (int64_t)(workspace_bytes / per_split)));
     const int64_t per = (p.max_seqlen_k + splits - 1) / splits;
-    plan->chunk = (int)std::min<int64_t>((per + kBN - 1) / kBN * kBN, 1 << 30);
+    plan->chunk = (int)std::min<int64_t>((per + 127) / 128 * 128, 1 << 30);
     plan->splits = (int)((p.max_seqlen_k + (int64_t)plan->chunk - 1) / plan->chunk);
     if (tiles * plan->splits > 0x7fffffffLL || p.hk > 65535) return false;
     plan->tiles = (int)tiles;
