@@ -11,7 +11,7 @@
 // One CTA per (KV segment, tile of floor(128 / g) positions, KV head, sequence),
 // heaviest tile first.  Roles (14 warps):
 //   warps 0-3   softmax and epilogue: thread r owns row r (tensor-memory lane r);
-//               two passes over the tile's columns, 32 at a time (maximum, then
+//               two passes over the tile's columns, 64 at a time (maximum, then
 //               P), so the code stays small: four roles share each scheduler's
 //               instruction cache, and a fully unrolled row cost 2-3 times as
 //               many cycles per instruction;
@@ -39,7 +39,7 @@ using namespace pf;
 
 constexpr int kThreadsR = 448;
 constexpr int kWarpMmaR = 12;
-constexpr int kWarpCopyR = 13;
+constexpr int kCols = 64;          // columns of S a softmax thread holds at a time
 
 template <int D>
 struct RCfg {
@@ -426,84 +426,94 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
             float alpha = 1.f;
             if (live) {
                 tc::fence_after_sync();
-                // x of 32 columns, log2 units, masked.
-                auto scores = [&](int c, uint32_t (&x)[32]) {
-                    tc::ld32(s_col + c * 32, x);
-                    tc::wait_ld();
-                    const int key = key0 + c * 32;
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        float v = __uint_as_float(x[e]) * fac;
-                        if constexpr (GEN) {
-                            if (softcap) v = p.softcap * tanh_from_exp2(v / p.softcap);
-                            if (alibi) v += slope * (float)(key + e - ctx);
-                            if (qq && valid && key + e >= ctx && key + e <= hi)
-                                v += __ldg(p.qq_bias + (int64_t)pos * p.qq_stride + (key + e - ctx));
-                            v *= kLog2e;
-                        }
-                        x[e] = __float_as_uint(v);
-                    }
-                    if (edge) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (key + e < lo || key + e > hi) x[e] = __float_as_uint(-INFINITY);
-                    }
-                    // The second pass reads the finished scores back.
-                    if constexpr (GEN) tc::st32(s_col + c * 32, x);
-                };
+                // First pass: the maximum.  Plain scores stay as the MMA left
+                // them (their factor is positive); a general score chain is
+                // finished here and written back for the second pass.
                 float top = -INFINITY;
 #pragma unroll 1
-                for (int c = 0; c < kBN / 32; ++c) {
-                    uint32_t x[32];
-                    scores(c, x);
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                for (int c = 0; c < kBN; c += kCols) {
+                    uint32_t x[kCols / 32][32];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
+                    for (int h = 0; h < kCols / 32; ++h) tc::ld32(s_col + c + h * 32, x[h]);
+                    tc::wait_ld();
 #pragma unroll
-                        for (int a = 0; a < 4; ++a)
-                            mx[a] = fmax3(mx[a], __uint_as_float(x[e + 2 * a]), __uint_as_float(x[e + 2 * a + 1]));
-                    top = fmax3(top, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    for (int h = 0; h < kCols / 32; ++h) {
+                        const int key = key0 + c + h * 32;
+                        if constexpr (GEN) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                float v = __uint_as_float(x[h][e]) * tau;
+                                if (softcap) v = p.softcap * tanh_from_exp2(v / p.softcap);
+                                if (alibi) v += slope * (float)(key + e - ctx);
+                                if (qq && valid && key + e >= ctx && key + e <= hi)
+                                    v += __ldg(p.qq_bias + (int64_t)pos * p.qq_stride + (key + e - ctx));
+                                x[h][e] = __float_as_uint(v * kLog2e);
+                            }
+                        }
+                        if (edge) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (key + e < lo || key + e > hi) x[h][e] = __float_as_uint(-INFINITY);
+                        }
+                        if (GEN || edge) tc::st32(s_col + c + h * 32, x[h]);
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                            for (int a = 0; a < 4; ++a)
+                                mx[a] = fmax3(mx[a], __uint_as_float(x[h][e + 2 * a]), __uint_as_float(x[h][e + 2 * a + 1]));
+                        top = fmax3(top, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    }
                 }
-                if constexpr (GEN) tc::wait_st();
+                if (GEN || edge) tc::wait_st();
+                if constexpr (!GEN) top *= fac;
                 reanchor = top > m + kLazy;
                 if (reanchor) {
                     alpha = fast_exp2(m - top);
                     m = top;
                 }
-                // P = 2^(x - m): fp32 into the row sum, f16 over columns of S
-                // that have been read (16 of P for 32 of S).
+                // Second pass: P = 2^(x - m), fp32 into the row sum, f16 over
+                // columns of S that have been read (16 of P for 32 of S).
                 const float mu = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 f2 = make_float2(GEN ? 1.f : fac, GEN ? 1.f : fac), nm2 = make_float2(-mu, -mu);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
-                for (int c = 0; c < kBN / 32; ++c) {
-                    uint32_t x[32], pk[16];
-                    if constexpr (GEN) {
-                        tc::ld32(s_col + c * 32, x);
-                        tc::wait_ld();
-                    } else {
-                        scores(c, x);
-                    }
-                    if (EMIT && valid) {
-                        // 32 consecutive floats a thread (the row stride is a
-                        // multiple of 128), whole sectors by 32-byte stores.
-                        float* dst = p.scores + row * p.score_stride + key0 + c * 32;
+                for (int c = 0; c < kBN; c += kCols) {
+                    uint32_t x[kCols / 32][32];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + e),
-                                         "r"(x[e]), "r"(x[e + 1]), "r"(x[e + 2]), "r"(x[e + 3]), "r"(x[e + 4]),
-                                         "r"(x[e + 5]), "r"(x[e + 6]), "r"(x[e + 7])
-                                         : "memory");
-                    }
+                    for (int h = 0; h < kCols / 32; ++h) tc::ld32(s_col + c + h * 32, x[h]);
+                    tc::wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float p0 = fast_exp2(__uint_as_float(x[e]) - mu);
-                        const float p1 = fast_exp2(__uint_as_float(x[e + 1]) - mu);
-                        sum[(e >> 1) & 3] += p0 + p1;
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[e / 2]) : "f"(p1), "f"(p0));
+                    for (int h = 0; h < kCols / 32; ++h) {
+                        if (EMIT && valid) {
+                            // 32 consecutive floats a thread (the row stride is a
+                            // multiple of 128), whole sectors by 32-byte stores.
+                            float* dst = p.scores + row * p.score_stride + key0 + c + h * 32;
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                float y[8];
+#pragma unroll
+                                for (int a = 0; a < 8; ++a)
+                                    y[a] = GEN ? __uint_as_float(x[h][e + a]) : __uint_as_float(x[h][e + a]) * fac;
+                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + e),
+                                             "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]),
+                                             "f"(y[6]), "f"(y[7])
+                                             : "memory");
+                            }
+                        }
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const float2 pr = exp2_pair_f32(
+                                ffma2(make_float2(__uint_as_float(x[h][e]), __uint_as_float(x[h][e + 1])), f2, nm2));
+                            sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], pr);
+                            asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(pk[e / 2]) : "f"(pr.y), "f"(pr.x));
+                        }
+                        tc::st16(s_col + c / 2 + h * 16, pk);
                     }
-                    tc::st16(s_col + c * 16, pk);
                 }
-                l = l * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                const float2 both = fadd2(sum[0], sum[1]);
+                l = l * alpha + (both.x + both.y);
                 tc::wait_st();
             }
             if (live && j > 0 && __any_sync(0xffffffffu, reanchor)) {
