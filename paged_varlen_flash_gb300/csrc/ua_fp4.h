@@ -25,8 +25,12 @@ bool plan_fp4(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4Plan* 
 cudaError_t launch_fp4(const Fp4Plan& plan, const FwdParams& p, cudaStream_t stream);
 
 // Calls with at least this many packed rows per KV head go to the tcgen05
-// kernel (tiles of 128 rows), the others to the register-operand one.
-constexpr int kFp4RowsMin = 33;
+// kernel (tiles of 128 rows), the others to the register-operand one.  Measured
+// (us, register / tcgen05): 16 sequences of 4096 keys, 8 KV heads, d = 128, 16
+// rows 43 / 49, 32 rows 59 / 49, 64 rows 100 / 49; 4 of 30000, 2 heads, d = 256,
+// 16 rows 58 / 78, 32 rows 86 / 80; 32 of 2000, 2 heads, d = 64, 32 rows 24 / 27,
+// 64 rows 31 / 27.
+constexpr int kFp4RowsMin = 25;
 
 struct Fp4RowsPlan {
     int tiles = 1;   // row tiles per (sequence, kv head)

@@ -9,7 +9,7 @@
 // M = 128 rows, P in tensor memory over its own S tile.
 //
 // One CTA per (KV segment, tile of floor(128 / g) positions, KV head, sequence),
-// heaviest tile first.  Roles (14 warps):
+// heaviest tile first.  Roles (15 warps):
 //   warps 0-3   softmax and epilogue: thread r owns row r (tensor-memory lane r);
 //               two passes over the tile's columns, 64 at a time (maximum, then
 //               P), so the code stays small: four roles share each scheduler's
@@ -17,9 +17,11 @@
 //               many cycles per instruction;
 //   warps 4-7   convert the K tiles, warps 8-11 the V tiles, both together Q
 //               before (f16, each row scaled by a power of two into [1, 2));
-//   warp 12     MMA issuer and tensor-memory owner: S(j + 1) goes out before it
-//               waits for P(j), so the tensor pipe works through the softmax;
-//   warp 13     bulk copies of the pages into a ring of 4-bit tiles.
+//   warp 12     QK^T issuer and tensor-memory owner; S(j) waits for P.V(j - 2),
+//               whose P its columns hold;
+//   warp 13     bulk copies of the pages into a ring of 4-bit tiles;
+//   warp 14     P.V issuer.  (One thread issuing both needed 2,500 cycles per
+//               tile for MMAs of 1,024.)
 // Key tiles are 128 keys, at d = 256 64 (shared memory).
 // Tensor memory: S(0), S(1) in columns [0, 256), O in [256, 256 + d).
 #include <algorithm>
@@ -37,8 +39,9 @@ namespace {
 
 using namespace pf;
 
-constexpr int kThreadsR = 448;
-constexpr int kWarpMmaR = 12;
+constexpr int kThreadsR = 480;
+constexpr int kWarpQk = 12;        // also owns tensor memory
+constexpr int kWarpCopy = 13;
 constexpr int kCols = 64;          // columns of S a softmax thread holds at a time
 
 template <int D>
@@ -59,8 +62,8 @@ struct RCfg {
     static constexpr int kOffScale = kOffRawV + kRing * kRaw;   // Q's row scales
     static constexpr int kOffBar = kOffScale + kRows * 4;
     // q_full, {k, v} x {full, empty} [kStages], {k, v} x {raw full, raw empty}
-    // [kRing], s_full[2], p_full[2], o_done[2], drain, never
-    static constexpr int kNumBars = 1 + 4 * kStages + 4 * kRing + 8;
+    // [kRing], s_full[2], p_full[2], o_done[2], drain[2], never
+    static constexpr int kNumBars = 1 + 4 * kStages + 4 * kRing + 9;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kSmem = kOffMisc + 16 + 1024;
     static constexpr int kTmemO = 256;
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
     const uint32_t p_full0 = s_full0 + 16;
     const uint32_t o_done0 = s_full0 + 32;
     const uint32_t drain = s_full0 + 48;
-    const uint32_t never = s_full0 + 56;
+    const uint32_t never = s_full0 + 64;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
     float* q_scale = reinterpret_cast<float*>(smem + C::kOffScale);
@@ -173,11 +176,12 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
             mbar_init(o_done0 + 8 * i, 1);
         }
         mbar_init(drain, 1);
+        mbar_init(drain + 8, 1);
         mbar_init(never, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kWarpMmaR) {
+    if (warp == kWarpQk) {
         tc::tmem_alloc(smem_u32(tmem_slot), kTmemCols);
         tc::tmem_relinquish();
     }
@@ -190,66 +194,69 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
     };
 
     if (warp >= 12) {
-        if (warp == kWarpMmaR) {
-            // ------------------------------ MMA issuer ------------------------------
-            constexpr uint32_t idesc_qk = tc::idesc_f16_f32(kRows, kBN, false, false);
-            constexpr int kNV = D == 64 ? 64 : 128;      // dims per P.V MMA
-            constexpr uint32_t idesc_pv = tc::idesc_f16_f32(kRows, kNV, false, true);
-            const uint32_t sQ = smem_u32(smem + C::kOffQ);
-            auto issue_qk = [&](int j) -> bool {
-                const int stg = j % C::kStages;
-                // Testing hook: the first K wait waits on a barrier that nothing
-                // completes and gives up after stall_ns.
-                if (p.stall && j == 0 &&
-                    !__all_sync(0xffffffffu, wait_or_abort(never, 0, abort_flag, p.err, (uint64_t)p.stall_ns)))
-                    return false;
-                if (!wwait(k_full0 + 8 * stg, (j / C::kStages) & 1)) return false;
-                tc::fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t kst = smem_u32(smem + C::kOffK) + stg * C::kTile;
+        if (warp != kWarpCopy) {
+            // ------------------------- MMA issuers (one thread each) -------------------------
+            // Shared-memory descriptors are bases plus compile-time offsets (the
+            // address field counts 16 bytes).
+            bool ok = true;
+            if (warp == kWarpQk) {
+                constexpr uint32_t idesc = tc::idesc_f16_f32(kRows, kBN, false, false);
+                const uint64_t qd = tc::smem_desc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+                const uint64_t kd = tc::smem_desc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+                ok = wwait(q_full, 0);
+                for (int j = 0; ok && j < n; ++j) {
+                    const int stg = j % C::kStages;
+                    // Testing hook: the first K wait waits on a barrier that
+                    // nothing completes and gives up after stall_ns.
+                    if (p.stall && j == 0 &&
+                        !(ok = __all_sync(0xffffffffu, wait_or_abort(never, 0, abort_flag, p.err, (uint64_t)p.stall_ns))))
+                        break;
+                    if (j >= 2 && !(ok = wwait(o_done0 + 8 * (j & 1), ((j - 2) >> 1) & 1))) break;
+                    if (!(ok = wwait(k_full0 + 8 * stg, (j / C::kStages) & 1))) break;
+                    tc::fence_after_sync();
+                    if (lane == 0) {
+                        const uint64_t kst = kd + stg * (C::kTile >> 4);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const int pn = k >> 2, off = (k & 3) * 32;
-                        tc::mma_bf16(tmem + (j & 1) * 128, tc::smem_desc_sw128(sQ + pn * C::kQPanel + off, 16, 1024),
-                                     tc::smem_desc_sw128(kst + pn * C::kPanel + off, 16, 1024), idesc_qk,
-                                     k > 0 ? 1u : 0u);
+                        for (int k = 0; k < D / 16; ++k)
+                            tc::mma_bf16(tmem + (j & 1) * 128, qd + (k >> 2) * (C::kQPanel >> 4) + (k & 3) * 2,
+                                         kst + (k >> 2) * (C::kPanel >> 4) + (k & 3) * 2, idesc, k > 0 ? 1u : 0u);
+                        tc::commit(s_full0 + 8 * (j & 1));
+                        tc::commit(k_empty0 + 8 * stg);
                     }
-                    tc::commit(s_full0 + 8 * (j & 1));
-                    tc::commit(k_empty0 + 8 * stg);
+                    __syncwarp();
                 }
-                __syncwarp();
-                return true;
-            };
-            bool ok = wwait(q_full, 0) && issue_qk(0);
-            for (int j = 0; ok && j < n; ++j) {
-                // S(j + 1) overwrites P(j - 1), whose P.V this thread issued
-                // before: MMAs of one thread run in issue order.
-                if (j + 1 < n && !(ok = issue_qk(j + 1))) break;
-                const int stg = j % C::kStages;
-                if (!(ok = wwait(p_full0 + 8 * (j & 1), (j >> 1) & 1))) break;
-                if (!(ok = wwait(v_full0 + 8 * stg, (j / C::kStages) & 1))) break;
-                tc::fence_after_sync();
-                if (lane == 0) {
-                    const uint32_t vst = smem_u32(smem + C::kOffV) + stg * C::kTile;
+            } else {
+                constexpr int kNV = D == 64 ? 64 : 128;      // dims per P.V MMA
+                constexpr uint32_t idesc = tc::idesc_f16_f32(kRows, kNV, false, true);
+                const uint64_t vd = tc::smem_desc_sw128(smem_u32(smem + C::kOffV), C::kPanel, 1024);
+                for (int j = 0; ok && j < n; ++j) {
+                    const int stg = j % C::kStages;
+                    if (!(ok = wwait(v_full0 + 8 * stg, (j / C::kStages) & 1))) break;
+                    if (!(ok = wwait(p_full0 + 8 * (j & 1), (j >> 1) & 1))) break;
+                    tc::fence_after_sync();
+                    if (lane == 0) {
+                        const uint64_t vst = vd + stg * (C::kTile >> 4);
 #pragma unroll
-                    for (int k = 0; k < kBN / 16; ++k)
+                        for (int k = 0; k < kBN / 16; ++k)
 #pragma unroll
-                        for (int h = 0; h < D / kNV; ++h)
-                            // A = P from tensor memory (16 keys = 8 columns), B = V
-                            // MN-major, two 64-dim panels.
-                            tc::mma_bf16_ts(tmem + C::kTmemO + h * kNV, tmem + (j & 1) * 128 + k * 8,
-                                            tc::smem_desc_sw128(vst + h * 2 * C::kPanel + k * 16 * 128, C::kPanel, 1024),
-                                            idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
-                    tc::commit(o_done0 + 8 * (j & 1));
-                    tc::commit(v_empty0 + 8 * stg);
+                            for (int h = 0; h < D / kNV; ++h)
+                                // A = P from tensor memory (16 keys = 8 columns), B = V
+                                // MN-major, two 64-dim panels.
+                                tc::mma_bf16_ts(tmem + C::kTmemO + h * kNV, tmem + (j & 1) * 128 + k * 8,
+                                                vst + h * 2 * (C::kPanel >> 4) + k * 128, idesc,
+                                                (j > 0 || k > 0) ? 1u : 0u);
+                        tc::commit(o_done0 + 8 * (j & 1));
+                        tc::commit(v_empty0 + 8 * stg);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
             if (*abort_flag) {
-                // No MMA may still run when tensor memory is freed.
-                if (lane == 0) tc::commit(drain);
+                // No MMA of this thread may still run when tensor memory is freed.
+                const uint32_t dr = drain + (warp == kWarpQk ? 0 : 8);
+                if (lane == 0) tc::commit(dr);
                 __syncwarp();
-                mbar_wait_bounded(drain, 0);
+                mbar_wait_bounded(dr, 0);
             }
         } else {
             // ------------------------------ bulk copies ------------------------------
@@ -586,7 +593,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
 
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == kWarpMmaR) {
+    if (warp == kWarpQk) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, kTmemCols);
     }
@@ -616,11 +623,24 @@ bool plan_fp4_rows(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4R
     if (p.g > kRows || (int64_t)p.g * p.max_seqlen_q < kFp4RowsMin) return false;
     const int ppt = kRows / p.g;
     const int64_t tiles = (p.max_seqlen_q + ppt - 1) / ppt;
-    // Segments of at least 512 keys, as many as give two CTAs per SM.
+    // Segments.  A CTA (one per SM) costs its key tiles plus about seven tiles'
+    // time to start and finish.  The host knows the longest sequence only, so
+    // the number taken is the one whose time is least over two batches: all
+    // that long (whole waves of CTAs), and lengths spread evenly below it
+    // (half the CTAs of every further segment leave at once).
     const int64_t base = (int64_t)p.hk * p.num_seqs * tiles;
-    const int64_t want = (2LL * num_sms + base - 1) / base;
-    const int64_t by_len = std::max<int64_t>(1, p.max_seqlen_k / 512);
-    int64_t splits = std::min<int64_t>(std::min<int64_t>(want, by_len), 64);
+    const int64_t key_tiles = (p.max_seqlen_k + 127) / 128;
+    int64_t splits = 1;
+    double best = 0.;
+    for (int64_t s = 1; s <= std::min<int64_t>(64, std::max<int64_t>(1, key_tiles / 4)); ++s) {
+        const double each = 7. + (double)((key_tiles + s - 1) / s);
+        const double cost = (double)((base * s + num_sms - 1) / num_sms) * each +
+                            std::max(1., (double)(base * (s + 1)) / (2. * num_sms)) * each;
+        if (s == 1 || cost < best) {
+            best = cost;
+            splits = s;
+        }
+    }
     const size_t per_split = fp4_workspace_bytes(p.total_q * p.hq, p.d);
     splits = std::max<int64_t>(1, std::min<int64_t>(splits, (int64_t)(workspace_bytes / per_split)));
     const int64_t per = (p.max_seqlen_k + splits - 1) / splits;
