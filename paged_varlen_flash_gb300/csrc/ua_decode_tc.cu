@@ -741,6 +741,11 @@ void plan_decode_tc(const FwdParams& p, int num_sms, size_t workspace_bytes, Dec
     const int64_t want = (8LL * num_sms + base - 1) / base;
     const int64_t by_len = std::max<int64_t>(1, p.max_seqlen_k / (8 * kBN));
     int splits = (int)std::min<int64_t>(std::min<int64_t>(want, by_len), 64);
+    if (p.scores)
+        // Key weights go through the combine anyway: a small batch is cut down
+        // to one key tile per CTA while SMs are idle (601 keys, 2 KV heads, d =
+        // 64: 19 -> 9 us for the kernel).
+        splits = std::max(splits, (int)std::min<int64_t>(std::min<int64_t>(num_sms / base, p.max_seqlen_k / kBN), 64));
     const size_t per_split = (size_t)p.total_q * p.hq * (p.d + 2) * sizeof(float);
     splits = (int)std::min<size_t>((size_t)splits, per_split ? workspace_bytes / per_split : 1);
     if (splits < 1) splits = 1;

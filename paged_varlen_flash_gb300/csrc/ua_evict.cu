@@ -3,7 +3,7 @@
 // moved to the front of the destination table (move_kernel).
 //
 // Select: a cluster of 1, 2, 4 or 8 CTAs per (sequence, KV head), each with a
-// run of the keys (up to 8192 of them stay in registers; a
+// run of the keys (up to 8192 of them stay in shared memory; a
 // longer run, past 65536 keys, is read again in every pass).  A weight's bits, flipped so that unsigned order is float order,
 // are searched for the m-th largest of the n candidates by three radix passes
 // (11 + 11 + 10 bits) over shared-memory histograms that the cluster's CTAs read
@@ -26,7 +26,7 @@
 namespace ua {
 namespace {
 
-constexpr int kSelKeys = 8192;  // keys a cluster's CTA should have, kept in registers
+constexpr int kSelKeys = 8192;  // keys a cluster's CTA should have, kept in shared memory
 constexpr int kBins = 2048;
 constexpr int kMove = 256;      // threads of move_kernel
 constexpr int kHold = 8;        // 16-byte pieces a move thread holds at a time
@@ -61,15 +61,16 @@ __device__ __forceinline__ void team_sync() {
     else cluster_sync_all();
 }
 
-// Threads: 512 where a CTA works alone (three to four of them share an SM),
-// 1024 in a cluster (few CTAs, each should be quick).
+// Threads: 512 where a CTA works alone (four of them share an SM), 1024 in a
+// cluster (few CTAs, each should be quick).
 template <int CL>
 constexpr int kSelThreads = CL == 1 ? 512 : 1024;
 
 template <int CL>
-__global__ void __launch_bounds__(kSelThreads<CL>) select_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kSelThreads<CL>, CL == 1 ? 4 : 1) select_kernel(const EvictParams p) {
     constexpr int kSel = kSelThreads<CL>;
-    constexpr int kKeep = kSelKeys / kSel;    // weights a thread keeps in registers
+    constexpr int kKeep = kSelKeys / kSel;    // weights a thread holds of a run (or of 8192 keys of it)
+    extern __shared__ float keep[];           // [kSelKeys], weight of key j0 + i at i
     constexpr int kPerBin = kBins / kSel;
     __shared__ uint32_t hist[2][kBins];       // a pass's counts; the next pass's are cleared meanwhile
     __shared__ uint32_t wsum[kSel / 32], counts[kKeep * (kSel / 32) + 1];
@@ -104,13 +105,13 @@ __global__ void __launch_bounds__(kSelThreads<CL>) select_kernel(const EvictPara
     uint32_t thr = 0;                         // found high bits of the threshold
     uint32_t need = m;                        // keys equal to the threshold to take
     const bool cached = run <= kSelKeys;
-    float v[kKeep];                           // weights of keys j0 + q * kSel + tid
+    // A thread reads back only what it wrote itself, keys j0 + q * kSel + tid.
     auto load = [&](int j0) {
+        float v[kKeep];
 #pragma unroll
-        for (int q = 0; q < kKeep; ++q) {
-            const int j = j0 + q * kSel + tid;
-            v[q] = j < hi ? wi[j] : 0.f;
-        }
+        for (int q = 0; q < kKeep; ++q) v[q] = j0 + q * kSel + tid < hi ? wi[j0 + q * kSel + tid] : 0.f;
+#pragma unroll
+        for (int q = 0; q < kKeep; ++q) keep[q * kSel + tid] = v[q];
     };
     if (cached) load(lo);
     for (int i = tid; i < kBins; i += kSel) hist[0][i] = 0;
@@ -124,7 +125,7 @@ __global__ void __launch_bounds__(kSelThreads<CL>) select_kernel(const EvictPara
             if (!cached) load(j0);
 #pragma unroll
             for (int q = 0; q < kKeep; ++q) {
-                const uint32_t k = weight_key(v[q]);
+                const uint32_t k = weight_key(keep[q * kSel + tid]);
                 if (j0 + q * kSel + tid < hi && (pass == 0 || (k >> (shift + bits)) == thr))
                     atomicAdd(&cur[(k >> shift) & ((1u << bits) - 1)], 1u);
             }
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kSelThreads<CL>) select_kernel(const EvictPara
             if (!cached) load(j0);
 #pragma unroll
             for (int q = 0; q < kKeep; ++q) {
-                const uint32_t k = weight_key(v[q]);
+                const uint32_t k = weight_key(keep[q * kSel + tid]);
                 const bool in = j0 + q * kSel + tid < hi;
                 na += in && k > thr;
                 ne += in && k == thr;
@@ -194,7 +195,7 @@ __global__ void __launch_bounds__(kSelThreads<CL>) select_kernel(const EvictPara
         }
     }
     // From here on weights_out may overwrite weights_in; cached weights are in
-    // every thread's hands by now.
+    // shared memory by now.
     team_sync<CL>();
     if constexpr (CL > 1) {
         for (uint32_t q = 0; m > 0 && q < rank; ++q) {
@@ -213,7 +214,7 @@ __global__ void __launch_bounds__(kSelThreads<CL>) select_kernel(const EvictPara
                 // key order; equal and above packed in one word (8192 at most).
 #pragma unroll
                 for (int q = 0; q < kKeep; ++q) {
-                    const uint32_t k = weight_key(v[q]);
+                    const uint32_t k = weight_key(keep[q * kSel + tid]);
                     const bool in = j0 + q * kSel + tid < hi;
                     const unsigned ba = __ballot_sync(0xffffffffu, in && k > thr);
                     const unsigned be = __ballot_sync(0xffffffffu, in && k == thr);
@@ -237,7 +238,7 @@ __global__ void __launch_bounds__(kSelThreads<CL>) select_kernel(const EvictPara
 #pragma unroll
                 for (int q = 0; q < kKeep; ++q) {
                     const int j = j0 + q * kSel + tid;
-                    const uint32_t k = weight_key(v[q]);
+                    const uint32_t k = weight_key(keep[q * kSel + tid]);
                     const bool above = j < hi && k > thr, equal = j < hi && k == thr;
                     const unsigned ba = __ballot_sync(0xffffffffu, above), be = __ballot_sync(0xffffffffu, equal);
                     const uint32_t before = counts[q * (kSel / 32) + warp];
@@ -247,7 +248,7 @@ __global__ void __launch_bounds__(kSelThreads<CL>) select_kernel(const EvictPara
                     if (above || (equal && re < need)) {
                         const uint32_t to = ra + min(re, need);
                         kept[to] = j;
-                        wo[to] = v[q];
+                        wo[to] = keep[q * kSel + tid];
                     }
                 }
                 const uint32_t all = counts[kKeep * (kSel / 32)];
@@ -368,10 +369,13 @@ cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.c.hk * CL), (unsigned)p.c.num_seqs);
     cfg.blockDim = dim3(kSelThreads<CL>);
+    cfg.dynamicSmemBytes = kSelKeys * sizeof(float);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = CL > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, select_kernel<CL>, p);
+    cudaError_t e = cudaFuncSetAttribute(select_kernel<CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)cfg.dynamicSmemBytes);
+    return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, select_kernel<CL>, p);
 }
 
 }  // namespace
