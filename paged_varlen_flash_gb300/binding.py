@@ -143,8 +143,9 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
+        # The current device's stream without a Stream object: 0.6 us a call against 2.9.
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -257,15 +258,23 @@ def cache_shape(num_blocks, num_kv_heads, head_size, block_size, kv_dtype=UA_DTY
 
 def _token_stride(t, name):
     """Elements between the tokens of a [total, H_k, d] tensor whose rows are contiguous."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
         raise ValueError("%s must be [total_q, H_k, d] with contiguous heads" % name)
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+    return stride[0] if shape[0] > 1 else max(stride[0], shape[1] * shape[2])
 
 
 def _weight_stride(t, name):
-    if t.dim() != 3 or t.stride(2) != 1 or t.stride(0) != t.shape[1] * t.stride(1):
-        raise ValueError("%s must be [num_seqs, H_k, n] with evenly spaced rows" % name)
-    return t.stride(1)
+    """Elements between the rows of a [num_seqs, H_k, n] tensor; a dimension of
+    one row has no stride of its own."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3 and stride[2] == 1:
+        if shape[1] > 1:
+            if shape[0] <= 1 or stride[0] == shape[1] * stride[1]:
+                return stride[1]
+        else:
+            return stride[0] if shape[0] > 1 else shape[2]
+    raise ValueError("%s must be [num_seqs, H_k, n] with evenly spaced rows" % name)
 
 
 def ua_forward_host(problem, q_host, k_cache, v_cache, block_table_host, cu_seqlens_q_host,

@@ -106,3 +106,21 @@ def test_entry_points_check_their_handle_first(lib):
                              stream=0) == 1
     assert ua.ua_forward_weights(None, None, None, None, None, None, None, 1, 1, 1, 1, 0, None, None, None,
                                  None, 1, 1.0, None, stream=0) == 1
+
+
+def test_row_strides_are_read_from_the_dimensions_that_have_them():
+    from paged_varlen_flash_gb300.binding import _token_stride, _weight_stride
+    w = torch.zeros(4, 2, 12)
+    assert _weight_stride(w, "w") == 12 and _weight_stride(w[1:, :, :9], "w") == 12
+    assert _weight_stride(torch.zeros(3, 5, 12)[:, 1:2, :10], "w") == 60
+    assert _weight_stride(torch.zeros(1, 1, 12)[:, :, :7], "w") == 7
+    assert _weight_stride(torch.zeros(12).expand(4, 2, 12), "w") == 0    # the call refuses it
+    for bad in (w[:, :1].expand(4, 2, 12), w.transpose(1, 2), w[::2], w[0]):
+        with pytest.raises(ValueError):
+            _weight_stride(bad, "w")
+    x = torch.zeros(6, 4, 64)
+    assert _token_stride(x, "x") == 256 and _token_stride(x[:, :2], "x") == 256
+    assert _token_stride(x[:1, :2], "x") == 256 and _token_stride(x[:, 1:2, :32], "x") == 256
+    for bad in (x[:, ::2], x.transpose(0, 2), x[0]):
+        with pytest.raises(ValueError):
+            _token_stride(bad, "x")
