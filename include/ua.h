@@ -101,7 +101,11 @@ enum {
  * bit), then b rows of d / 16 e4m3 scales, one per 16 consecutive dims.
  * K = code * scale * k_scale, V = code * scale * v_scale; ua_cache_store
  * writes this format, and a (block, KV head) is one contiguous, 16-byte
- * aligned run.  Any d, b, g and S_q; needs path AUTO. */
+ * aligned run.  Any d, b, g and S_q; needs path AUTO and, for ua_forward, the
+ * problem's device to be current (else UA_ERR_INVALID_ARG).  A NaN value
+ * reaches the rows that see its key and no others.  UA_ERR_UNSUPPORTED past
+ * max_seqlen_k = 2^30, g * max_seqlen_q = 2^30, total_q * H_q = 2^32, or 2^31
+ * steps of 32 keys over all (sequence, KV head, tile of 8 or 16 rows). */
 enum { UA_DTYPE_BF16 = 0, UA_DTYPE_FP8_E4M3 = 1, UA_DTYPE_FP4_E2M1 = 2 };
 
 /* Execution path (gfx950 spec section 6: a path whose query-tile grid fills
@@ -249,12 +253,13 @@ ua_status ua_forward_host(ua_problem *p, const void *q_host, const void *k_cache
 ua_status ua_check_device_error(ua_problem *p, void *stream, int32_t *code);
 
 /*
- * Number of kernel launches the most recent ua_forward / ua_forward_host call
- * enqueued (for launch accounting in benchmarks).
+ * Number of kernel launches the most recent ua_forward, ua_forward_host,
+ * ua_forward_topk, ua_forward_weights or ua_cache_* call enqueued (for launch
+ * accounting in benchmarks).
  */
 int32_t ua_last_launch_count(const ua_problem *p);
 
-/* Human-readable name of the execution path the last forward call took. */
+/* Human-readable name of the execution path the last of those calls took. */
 const char *ua_last_path(const ua_problem *p);
 
 /*
@@ -292,7 +297,7 @@ ua_status ua_set_profile_events(ua_problem *p, void *ev_begin, void *ev_end);
  * gives up, the kernel sets UA_DEVERR_TIMEOUT, raises a CTA-wide abort flag so
  * that every role leaves its loop, waits (bounded) for the copies and
  * tensor-core operations it issued, frees its tensor memory and returns.
- * While this hook is enabled, the split, decode tensor-core, two-tile and
+ * While this hook is enabled, the split, decode tensor-core, 4-bit, two-tile and
  * CTA-pair prefill kernels of later forward calls make their first
  * consumer-side K/V data wait wait on a barrier that nothing completes,
  * bounded by limit_ns instead: the wait gives up, the call returns,
@@ -430,7 +435,10 @@ ua_status ua_cache_expand(ua_problem *p, const void *k_cache, const void *v_cach
  * allocates 4 * max_total_q * H_q * (max_blocks_per_seq * b, rounded up to
  * 128) bytes for the scores: size max_total_q for the steps that are weighed
  * (a decode batch, a prompt's last tokens).  Needs g <= 16 on bf16 and fp8
- * caches, and path AUTO (else UA_ERR_UNSUPPORTED).
+ * caches, path AUTO, H_k <= 65535 and max_seqlen_k <= 2^30 (else
+ * UA_ERR_UNSUPPORTED).  `out` is ua_forward's up to rounding; on bf16 and fp8
+ * caches a NaN or infinite V value also reaches the rows of its tile (16 / g
+ * neighbouring positions) that do not see its key.
  */
 ua_status ua_forward_weights(ua_problem *p, const void *q, const void *k_cache,
                              const void *v_cache, const int32_t *block_table,
@@ -462,6 +470,7 @@ ua_status ua_forward_weights(ua_problem *p, const void *q, const void *k_cache,
  *                    ascending, then -1
  *   seqused_out      int32 [num_seqs]: min(S_k, budget); may be seqused_k
  *   budget >= 1, 0 <= recent <= budget, weight_stride >= max_seqlen_k
+ * Needs H_k <= 32767 and max_seqlen_k <= 2^30 (else UA_ERR_UNSUPPORTED).
  * A malformed length keeps nothing (kept -1, seqused_out 0, the cache and the
  * weights as they were; UA_DEVERR_BOUNDS).  Keys whose source or destination
  * block id is out of range are not moved (UA_DEVERR_BLOCK_ID).

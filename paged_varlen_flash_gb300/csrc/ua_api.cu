@@ -493,7 +493,7 @@ ua_status ua_forward(ua_problem* p, const void* q, const void* k_cache, const vo
     const int g = fp.g;
     max_seqlen_k = fp.max_seqlen_k;
 
-    if (d.kv_dtype == UA_DTYPE_FP4_E2M1) return run_fp4(p, &fp, st);
+    if (d.kv_dtype == UA_DTYPE_FP4_E2M1) return on_device(p) ? run_fp4(p, &fp, st) : UA_ERR_INVALID_ARG;
     rs = encode_maps(p, k_cache, v_cache, false);
     if (rs != UA_OK) return rs;
 
@@ -709,7 +709,7 @@ ua_status ua_forward_weights(ua_problem* p, const void* q, const void* k_cache, 
     if (!weights_out || (reinterpret_cast<uintptr_t>(weights_out) & 3u) != 0 ||
         (reinterpret_cast<uintptr_t>(weights_in) & 3u) != 0)
         return UA_ERR_INVALID_ARG;
-    if (d.path != UA_PATH_AUTO) return UA_ERR_UNSUPPORTED;
+    if (d.path != UA_PATH_AUTO || d.num_kv_heads > 65535 || max_seqlen_k > 1 << 30) return UA_ERR_UNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     fp.scores = p->d_scores;
     fp.score_stride = ((int64_t)fp.max_seqlen_k + 127) / 128 * 128;
@@ -833,7 +833,7 @@ ua_status ua_cache_evict(ua_problem* p, void* k_cache, void* v_cache, const int3
         recent < 0 || recent > budget || weight_stride < max_seqlen_k || !on_device(p))
         return UA_ERR_INVALID_ARG;
     if (num_seqs == 0) return UA_OK;
-    if (num_seqs > 65535 || d.num_kv_heads > 32767) return UA_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || d.num_kv_heads > 32767 || max_seqlen_k > 1 << 30) return UA_ERR_UNSUPPORTED;
     if (!k_cache || !v_cache || !block_table || !seqused_k || !weights_in || !weights_out || !kept ||
         !seqused_out || !aligned16(k_cache) || !aligned16(v_cache) ||
         (reinterpret_cast<uintptr_t>(weights_in) & 3u) != 0 ||

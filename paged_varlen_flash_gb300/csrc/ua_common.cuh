@@ -90,6 +90,10 @@ __device__ __forceinline__ uint32_t seq_status(const FwdParams& p, int s, int& s
     return st;
 }
 
+// The m to store beside l.  NaN scores leave m = -inf, which joins take for a
+// segment without keys; m = 0 instead lets the NaN in l and o count.
+__device__ __forceinline__ float stored_max(float m, float l) { return m == -INFINITY && l != l ? 0.f : m; }
+
 // Top-k calls: the list length of query token `token`, or -1 when it lies
 // outside [0, topk_stride] (a malformed list; the token's rows are written as 0).
 __device__ __forceinline__ int topk_length(const FwdParams& p, int64_t token) {

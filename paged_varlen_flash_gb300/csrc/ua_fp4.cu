@@ -543,18 +543,44 @@ fp4_kernel(const FwdParams p) {
             uint8_t* kst = ring + slot * C::kStage;
             uint8_t* vst = kst + C::kOp;
             const int key0 = step_key(i);
-            if (key0 < vis_beg || key0 + kStep > vis_end) {
-                // Keys no row of the tile sees (past the end, before the window):
-                // their V scales become 0, so that whatever the slots hold cannot
-                // reach O (0 * NaN is NaN; codes are always finite).
+            if (key0 < full_lo || key0 + kStep - 1 > full_hi) {
+                // Keys that some row does not see.  Those that no row of the tile
+                // sees (past the end, before the window): their V scales become
+                // 0, so that whatever the slots hold cannot reach O (0 * NaN is
+                // NaN; codes are always finite).  Those that only some rows see:
+                // NaN scales become 0 too, and the rows that see them take the
+                // NaN here.
                 const int key = key0 + lane;
+                uint8_t* sc = vst + scale_0 + (lane >> 4) * scale_kt + (lane & 15) * C::kScaleRow;
+                uint32_t bad = 0;                    // the key's NaN scales, one bit per 16 dims
                 if (key < vis_beg || key >= vis_end) {
-                    uint8_t* sc = vst + scale_0 + (lane >> 4) * scale_kt + (lane & 15) * C::kScaleRow;
 #pragma unroll
                     for (int e = 0; e < C::kScaleRow; e += 4) *reinterpret_cast<uint32_t*>(sc + e) = 0;
                     fence_proxy_async_smem();
+                } else if (key < full_lo || key > full_hi) {
+#pragma unroll 1
+                    for (int e = 0; e < C::kScaleRow; ++e)
+                        if ((sc[e] & 0x7f) == 0x7f) {
+                            sc[e] = 0;
+                            bad |= 1u << e;
+                        }
+                    if (bad) fence_proxy_async_smem();
                 }
                 __syncwarp();
+                for (unsigned some = __ballot_sync(0xffffffffu, bad != 0); some; some &= some - 1) {
+                    const int from = __ffs(some) - 1;
+                    const uint32_t groups = __shfl_sync(0xffffffffu, bad, from);
+#pragma unroll
+                    for (int k = 0; k < C::kKS; ++k) {
+                        if (!(groups >> ((u * (D / 8) + (k >> 2) * 8) >> 4) & 1)) continue;
+#pragma unroll
+                        for (int j = 0; j < NT; ++j)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+                                if (key0 + from >= rlo[j][c] && key0 + from <= rhi[j][c])
+                                    o[k][j][c] = o[k][j][c + 2] = __int_as_float(0x7fffffff);
+                    }
+                }
             }
 
             // S^T = K Q^T for two 16-key tiles.
@@ -760,9 +786,10 @@ fp4_kernel(const FwdParams p) {
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
                 if (8 * j + 2 * t + c >= e_rows) continue;
                 const int64_t row = e_row[j][c];
+                const float2 ml = make_float2(stored_max(m[j][c], v), v);
                 if (e_piece == 0 && u == 0) p.row_pieces[row] = make_int4(e_pieces, e_pieces, e_pieces, e_pieces);
                 if (e_pieces == 1) {
-                    if (EMIT && u == 0) *reinterpret_cast<float2*>(p.part_ml + row * 2) = make_float2(m[j][c], v);
+                    if (EMIT && u == 0) *reinterpret_cast<float2*>(p.part_ml + row * 2) = ml;
                     const float f = row_factor(p, e_head[j][c], m[j][c], v);
                     uint2* dst = reinterpret_cast<uint2*>(p.out + row * D + u * (D / 8));
 #pragma unroll
@@ -772,7 +799,7 @@ fp4_kernel(const FwdParams p) {
                     continue;
                 }
                 const int64_t at = row * p.splits + e_piece;
-                if (u == 0) *reinterpret_cast<float2*>(p.piece_ml + at * 2) = make_float2(m[j][c], v);
+                if (u == 0) *reinterpret_cast<float2*>(p.piece_ml + at * 2) = ml;
 #pragma unroll
                 for (int k = 0; k < C::kKS; k += 2) {
                     const int64_t e = at * D + u * (D / 8) + 2 * k;
@@ -943,7 +970,7 @@ size_t fp4_workspace_bytes(int64_t rows, int d) { return (size_t)rows * (d + 2) 
 bool plan_fp4(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4Plan* plan) {
     *plan = Fp4Plan();
     const int64_t rows = (int64_t)p.g * p.max_seqlen_q;
-    if (rows >= 1 << 30 || p.total_q * p.hq >= int64_t(1) << 32) return false;
+    if (rows >= 1 << 30 || p.max_seqlen_k > 1 << 30 || p.total_q * p.hq >= int64_t(1) << 32) return false;
     plan->rows = rows <= 8 ? 8 : 16;
     // The batch's steps stay below 2^31; no more CTAs than it can have steps.
     const int64_t steps = (p.max_seqlen_k + (int64_t)kStep - 1) / kStep;

@@ -82,6 +82,22 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
         : "memory");
 }
 
+// The dims (one bit per 16) that are NaN in V at keys [lo, hi) of sequence s.
+__device__ __noinline__ uint32_t nan_groups(const FwdParams& p, int s, int hkv, int lo, int hi) {
+    const int scale_row = p.d / 16, b_log2 = 31 - __clz(p.b);
+    const int64_t page_bytes = fp4_page_bytes(p.b, p.d);
+    uint32_t found = 0;
+    for (int key = lo; key < hi; ++key) {
+        const int32_t id = __ldg(p.block_table + (int64_t)s * p.bt_stride + (key >> b_log2));
+        if (id < 0 || (int64_t)id >= p.num_blocks) continue;       // reads as zeros
+        const uint8_t* sc = static_cast<const uint8_t*>(p.v_cache) + ((int64_t)id * p.hk + hkv) * page_bytes +
+                            p.b * (p.d / 2) + (key & (p.b - 1)) * scale_row;
+        for (int e = 0; e < scale_row; ++e)
+            if ((sc[e] & 0x7f) == 0x7f) found |= 1u << e;
+    }
+    return found;
+}
+
 template <int D, bool GEN, bool EMIT>
 __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams p) {
     using C = RCfg<D>;
@@ -139,6 +155,9 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
     }
     const int t_begin = k_beg / kBN;
     const int n = (k_end + kBN - 1) / kBN - t_begin;
+    // Keys every row of the tile sees.
+    const int full_lo = window ? max(0, last + ctx - p.window + 1) : 0;
+    const int full_hi = causal ? min(first + ctx, sk - 1) : sk - 1;
 
     uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     const uint32_t q_full = smem_u32(bar_mem);
@@ -154,6 +173,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
     const uint32_t never = s_full0 + 64;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+    volatile int* nan_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
     float* q_scale = reinterpret_cast<float*>(smem + C::kOffScale);
 
     if (threadIdx.x == 0) {
@@ -179,6 +199,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
         mbar_init(drain + 8, 1);
         mbar_init(never, 1);
         *abort_flag = 0;
+        *nan_flag = 0;
         fence_mbar_init();
     }
     if (warp == kWarpQk) {
@@ -378,15 +399,24 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
             const uint8_t* raw = raw_mem + slot * C::kRaw;
             uint8_t* tile_mem = tiles_mem + stg * C::kTile + (chunk >> 1) * C::kPanel;
             // Keys no row of the tile sees are zeros in V: whatever their slots
-            // hold must not reach O (0 * NaN is NaN).
+            // hold must not reach O (0 * NaN is NaN).  So are NaN scales of keys
+            // that only some rows see; the epilogue gives those rows the NaN.
             const int key0 = (t_begin + j) * kBN;
-            const bool edge = is_v && (key0 < vis_beg || key0 + kBN > vis_end);
+            const bool edge = is_v && (key0 < full_lo || key0 + kBN - 1 > full_hi);
 #pragma unroll 2
             for (int i = 0; i < C::kEach; ++i) {
                 const int k = k0 + i * (128 / C::kChunks);
                 const uint4 c = *reinterpret_cast<const uint4*>(raw + k * (D / 2) + chunk * 16);
                 uint32_t s8 = *reinterpret_cast<const uint16_t*>(raw + kBN * (D / 2) + k * (D / 16) + chunk * 2);
-                if (edge && (key0 + k < vis_beg || key0 + k >= vis_end)) s8 = 0;
+                if (edge && (key0 + k < full_lo || key0 + k > full_hi)) {
+                    if (key0 + k < vis_beg || key0 + k >= vis_end) {
+                        s8 = 0;
+                    } else if ((s8 & 0x7f) == 0x7f || (s8 & 0x7f00) == 0x7f00) {
+                        if ((s8 & 0x7f) == 0x7f) s8 &= 0xff00;
+                        if ((s8 & 0x7f00) == 0x7f00) s8 &= 0xff;
+                        *nan_flag = 1;
+                    }
+                }
                 const uint32_t sc = e4m3x2_to_f16(s8), s0 = splat_lo(sc), s1 = splat_hi(sc);
                 const uint32_t w[4] = {c.x, c.y, c.z, c.w};
                 // Dims 32 chunk .. + 31: four 16-byte units of the row, swizzled.
@@ -413,8 +443,6 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
         const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
         const int hi = causal ? min(pos + ctx, sk - 1) : sk - 1;
         const int lo = window ? max(0, pos + ctx - p.window + 1) : 0;
-        const int full_hi = causal ? min(first + ctx, sk - 1) : sk - 1;   // keys every row sees
-        const int full_lo = window ? max(0, last + ctx - p.window + 1) : 0;
         const bool softcap = GEN && (p.flags & UA_FLAG_SOFTCAP) != 0;
         const bool alibi = GEN && (p.flags & UA_FLAG_ALIBI) != 0;
         const bool qq = GEN && (p.flags & UA_FLAG_QQ_BIAS) != 0;
@@ -543,13 +571,20 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
             mbar_arrive(p_full0 + 8 * (j & 1));
         }
         if (ok) ok = wwait(o_done0 + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1);
+        if (ok) ok = wwait(v_full0 + 8 * ((n - 1) % C::kStages), ((n - 1) / C::kStages) & 1);   // nan_flag
         if (ok && live) {
+            // Dims that are NaN at keys this row sees and others of the tile do not.
+            uint32_t nans = 0;
+            if (valid && *nan_flag) {
+                const int beg = max(lo, t_begin * kBN), end = min(hi + 1, (t_begin + n) * kBN);
+                nans = nan_groups(p, s, hkv, beg, min(end, full_lo)) | nan_groups(p, s, hkv, max(beg, full_hi + 1), end);
+            }
             // tcgen05.ld is warp-collective: every lane of a live warp loads.
             tc::fence_after_sync();
             float f = p.v_scale;
             if (split) {
                 if (valid) {
-                    p.part_ml[(row * p.splits + seg) * 2 + 0] = m;
+                    p.part_ml[(row * p.splits + seg) * 2 + 0] = stored_max(m, l);
                     p.part_ml[(row * p.splits + seg) * 2 + 1] = l;
                 }
             } else {
@@ -575,7 +610,8 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                 tc::wait_ld();
                 if (!valid) continue;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                for (int e = 0; e < 32; ++e)
+                    o[e] = nans >> (2 * c + e / 16) & 1 ? 0x7fffffffu : __float_as_uint(__uint_as_float(o[e]) * f);
                 if (split) {
                     part_store32(p, (row * p.splits + seg) * D + c * 32, o);
                 } else {
@@ -620,7 +656,7 @@ cudaError_t launch_rows_d(const Fp4RowsPlan& plan, const FwdParams& p, cudaStrea
 
 bool plan_fp4_rows(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4RowsPlan* plan) {
     *plan = Fp4RowsPlan();
-    if (p.g > kRows || (int64_t)p.g * p.max_seqlen_q < kFp4RowsMin) return false;
+    if (p.g > kRows || p.max_seqlen_k > 1 << 30 || (int64_t)p.g * p.max_seqlen_q < kFp4RowsMin) return false;
     const int ppt = kRows / p.g;
     const int64_t tiles = (p.max_seqlen_q + ppt - 1) / ppt;
     // Segments.  A CTA (one per SM) costs its key tiles plus about seven tiles'

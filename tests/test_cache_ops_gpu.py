@@ -334,6 +334,128 @@ def test_nan_in_places_no_row_sees_stays_out(nq):
         check_out(bt, got, s, o, a, mag)
 
 
+@pytest.mark.parametrize("d,b,hq,hk,sq,sk,window", [
+    (128, 16, 8, 2, (3, 2), (40, 130), 0), (64, 32, 4, 4, (6, 1), (70, 33), 0), (64, 16, 4, 4, (8, 8), (8, 500), 5),
+    (256, 64, 16, 2, (2, 2), (100, 65), 20), (128, 16, 8, 2, (40, 33), (40, 1500), 0),
+    (256, 64, 4, 2, (90, 20), (200, 150), 30), (64, 32, 8, 1, (70, 9), (70, 300), 0),
+    (128, 64, 2, 2, (200, 150), (900, 150), 100)])
+def test_nan_values_reach_only_the_rows_that_see_them(d, b, hq, hk, sq, sk, window):
+    """NaN in V at keys that the masks hide from some rows of a tile."""
+    bt = Batch(90, "fp4", hq, hk, d, b, sq, sk)
+    marks = []
+    for s in range(2):
+        ctx = sk[s] - sq[s]
+        for j in {sk[s] - 1, ctx + sq[s] // 2, max(0, ctx - window + 2) if window else sk[s] - 1}:
+            h, grp = int(bt.rng.integers(hk)), int(bt.rng.integers(d // 16))
+            bt.vc.raw[int(bt.table[s, j // b]), h, b * (d // 2) + (j % b) * (d // 16) + grp] = 0x7f
+            marks.append((s, j, h, grp))
+    flags = ua.UA_FLAG_CAUSAL | (ua.UA_FLAG_WINDOW if window else 0)
+    p = bt.device().problem(flags | ua.UA_FLAG_KEY_WEIGHTS, window=window)
+    got = p.forward(*bt.args(), flags).double().cpu().numpy()
+    w = torch.zeros(2, hk, max(sk), device="cuda")
+    again = p.forward_weights(*bt.args(), flags, None, w).double().cpu().numpy()
+    assert p.check_device_error() == 0 and bool(torch.isfinite(w).all())
+    for s in range(2):
+        nan = np.zeros((sq[s], hk, d), bool)
+        for t, j, h, grp in marks:
+            pos = np.arange(sq[s]) + sk[s] - sq[s]
+            see = (j <= pos) & ((j > pos - window) if window else True)
+            if t == s:
+                nan[see, h, 16 * grp:16 * grp + 16] = True
+        nan = np.repeat(nan, hq // hk, 1)
+        lo, hi = R.tokens_of(bt.cu, s)
+        keys, vals = (c.rows(bt.table[s], sk[s]) for c in (bt.kc, bt.vc))
+        o, a, _, mag = R.attention(bt.q[lo:hi], keys, np.nan_to_num(vals), bt.scale, window=window)
+        for x in (got, again):
+            np.testing.assert_array_equal(np.isnan(x[lo:hi]), nan)
+            x[lo:hi][nan] = o[nan]
+            check_out(bt, x, s, o, a, mag)
+
+
+@pytest.mark.parametrize("kind,d,sq,sk", [("fp4", 128, (1, 2), (1, 40)), ("fp4", 64, (1, 3), (900, 300)),
+                                          ("fp4", 128, (40, 30), (40, 2000)), ("fp4", 256, (1, 26), (33, 700)),
+                                          ("bf16", 128, (1, 2), (1, 1500)), ("bf16", 64, (4, 1), (4, 40)),
+                                          ("fp8", 128, (1, 3), (300, 3))])
+def test_nan_keys_make_the_rows_that_see_them_nan(kind, d, sq, sk):
+    """A NaN key (the chunk's last, of one KV head) and a segment of nothing but
+    NaN keys: the rows that see one, and their weights, are NaN; others are not."""
+    bt = Batch(95, kind, 4, 2, d, 16, sq, sk)
+    for s, js in ((0, [sk[0] - 1]), (1, range(0, min(256, sk[1])))):
+        for j in js:
+            blk, slot = int(bt.table[s, j // 16]), j % 16
+            if kind == "fp4":
+                bt.kc.raw[blk, 1, 16 * (d // 2) + slot * (d // 16):][:d // 16] = 0x7f
+            else:
+                bt.kc.raw[blk, slot, 1] = 0x7fc0 if kind == "bf16" else 0x7f
+    bt.device()
+    p = bt.problem(ua.UA_FLAG_CAUSAL | ua.UA_FLAG_KEY_WEIGHTS)
+    w = torch.zeros(2, 2, max(sk), device="cuda")
+    out = p.forward_weights(*bt.args(), ua.UA_FLAG_CAUSAL, None, w).float().cpu().numpy()
+    if kind == "fp4":
+        same = p.forward(*bt.args(), ua.UA_FLAG_CAUSAL).float().cpu().numpy()
+        np.testing.assert_array_equal(np.isnan(same), np.isnan(out))
+    assert p.check_device_error() == 0
+    nan = np.zeros(out.shape, bool)
+    nan[sq[0] - 1, 2:] = True
+    nan[sq[0]:, 2:] = True
+    np.testing.assert_array_equal(np.isnan(out), nan)
+    w = w.cpu().numpy()
+    for s in range(2):
+        assert np.isfinite(w[s, 0]).all() and np.isnan(w[s, 1, :sk[s]]).all() and np.isfinite(w[s, 1, sk[s]:]).all()
+
+
+def test_4bit_batch_of_more_sequences_than_one_scan_covers():
+    """1,300 short sequences, some empty, some malformed: the work split takes three rounds."""
+    g = np.random.default_rng(91)
+    n = 1300
+    sk = [int(x) for x in g.integers(1, 70, n)]
+    sq = [int(x) for x in np.minimum(sk, g.integers(0, 3, n))]
+    bt = Batch(92, "fp4", 4, 2, 64, 16, sq, sk, store=False)
+    for s in range(0, n, 37):
+        for j in range(sk[s]):
+            bt.put(s, j)
+    bt.device()
+    bad = [600, 1299]
+    for s in bad:
+        bt.d_sk[s] = 1000
+    p = bt.problem()
+    # Sequences that were not filled hold NaN scales: only the checked ones are finite.
+    out = torch.full_like(bt.d_q, 5.0)
+    got = p.forward(*bt.args(), ua.UA_FLAG_CAUSAL, out=out).double().cpu().numpy()
+    assert p.check_device_error() == ua.UA_DEVERR_BOUNDS
+    for s in range(n):
+        lo, hi = R.tokens_of(bt.cu, s)
+        if s in bad:
+            assert np.all(got[lo:hi] == 0)
+        elif s % 37 == 0 and sq[s]:
+            o, a, _, mag = bt.reference(s)
+            check_out(bt, got, s, o, a, mag)
+        elif sq[s]:
+            assert np.all(np.isnan(got[lo:hi]))
+
+
+def test_two_problems_on_two_streams_do_not_touch_each_other():
+    a = Batch(93, "fp4", 8, 2, 128, 16, (1,) * 8, (900, 20, 300, 1, 64, 512, 33, 700)).device()
+    c = Batch(94, "fp4", 8, 2, 128, 16, (20,) * 3, (700, 20, 100)).device()
+    probs = [bt.problem(ua.UA_FLAG_CAUSAL | ua.UA_FLAG_KEY_WEIGHTS) for bt in (a, c)]
+    ws = [torch.zeros(bt.n, 2, max(bt.sk), device="cuda") for bt in (a, c)]
+    outs = [torch.empty_like(bt.d_q) for bt in (a, c)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, bt, w, o, st in zip(probs, (a, c), ws, outs, streams):
+            p.forward_weights(*bt.args(), ua.UA_FLAG_CAUSAL, None, w, out=o, stream=st)
+    torch.cuda.synchronize()
+    for p, bt, w, o in zip(probs, (a, c), ws, outs):
+        assert p.check_device_error() == 0
+        got, gw = o.double().cpu().numpy(), w.double().cpu().numpy()
+        for s in range(bt.n):
+            want, ab, weights, mag = bt.reference(s)
+            check_out(bt, got, s, want, ab, mag)
+            fresh = weights.reshape(2, 4, bt.sq[s], bt.sk[s]).sum((1, 2))
+            check_weights(gw[s, :, :bt.sk[s]], fresh, fresh, mag, bt.d, 4 * bt.sq[s])
+
+
 @pytest.mark.parametrize("g,sq", [(4, (3, 20)), (4, (3, 4)), (1, (3, 2)), (2, (50, 17))])
 def test_4bit_qq_bias(g, sq):
     bt = Batch(83, "fp4", 2 * g, 2, 128, 16, sq, (90, 20)).device()
