@@ -349,6 +349,8 @@ fp4_kernel(const FwdParams p) {
     const bool softcap = GEN && (p.flags & UA_FLAG_SOFTCAP) != 0;
     const bool alibi = GEN && (p.flags & UA_FLAG_ALIBI) != 0;
     const bool qq = GEN && (p.flags & UA_FLAG_QQ_BIAS) != 0;
+    // The score chain is in log2 units from the products on.
+    const float cap = p.softcap * kLog2e, cap_inv = softcap ? 1.f / p.softcap : kLog2e;
 
     // ---- the piece that is being copied and, from its first step on, computed
     int it = 0;                  // steps this warp has issued in earlier pieces
@@ -504,8 +506,8 @@ fp4_kernel(const FwdParams p) {
                 full_lo = max(full_lo, rlo[j][c]);
                 full_hi = min(full_hi, rhi[j][c]);
                 const float tau = p.scale * p.k_scale * q_scale[r];
-                fac[j][c] = GEN ? tau : tau * kLog2e;
-                slope[j][c] = alibi && r < nrows ? __ldg(p.alibi + head_of(r)) : 0.f;
+                fac[j][c] = tau * (GEN ? cap_inv : kLog2e);
+                slope[j][c] = alibi && r < nrows ? __ldg(p.alibi + head_of(r)) * kLog2e : 0.f;
             }
         full_lo = max(full_lo, __shfl_xor_sync(0xffffffffu, full_lo, 1));
         full_lo = max(full_lo, __shfl_xor_sync(0xffffffffu, full_lo, 2));
@@ -631,11 +633,10 @@ fp4_kernel(const FwdParams p) {
                         float x = sacc[kt][j][c4] * fac[j][c];
                         if constexpr (GEN) {
                             const int key = key0 + kt * 16 + rho(u) + (c4 >> 1) * 8;
-                            if (softcap) x = p.softcap * tanh_from_exp2(x / p.softcap);
+                            if (softcap) x = cap * tanh_from_exp2(x);
                             if (alibi) x += slope[j][c] * (float)(key - ctx);
                             if (qq && key >= ctx && key <= rhi[j][c])
-                                x += __ldg(p.qq_bias + (int64_t)ri[j][c] * p.qq_stride + (key - ctx));
-                            x *= kLog2e;
+                                x += __ldg(p.qq_bias + (int64_t)ri[j][c] * p.qq_stride + (key - ctx)) * kLog2e;
                         }
                         sacc[kt][j][c4] = x;
                     }

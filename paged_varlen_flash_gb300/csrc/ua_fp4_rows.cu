@@ -446,12 +446,13 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
         const bool softcap = GEN && (p.flags & UA_FLAG_SOFTCAP) != 0;
         const bool alibi = GEN && (p.flags & UA_FLAG_ALIBI) != 0;
         const bool qq = GEN && (p.flags & UA_FLAG_QQ_BIAS) != 0;
-        const float slope = alibi && valid ? __ldg(p.alibi + head) : 0.f;
+        const float slope = alibi && valid ? __ldg(p.alibi + head) * kLog2e : 0.f;
         const int64_t row = (q0 + pos) * p.hq + head;
         float m = -INFINITY, l = 0.f;
         bool ok = wwait(q_full, 0);              // q_scale
         const float tau = p.scale * p.k_scale * q_scale[r];
-        const float fac = GEN ? tau : tau * kLog2e;
+        // The score chain is in log2 units from the products on.
+        const float cap = p.softcap * kLog2e, fac = tau * (softcap ? 1.f / p.softcap : kLog2e);
         for (int j = 0; ok && j < n; ++j) {
             if (!(ok = wwait(s_full0 + 8 * (j & 1), (j >> 1) & 1))) break;
             const int key0 = (t_begin + j) * kBN;
@@ -477,12 +478,12 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                         if constexpr (GEN) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
-                                float v = __uint_as_float(x[h][e]) * tau;
-                                if (softcap) v = p.softcap * tanh_from_exp2(v / p.softcap);
+                                float v = __uint_as_float(x[h][e]) * fac;
+                                if (softcap) v = cap * tanh_from_exp2(v);
                                 if (alibi) v += slope * (float)(key + e - ctx);
                                 if (qq && valid && key + e >= ctx && key + e <= hi)
-                                    v += __ldg(p.qq_bias + (int64_t)pos * p.qq_stride + (key + e - ctx));
-                                x[h][e] = __float_as_uint(v * kLog2e);
+                                    v += __ldg(p.qq_bias + (int64_t)pos * p.qq_stride + (key + e - ctx)) * kLog2e;
+                                x[h][e] = __float_as_uint(v);
                             }
                         }
                         if (edge) {
