@@ -3,11 +3,11 @@
 // moved to the front of the destination table (move_kernel).
 //
 // Select: a cluster of 1, 2, 4 or 8 CTAs per (sequence, KV head), each with a
-// run of the keys (up to 8192 of them stay in shared memory; a
-// longer run, past 65536 keys, is read again in every pass).  A weight's bits, flipped so that unsigned order is float order,
-// are searched for the m-th largest of the n candidates by three radix passes
-// (11 + 11 + 10 bits) over shared-memory histograms that the cluster's CTAs read
-// from one another; one pass in key order then writes the kept positions,
+// run of the keys (up to 8192 of them stay in shared memory; a longer run, past
+// 65536 keys, is read again in every pass).  A weight's bits, flipped so that
+// unsigned order is float order, are searched for the m-th largest of the n candidates by three radix passes
+// (11 + 11 + 10 bits) over shared-memory histograms, of which the cluster's CTAs
+// read 32 sums and 64 bins from one another; one pass in key order then writes the kept positions,
 // taking keys above the threshold, the first `need` of those equal to it, and
 // the recent tail.
 //
@@ -48,10 +48,17 @@ __device__ __forceinline__ uint32_t warp_incl_scan(uint32_t v, int lane) {
     return v;
 }
 
-// A 32-bit word of the same shared-memory variable in CTA `rank` of the cluster.
+// A 32-bit word, or two, of the same shared-memory variable in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_word(const uint32_t* local, uint32_t rank) {
     uint32_t v;
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(local), rank)) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ uint2 cluster_pair(const uint2* local, uint32_t rank) {
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(v.x), "=r"(v.y) : "r"(mapa_shared(smem_u32(local), rank)) : "memory");
     return v;
 }
 
@@ -61,19 +68,29 @@ __device__ __forceinline__ void team_sync() {
     else cluster_sync_all();
 }
 
-// Threads: 512 where a CTA works alone (four of them share an SM), 1024 in a
-// cluster (few CTAs, each should be quick).
+// Threads: 512 where a CTA works alone (three share an SM at 40 registers; four,
+// at 32, spill: 199 against 193 us for the 64-request eviction), 1024 in a cluster
+// (few CTAs, each should be quick).
 template <int CL>
 constexpr int kSelThreads = CL == 1 ? 512 : 1024;
 
+// Dynamic shared memory: the run's weights, the histogram, its copy in pairs of
+// bins from the top (in a cluster of two passes: another CTA may still read the
+// last one's).
 template <int CL>
-__global__ void __launch_bounds__(kSelThreads<CL>, CL == 1 ? 4 : 1) select_kernel(const EvictParams p) {
+constexpr int kPairs = CL == 1 ? 1 : 2;
+template <int CL>
+constexpr int kSelSmem = (kSelKeys + kBins) * 4 + kPairs<CL> * (kBins / 2) * 8;
+
+template <int CL>
+__global__ void __launch_bounds__(kSelThreads<CL>, CL == 1 ? 3 : 1) select_kernel(const EvictParams p) {
     constexpr int kSel = kSelThreads<CL>;
     constexpr int kKeep = kSelKeys / kSel;    // weights a thread holds of a run (or of 8192 keys of it)
-    extern __shared__ float keep[];           // [kSelKeys], weight of key j0 + i at i
-    constexpr int kPerBin = kBins / kSel;
-    __shared__ uint32_t hist[2][kBins];       // a pass's counts; the next pass's are cleared meanwhile
-    __shared__ uint32_t wsum[kSel / 32], counts[kKeep * (kSel / 32) + 1];
+    extern __shared__ __align__(16) float keep[];   // [kSelKeys], weight of key j0 + i at i
+    uint32_t* hist = reinterpret_cast<uint32_t*>(keep + kSelKeys);
+    uint2* pairs = reinterpret_cast<uint2*>(hist + kBins);
+    __shared__ uint32_t sums[kPairs<CL>][32];       // of 64 bins each, from the top
+    __shared__ uint32_t counts[kKeep * (kSel / 32) + 1];
     __shared__ uint32_t found[2];
     __shared__ uint32_t mine[2];              // this CTA's keys above and equal to the threshold
     const uint32_t rank = CL == 1 ? 0u : cluster_ctarank();
@@ -114,56 +131,62 @@ __global__ void __launch_bounds__(kSelThreads<CL>, CL == 1 ? 4 : 1) select_kerne
         for (int q = 0; q < kKeep; ++q) keep[q * kSel + tid] = v[q];
     };
     if (cached) load(lo);
-    for (int i = tid; i < kBins; i += kSel) hist[0][i] = 0;
+    for (int i = tid; i < kBins; i += kSel) hist[i] = 0;
     __syncthreads();
 #pragma unroll 1
     for (int pass = 0; pass < 3 && m > 0; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const int bits = pass == 2 ? 10 : 11;
-        uint32_t* cur = hist[pass & 1];
+        uint2* pair = pairs + (pass & (kPairs<CL> - 1)) * (kBins / 2);
+        uint32_t* sum64 = sums[pass & (kPairs<CL> - 1)];
         for (int j0 = lo; j0 < hi; j0 += kSelKeys) {
             if (!cached) load(j0);
-#pragma unroll
+#pragma unroll 4
             for (int q = 0; q < kKeep; ++q) {
                 const uint32_t k = weight_key(keep[q * kSel + tid]);
                 if (j0 + q * kSel + tid < hi && (pass == 0 || (k >> (shift + bits)) == thr))
-                    atomicAdd(&cur[(k >> shift) & ((1u << bits) - 1)], 1u);
+                    atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
             }
+        }
+        __syncthreads();
+        // Bins 2047 - 2 i and 2046 - 2 i are pair i; a warp has 32 of them at a time.
+#pragma unroll
+        for (int i = tid; i < kBins / 2; i += kSel) {
+            const uint2 v = *reinterpret_cast<const uint2*>(hist + kBins - 2 - 2 * i);
+            pair[i] = make_uint2(v.y, v.x);
+            const uint32_t sum = __reduce_add_sync(0xffffffffu, v.x + v.y);
+            if (lane == 0) sum64[i >> 5] = sum;
         }
         team_sync<CL>();
-        // Bins from the top, summed over the cluster: thread t holds kPerBin of
-        // them from bin 2047 - kPerBin * t down.
-        uint32_t cnt[kPerBin] = {}, sum = 0;
+        if (warp == 0) {
+            // Over the cluster: the 64 bins that hold the `need`-th key, then its bin.
+            uint32_t v[CL], sum = 0;
 #pragma unroll
-        for (int q = 0; q < CL; ++q)
+            for (int q = 0; q < CL; ++q) v[q] = CL == 1 ? sum64[lane] : cluster_word(sum64 + lane, q);
 #pragma unroll
-            for (int e = 0; e < kPerBin; ++e) {
-                const uint32_t* bin = cur + kBins - 1 - kPerBin * tid - e;
-                if constexpr (CL == 1) cnt[e] += *bin;
-                else cnt[e] += cluster_word(bin, q);
+            for (int q = 0; q < CL; ++q) sum += v[q];
+            uint32_t incl = warp_incl_scan(sum, lane);
+            const int at = __ffs(__ballot_sync(0xffffffffu, incl >= need)) - 1;
+            const uint32_t over = __shfl_sync(0xffffffffu, incl - sum, at);   // keys in higher bins
+            uint2 w[CL], c = make_uint2(0, 0);
+#pragma unroll
+            for (int q = 0; q < CL; ++q) w[q] = CL == 1 ? pair[at * 32 + lane] : cluster_pair(pair + at * 32 + lane, q);
+#pragma unroll
+            for (int q = 0; q < CL; ++q) {
+                c.x += w[q].x;
+                c.y += w[q].y;
             }
-#pragma unroll
-        for (int e = 0; e < kPerBin; ++e) sum += cnt[e];
-        for (int i = tid; i < kBins; i += kSel) hist[(pass + 1) & 1][i] = 0;
-        const uint32_t incl = warp_incl_scan(sum, lane);
-        if (lane == 31) wsum[warp] = incl;
-        __syncthreads();
-        // Keys in higher bins; every warp scans the warps' sums.
-        const uint32_t warps = warp_incl_scan(lane < kSel / 32 ? wsum[lane] : 0u, lane);
-        uint32_t before = __shfl_sync(0xffffffffu, warps, warp) - wsum[warp] + incl - sum;
-        if (before < need && before + sum >= need) {
-#pragma unroll
-            for (int e = 0; e < kPerBin; ++e) {
-                if (before < need && before + cnt[e] >= need) {
-                    found[0] = (uint32_t)(kBins - 1 - kPerBin * tid - e);
-                    found[1] = need - before;
-                    break;
-                }
-                before += cnt[e];
+            incl = over + warp_incl_scan(c.x + c.y, lane);
+            const int in = __ffs(__ballot_sync(0xffffffffu, incl >= need)) - 1;
+            if (lane == in) {
+                const uint32_t before = incl - c.x - c.y;
+                const bool second = before + c.x < need;
+                found[0] = (uint32_t)(kBins - 1 - 2 * (at * 32 + in) - second);
+                found[1] = need - before - (second ? c.x : 0u);
             }
+        } else if (pass < 2) {
+            for (int i = tid - 32; i < kBins; i += kSel - 32) hist[i] = 0;
         }
-        // Nobody clears or counts into a histogram that another CTA still reads:
-        // `cur` is cleared two passes on, after the next pass's cluster barrier.
         __syncthreads();
         thr = (thr << bits) | found[0];
         need = found[1];
@@ -174,7 +197,7 @@ __global__ void __launch_bounds__(kSelThreads<CL>, CL == 1 ? 4 : 1) select_kerne
         uint32_t na = 0, ne = 0;
         for (int j0 = lo; j0 < hi; j0 += kSelKeys) {
             if (!cached) load(j0);
-#pragma unroll
+#pragma unroll 4
             for (int q = 0; q < kKeep; ++q) {
                 const uint32_t k = weight_key(keep[q * kSel + tid]);
                 const bool in = j0 + q * kSel + tid < hi;
@@ -198,10 +221,12 @@ __global__ void __launch_bounds__(kSelThreads<CL>, CL == 1 ? 4 : 1) select_kerne
     // shared memory by now.
     team_sync<CL>();
     if constexpr (CL > 1) {
-        for (uint32_t q = 0; m > 0 && q < rank; ++q) {
-            above0 += cluster_word(&mine[0], q);
-            equal0 += cluster_word(&mine[1], q);
+        if (m > 0 && lane < (int)rank) {
+            above0 = cluster_word(&mine[0], lane);
+            equal0 = cluster_word(&mine[1], lane);
         }
+        above0 = __reduce_add_sync(0xffffffffu, above0);
+        equal0 = __reduce_add_sync(0xffffffffu, equal0);
     }
     // A CTA writes at or below its own keys, possibly in an earlier CTA's run:
     // where weights are moved in place and read again, the CTAs take turns.
@@ -212,7 +237,7 @@ __global__ void __launch_bounds__(kSelThreads<CL>, CL == 1 ? 4 : 1) select_kerne
                 if (!cached) load(j0);
                 // Counts of every (row of kSel keys, warp), scanned by warp 0 in
                 // key order; equal and above packed in one word (8192 at most).
-#pragma unroll
+#pragma unroll 4
                 for (int q = 0; q < kKeep; ++q) {
                     const uint32_t k = weight_key(keep[q * kSel + tid]);
                     const bool in = j0 + q * kSel + tid < hi;
@@ -235,7 +260,7 @@ __global__ void __launch_bounds__(kSelThreads<CL>, CL == 1 ? 4 : 1) select_kerne
                     if (lane == 31) counts[kKeep * (kSel / 32)] = incl;
                 }
                 __syncthreads();
-#pragma unroll
+#pragma unroll 4
                 for (int q = 0; q < kKeep; ++q) {
                     const int j = j0 + q * kSel + tid;
                     const uint32_t k = weight_key(keep[q * kSel + tid]);
@@ -369,7 +394,7 @@ cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(p.c.hk * CL), (unsigned)p.c.num_seqs);
     cfg.blockDim = dim3(kSelThreads<CL>);
-    cfg.dynamicSmemBytes = kSelKeys * sizeof(float);
+    cfg.dynamicSmemBytes = kSelSmem<CL>;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = CL > 1 ? 1 : 0;
