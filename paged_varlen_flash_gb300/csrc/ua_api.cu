@@ -737,7 +737,10 @@ ua_status ua_forward_weights(ua_problem* p, const void* q, const void* k_cache, 
         if (rs != UA_OK) return rs;
         p->last_path = "decode_tc+combine+weights";
     }
-    const cudaError_t e = ua::launch_weights(fp, weights_in, weights_out, weight_stride, decay, st);
+    const bool again = std::strncmp(p->last_path, "fp4_rows", 8) == 0;
+    const cudaError_t e =
+        again ? ua::launch_fp4_weights(fp, p->num_sms, weights_in, weights_out, weight_stride, decay, st)
+              : ua::launch_weights(fp, weights_in, weights_out, weight_stride, decay, st);
     if (e != cudaSuccess) {
         note_cuda(e, "weights kernel launch");
         return UA_ERR_CUDA;

@@ -60,6 +60,7 @@ struct FwdParams {
     int64_t stall_ns;
     // Key weights: every row's scores in log2 units, masks applied, element
     // (row, key) at row * score_stride + key; null outside ua_forward_weights.
+    // (The tcgen05 kernel over 4-bit caches stores the rows' (m, l) only.)
     float* scores;
     int64_t score_stride;
     // 4-bit caches: (m, l) of every piece of a row (beside its o in part_o), and

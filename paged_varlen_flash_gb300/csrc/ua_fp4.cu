@@ -93,15 +93,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     return h;
 }
 
-// Contiguous copy global -> shared (16-byte aligned, a multiple of 16 bytes),
-// completion signalled on `bar`.
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
-}
-
 // Key of a 16-key tile that MMA key index i < 8 stands for (index i + 8: + 8).
 __device__ __forceinline__ int rho(int i) { return (i & 1) ? ((i >> 1) + 4) ^ 1 : i >> 1; }
 

@@ -42,8 +42,7 @@ struct Fp4RowsPlan {
 bool plan_fp4_rows(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4RowsPlan* plan);
 
 // Enqueue it (p.splits / p.chunk / partial pointers set from the plan).  With
-// p.scores set every row's scores are stored as well and partials are written
-// even for one segment.
+// p.scores set partials are written even for one segment (scores are not).
 cudaError_t launch_fp4_rows(const Fp4RowsPlan& plan, const FwdParams& p, cudaStream_t stream);
 
 }  // namespace ua

@@ -30,6 +30,7 @@
 #include "ua_common.cuh"
 #include "ua_fp4.cuh"
 #include "ua_fp4.h"
+#include "ua_fp4_tiles.cuh"
 #include "ua_prefill_common.cuh"
 #include "ua_ptx.cuh"
 #include "ua_tc.cuh"
@@ -73,15 +74,6 @@ struct RCfg {
     static_assert(kRaw % 16 == 0, "bulk copy alignment");
 };
 
-// Contiguous copy global -> shared (16-byte aligned, a multiple of 16 bytes),
-// completion signalled on `bar`.
-__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(src), "r"(bytes), "r"(bar)
-        : "memory");
-}
-
 // The dims (one bit per 16) that are NaN in V at keys [lo, hi) of sequence s.
 __device__ __noinline__ uint32_t nan_groups(const FwdParams& p, int s, int hkv, int lo, int hi) {
     const int scale_row = p.d / 16, b_log2 = 31 - __clz(p.b);
@@ -98,7 +90,7 @@ __device__ __noinline__ uint32_t nan_groups(const FwdParams& p, int s, int hkv, 
     return found;
 }
 
-template <int D, bool GEN, bool EMIT>
+template <int D, bool GEN>
 __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams p) {
     using C = RCfg<D>;
     constexpr int kBN = C::kBN;
@@ -112,7 +104,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
     const int tiles = (int)(gridDim.x / p.splits);
     const int seg = blockIdx.x % p.splits;
     const int tile = tiles - 1 - blockIdx.x / p.splits;
-    const bool split = EMIT || p.splits > 1;
+    const bool split = p.scores || p.splits > 1;   // key weights read the rows' (m, l)
     const int g = p.g;
     const int ppt = kRows / g;                   // positions per tile
     const int first = tile * ppt;
@@ -323,8 +315,8 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                 __syncwarp();
                 if (good) {
                     const uint8_t* src = cache + (int64_t)id * p.hk * page_bytes;
-                    bulk_copy(smem_u32(codes), src, code_bytes, full0 + 8 * slot);
-                    bulk_copy(smem_u32(scales), src + code_bytes, scale_bytes, full0 + 8 * slot);
+                    bulk_load(smem_u32(codes), src, code_bytes, full0 + 8 * slot);
+                    bulk_load(smem_u32(scales), src + code_bytes, scale_bytes, full0 + 8 * slot);
                 }
                 issued = j + 1;
             }
@@ -338,52 +330,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
         // -------------------------------- converters --------------------------------
         const bool is_v = warp >= 8;
         const int t = threadIdx.x & 127;
-        // Q: eight threads a row, 32 rows per pass, several passes' loads together.
-        constexpr int kPer = D / 8, kPass = D == 256 ? 2 : 4;
-#pragma unroll 1
-        for (int pass = 0; pass < 4; pass += kPass) {
-            uint4 x[kPass][kPer / 8];
-            const int r_0 = pass * 32 + ((threadIdx.x - 128) >> 3), e0 = (t & 7) * kPer;
-#pragma unroll
-            for (int a = 0; a < kPass; ++a) {
-                const int r = r_0 + 32 * a, i = first + r / g;
-                const bool real = r < g * ppt && i <= last;
-#pragma unroll
-                for (int c = 0; c < kPer / 8; ++c)
-                    x[a][c] = real ? __ldg(reinterpret_cast<const uint4*>(
-                                         p.q + ((q0 + i) * p.hq + hkv * g + r % g) * D + e0) + c)
-                                   : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int a = 0; a < kPass; ++a) {
-                const int r = r_0 + 32 * a;
-                uint32_t amax = 0;
-#pragma unroll
-                for (int c = 0; c < kPer / 8; ++c)
-                    amax = __vmaxu2(amax, __vmaxu2(__vmaxu2(x[a][c].x & 0x7fff7fffu, x[a][c].y & 0x7fff7fffu),
-                                                   __vmaxu2(x[a][c].z & 0x7fff7fffu, x[a][c].w & 0x7fff7fffu)));
-                amax = max(amax & 0xffffu, amax >> 16);
-                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-                amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
-                const int ef = (int)(amax >> 7);
-                const int e = (amax == 0 || ef == 255) ? 0 : min(max(ef, 1), 253) - 127;
-                const float down = __int_as_float((127 - e) << 23);
-                if ((t & 7) == 0) q_scale[r] = __int_as_float((127 + e) << 23);
-#pragma unroll
-                for (int c = 0; c < kPer / 8; ++c) {
-                    const uint32_t v[4] = {x[a][c].x, x[a][c].y, x[a][c].z, x[a][c].w};
-                    uint32_t h[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-                            : "=r"(h[k]) : "f"(bf16_hi(v[k]) * down), "f"(bf16_lo(v[k]) * down));
-                    const int dim = e0 + c * 8;
-                    *reinterpret_cast<uint4*>(smem + C::kOffQ + (dim >> 6) * C::kQPanel + r * 128 +
-                                              ((((dim & 63) >> 3) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                }
-            }
-        }
+        stage_q<D, 256, D == 256 ? 2 : 4>(p, TileRows{q0, hkv, g, first, last}, threadIdx.x - 128, smem + C::kOffQ, q_scale);
         fence_proxy_async_smem();
         mbar_arrive(q_full);
         const uint32_t full0 = is_v ? v_full0 : k_full0, empty0 = is_v ? v_empty0 : k_empty0;
@@ -417,17 +364,7 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                         *nan_flag = 1;
                     }
                 }
-                const uint32_t sc = e4m3x2_to_f16(s8), s0 = splat_lo(sc), s1 = splat_hi(sc);
-                const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-                // Dims 32 chunk .. + 31: four 16-byte units of the row, swizzled.
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t h[4];
-                    e2m1x8_to_f16(w[q], h);
-                    const uint32_t f = q < 2 ? s0 : s1;
-                    *reinterpret_cast<uint4*>(tile_mem + k * 128 + ((((chunk & 1) * 4 + q) ^ (k & 7)) << 4)) =
-                        make_uint4(mul_f16x2(h[0], f), mul_f16x2(h[1], f), mul_f16x2(h[2], f), mul_f16x2(h[3], f));
-                }
+                stage_codes(c, s8, chunk, k, tile_mem);
             }
             fence_proxy_async_smem();
             mbar_arrive(full0 + 8 * stg);
@@ -521,22 +458,6 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                     tc::wait_ld();
 #pragma unroll
                     for (int h = 0; h < kCols / 32; ++h) {
-                        if (EMIT && valid) {
-                            // 32 consecutive floats a thread (the row stride is a
-                            // multiple of 128), whole sectors by 32-byte stores.
-                            float* dst = p.scores + row * p.score_stride + key0 + c + h * 32;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8) {
-                                float y[8];
-#pragma unroll
-                                for (int a = 0; a < 8; ++a)
-                                    y[a] = GEN ? __uint_as_float(x[h][e + a]) : __uint_as_float(x[h][e + a]) * fac;
-                                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + e),
-                                             "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]),
-                                             "f"(y[6]), "f"(y[7])
-                                             : "memory");
-                            }
-                        }
                         uint32_t pk[16];
 #pragma unroll
                         for (int e = 0; e < 32; e += 2) {
@@ -636,21 +557,15 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
     }
 }
 
-template <int D, bool GEN, bool EMIT>
-cudaError_t launch_rows_t(const Fp4RowsPlan& plan, const FwdParams& p, cudaStream_t stream) {
-    auto kern = fp4_rows_kernel<D, GEN, EMIT>;
+template <int D>
+cudaError_t launch_rows_d(const Fp4RowsPlan& plan, const FwdParams& p, cudaStream_t stream) {
+    const bool gen = (p.flags & (UA_FLAG_SOFTCAP | UA_FLAG_ALIBI | UA_FLAG_QQ_BIAS)) != 0;
+    auto kern = gen ? fp4_rows_kernel<D, true> : fp4_rows_kernel<D, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)(plan.tiles * plan.splits), (unsigned)p.hk, (unsigned)p.num_seqs);
     kern<<<grid, kThreadsR, RCfg<D>::kSmem, stream>>>(p);
     return cudaGetLastError();
-}
-
-template <int D>
-cudaError_t launch_rows_d(const Fp4RowsPlan& plan, const FwdParams& p, cudaStream_t stream) {
-    const bool gen = (p.flags & (UA_FLAG_SOFTCAP | UA_FLAG_ALIBI | UA_FLAG_QQ_BIAS)) != 0;
-    if (p.scores) return gen ? launch_rows_t<D, true, true>(plan, p, stream) : launch_rows_t<D, false, true>(plan, p, stream);
-    return gen ? launch_rows_t<D, true, false>(plan, p, stream) : launch_rows_t<D, false, false>(plan, p, stream);
 }
 
 }  // namespace

@@ -240,4 +240,13 @@ __device__ __forceinline__ float tanh_from_exp2(float x) {
     return 1.0f - __fdividef(2.0f, e + 1.0f);
 }
 
+// Contiguous copy global -> shared (16-byte aligned, a multiple of 16 bytes),
+// completion signalled on `bar`.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
 }  // namespace ua

@@ -6,7 +6,9 @@
 // is 2^(x_j - M - log2 L); a thread owns four keys of one (sequence, KV head)
 // and adds those of all its rows in row order: no atomics, one order.  Scores
 // instead of a second Q K^T: 8 g bytes per (key, KV head) against the 2 d bytes
-// of the key's row.
+// of the key's row, a few rows per KV head at a decode step (64 requests, 250 us
+// with the attention, of which 40 here and in the joins).  Calls of many rows over
+// a 4-bit cache compute the scores again: ua_fp4_weights.cu.
 #include <cstdint>
 
 #include "ua_common.cuh"
@@ -46,31 +48,15 @@ weights_kernel(const FwdParams p, const float* in_w, float* out_w, int64_t strid
             const int r = (int)(r0 + threadIdx.x), i = r / g;
             const int h = hkv * g + r % g;
             const int64_t row = (q0 + i) * p.hq + h;
-            const float* ml = p.part_ml + row * p.splits * 2;
-            float M = -INFINITY, L = 0.f;
-            for (int k = 0; k < n; ++k) M = fmaxf(M, ml[2 * k]);
-            if (M != -INFINITY)
-                for (int k = 0; k < n; ++k) L = fmaf(fast_exp2(ml[2 * k] - M), ml[2 * k + 1], L);
-            if (p.flags & UA_FLAG_SINKS) {
-                const float s2 = __ldg(p.sinks + h) * kLog2e;
-                if (s2 == INFINITY) {
-                    L = INFINITY;                 // the sink takes the whole row
-                } else if (s2 > M) {
-                    L = (M == -INFINITY ? 0.f : L * fast_exp2(M - s2)) + 1.f;
-                    M = s2;
-                } else if (s2 != -INFINITY) {
-                    L += fast_exp2(s2 - M);
-                }
-            }
-            lse[threadIdx.x] = (M == -INFINITY || L == INFINITY || L == 0.f) ? INFINITY : M + log2f(L);
+            lse[threadIdx.x] = row_lse(p, row, h, n);
             hi[threadIdx.x] = causal ? min(i + ctx, sk - 1) : sk - 1;
             lo[threadIdx.x] = window ? max(0, i + ctx - p.window + 1) : 0;
             at_row[threadIdx.x] = row * p.score_stride;
         }
         __syncthreads();
         if (key >= sk) continue;
-        // Eight rows' loads in flight (many rows: 79 -> 43 us on the observation
-        // window batch).  Scores are stored for the keys a row sees (and masked
+        // Eight rows' loads in flight (32 to 128 rows per KV head, 8 sequences of
+        // 1000 to 12000 keys: 79 -> 43 us).  Scores are stored for the keys a row sees (and masked
         // ones of the same step); the padded row stride keeps a load of four in
         // bounds.
         for (int k0 = 0; k0 < nb; k0 += kAhead) {

@@ -2,6 +2,7 @@
 #pragma once
 
 #include "ua_common.cuh"
+#include "ua_ptx.cuh"
 
 namespace ua {
 
@@ -10,5 +11,44 @@ namespace ua {
 // null (zeros) or out_w itself; rows of `stride` floats per (sequence, KV head).
 cudaError_t launch_weights(const FwdParams& p, const float* in_w, float* out_w, int64_t stride, float decay,
                            cudaStream_t stream);
+
+// The same for a 4-bit cache and calls of the tcgen05 attention kernel: scores
+// are computed again (p.scores is not read).
+cudaError_t launch_fp4_weights(const FwdParams& p, int num_sms, const float* in_w, float* out_w, int64_t stride,
+                               float decay, cudaStream_t stream);
+
+// log2 of the denominator of a row (query head h) from its n segments' (m, l),
+// the sink joined like a key: 2^(x - lse) is the weight of a key with score x.
+// +inf for a row without weight.
+__device__ __forceinline__ float row_lse(const FwdParams& p, int64_t row, int h, int n) {
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row * p.splits;
+    float M = -INFINITY, L = 0.f;
+    for (int k0 = 0; k0 < n; k0 += 8) {          // eight loads in flight
+        float2 v[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) v[q] = ml[min(k0 + q, n - 1)];
+        float top = M;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) top = fmaxf(top, v[q].x);
+        if (top == -INFINITY) continue;
+        L *= fast_exp2(M - top);
+        M = top;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (k0 + q < n) L = fmaf(fast_exp2(v[q].x - M), v[q].y, L);
+    }
+    if (p.flags & UA_FLAG_SINKS) {
+        const float s2 = __ldg(p.sinks + h) * kLog2e;
+        if (s2 == INFINITY) {
+            L = INFINITY;                 // the sink takes the whole row
+        } else if (s2 > M) {
+            L = (M == -INFINITY ? 0.f : L * fast_exp2(M - s2)) + 1.f;
+            M = s2;
+        } else if (s2 != -INFINITY) {
+            L += fast_exp2(s2 - M);
+        }
+    }
+    return M == -INFINITY || L == INFINITY || L == 0.f ? INFINITY : M + log2f(L);
+}
 
 }  // namespace ua
