@@ -21,22 +21,11 @@ cudaError_t launch_fp4_weights(const FwdParams& p, int num_sms, const float* in_
 // the sink joined like a key: 2^(x - lse) is the weight of a key with score x.
 // +inf for a row without weight.
 __device__ __forceinline__ float row_lse(const FwdParams& p, int64_t row, int h, int n) {
-    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + row * p.splits;
+    const float* ml = p.part_ml + row * p.splits * 2;
     float M = -INFINITY, L = 0.f;
-    for (int k0 = 0; k0 < n; k0 += 8) {          // eight loads in flight
-        float2 v[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) v[q] = ml[min(k0 + q, n - 1)];
-        float top = M;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) top = fmaxf(top, v[q].x);
-        if (top == -INFINITY) continue;
-        L *= fast_exp2(M - top);
-        M = top;
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            if (k0 + q < n) L = fmaf(fast_exp2(v[q].x - M), v[q].y, L);
-    }
+    for (int k = 0; k < n; ++k) M = fmaxf(M, ml[2 * k]);
+    if (M != -INFINITY)
+        for (int k = 0; k < n; ++k) L = fmaf(fast_exp2(ml[2 * k] - M), ml[2 * k + 1], L);
     if (p.flags & UA_FLAG_SINKS) {
         const float s2 = __ldg(p.sinks + h) * kLog2e;
         if (s2 == INFINITY) {
