@@ -103,7 +103,9 @@ enum {
  * writes this format, and a (block, KV head) is one contiguous, 16-byte
  * aligned run.  Any d, b, g and S_q; needs path AUTO and, for ua_forward, the
  * problem's device to be current (else UA_ERR_INVALID_ARG).  A NaN value
- * reaches the rows that see its key and no others.  UA_ERR_UNSUPPORTED past
+ * reaches the rows that see its key and no others.  The problem's workspace
+ * holds two partials of every row at least: 8 * max_total_q * H_q * (d + 2)
+ * bytes.  UA_ERR_UNSUPPORTED past
  * max_seqlen_k = 2^30, g * max_seqlen_q = 2^30, total_q * H_q = 2^32, or 2^31
  * steps of 32 keys over all (sequence, KV head, tile of 8 or 16 rows). */
 enum { UA_DTYPE_BF16 = 0, UA_DTYPE_FP8_E4M3 = 1, UA_DTYPE_FP4_E2M1 = 2 };

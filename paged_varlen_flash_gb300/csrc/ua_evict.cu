@@ -16,6 +16,11 @@
 // loads per thread in flight before the first store.  A kept key's new position is never
 // behind its old one, so in place a CTA that walks the ranks in order and has
 // read a whole round before it writes any of it overwrites nothing unread.
+//
+// Measured: 512 heads of up to 8191 weights 24 us (a CTA each), 8 heads of up to
+// 65535 14.5 us (clusters of eight; a pass is 1 us of counting and 1.3 of barrier
+// and exchange); moving 2048 bf16 rows of each of the 512 163 us, 6.3 TB/s of reads
+// and writes.
 #include <algorithm>
 #include <cstdint>
 

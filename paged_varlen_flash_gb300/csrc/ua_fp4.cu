@@ -22,6 +22,14 @@
 // boundary cuts has several pieces; each leaves (m, l, o) in the workspace and
 // merge_kernel joins them in piece order.
 //
+// Measured: the 64-request decode batch (270 k keys, 32 / 8 heads, d = 128, 346 MB)
+// takes 78 us and 82 per call with the merge, 4.2 TB/s.  The copies alone take
+// about 80: 20 us to start, to drain unevenly and to merge, then 6.4 TB/s; the
+// instructions (360 per warp and 16 keys: K about 107, V 134) fill 58 % of the
+// issue slots of the 12 warps that 162 registers leave an SM.  Four CTAs per SM
+// were slower (115 us against 104 then), and so was claiming the last quarter of
+// the steps dynamically (124 against 86: a change of piece waits 4 us).
+//
 // Lane layout (lane = 4 * u + t, u < 8, t < 4; "key index" i < 16 of a 16-key
 // MMA tile is key rho(i) of it):
 //   K: lane (u, t) holds key indexes u and u + 8 and a quarter of the dims;

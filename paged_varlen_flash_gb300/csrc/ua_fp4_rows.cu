@@ -23,6 +23,12 @@
 //   warp 14     P.V issuer.  (One thread issuing both needed 2,500 cycles per
 //               tile for MMAs of 1,024.)
 // Key tiles are 128 keys, at d = 256 64 (shared memory).
+//
+// Measured: 1.55 us per tile of 128 x 128 at d = 128 (MMAs alone 0.52), the chain
+// convert -> QK^T -> softmax -> P.V; 16 sequences of 4096 keys and 8 KV heads, 64
+// rows each, 49 us; 8 of 1000 to 12000 keys, 67 us, of which a third is a tail of
+// CTAs with longer sequences than the others'.  Codes held in registers by the
+// converters instead of the staged ring: 106 to 128 us for the latter.
 // Tensor memory: S(0), S(1) in columns [0, 256), O in [256, 256 + d).
 #include <algorithm>
 #include <cstdint>

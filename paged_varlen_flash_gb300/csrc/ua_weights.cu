@@ -7,7 +7,7 @@
 // and adds those of all its rows in row order: no atomics, one order.  Scores
 // instead of a second Q K^T: 8 g bytes per (key, KV head) against the 2 d bytes
 // of the key's row, a few rows per KV head at a decode step (64 requests, 250 us
-// with the attention, of which 40 here and in the joins).  Calls of many rows over
+// with the attention, of which 21 here and 6 in the join).  Calls of many rows over
 // a 4-bit cache compute the scores again: ua_fp4_weights.cu.
 #include <cstdint>
 
