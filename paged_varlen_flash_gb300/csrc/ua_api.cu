@@ -740,7 +740,8 @@ ua_status ua_forward_weights(ua_problem* p, const void* q, const void* k_cache, 
     const bool again = std::strncmp(p->last_path, "fp4_rows", 8) == 0;
     const cudaError_t e =
         again ? ua::launch_fp4_weights(fp, p->num_sms, weights_in, weights_out, weight_stride, decay, st)
-              : ua::launch_weights(fp, weights_in, weights_out, weight_stride, decay, st);
+              : ua::launch_weights(fp, weights_in, weights_out, weight_stride, decay,
+                                   d.kv_dtype == UA_DTYPE_FP4_E2M1, st);
     if (e != cudaSuccess) {
         note_cuda(e, "weights kernel launch");
         return UA_ERR_CUDA;

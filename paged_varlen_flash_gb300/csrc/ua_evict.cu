@@ -26,6 +26,7 @@
 
 #include "ua_cache.h"
 #include "ua_fp4.cuh"
+#include "ua_launch.h"
 #include "ua_ptx.cuh"
 
 namespace ua {
@@ -102,6 +103,7 @@ __global__ void __launch_bounds__(kSelThreads<CL>, CL == 1 ? 3 : 1) select_kerne
     const int h = blockIdx.x / CL, s = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const CacheParams& c = p.c;
+    griddep_launch();
     const int sk = __ldg(c.seqused_k + s);
     const int64_t head = (int64_t)s * c.hk + h;
     int32_t* kept = p.kept + head * p.budget;
@@ -331,6 +333,7 @@ __global__ void __launch_bounds__(kMove, 3) move_kernel(const EvictParams p, int
     const int sl = (blockIdx.x >> 1) % slices, run = (blockIdx.x >> 1) / slices;
     const int h = blockIdx.y, s = blockIdx.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    griddep_wait();
     const int32_t* kept = p.kept + ((int64_t)s * c.hk + h) * p.budget;
     const int32_t* src_table = c.block_table + (int64_t)s * c.bt_stride;
     const int32_t* dst_table = p.dst_table + (int64_t)s * c.bt_stride;
@@ -340,12 +343,12 @@ __global__ void __launch_bounds__(kMove, 3) move_kernel(const EvictParams p, int
     const int b_log2 = 31 - __clz(c.b);
     const bool fp4 = c.kv_dtype == UA_DTYPE_FP4_E2M1;
     for (int64_t r0 = (int64_t)run * kRanks; r0 < p.budget; r0 += kRanks) {
-        if (__ldg(kept + r0) < 0) break;
+        if (kept[r0] < 0) break;
         // Lane = rank: the row's old and new place; j < 0: nothing to move.
         const int64_t r = r0 + warp * 32 + lane;
-        int32_t j = r < p.budget ? __ldg(kept + r) : -1, sb = -1, db = -1;
+        int32_t j = r < p.budget ? kept[r] : -1, sb = -1, db = -1;
         if (j >= 0) {
-            if (h == 0 && !v && sl == 0 && (r + 1 == p.budget || __ldg(kept + r + 1) < 0)) p.seqused_out[s] = (int)r + 1;
+            if (h == 0 && !v && sl == 0 && (r + 1 == p.budget || kept[r + 1] < 0)) p.seqused_out[s] = (int)r + 1;
             if (p.in_place && j == r) {
                 j = -1;                       // already there
             } else {
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(kMove, 3) move_kernel(const EvictParams p, int
         }
         if (!p.in_place) break;               // one round per run
     }
-    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0 && __ldg(kept) < 0) p.seqused_out[s] = 0;
+    if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0 && kept[0] < 0) p.seqused_out[s] = 0;
 }
 
 template <int CL>
@@ -434,8 +437,7 @@ cudaError_t launch_evict(const EvictParams& p, int num_sms, cudaStream_t stream)
     const int64_t n = std::max(1, std::min(p.budget, p.max_seqlen_k));
     const int64_t runs = p.in_place ? 1 : (n + kRanks - 1) / kRanks;
     dim3 grid((unsigned)(runs * slices * 2), (unsigned)c.hk, (unsigned)c.num_seqs);
-    move_kernel<<<grid, kMove, 0, stream>>>(p, pieces, slice);
-    return cudaGetLastError();
+    return launch_early(move_kernel, grid, kMove, 0, stream, p, pieces, slice);
 }
 
 }  // namespace ua

@@ -51,6 +51,7 @@
 #include "ua_common.cuh"
 #include "ua_fp4.cuh"
 #include "ua_fp4.h"
+#include "ua_launch.h"
 #include "ua_ptx.cuh"
 
 namespace ua {
@@ -932,18 +933,10 @@ cudaError_t launch_t(const Fp4Plan& plan, const FwdParams& p, cudaStream_t strea
     if (e != cudaSuccess) return e;
     // The merge may be scheduled while the last pieces finish; it waits for
     // them (griddep_wait) before it reads anything.
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg{};
     const int64_t rows = p.total_q * p.hq;
     const bool team = rows <= kTeamRows;
-    cfg.gridDim = dim3((unsigned)(team ? rows * (D / 64) : (rows + 7) / 8));
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, team ? merge_kernel<D, EMIT, true> : merge_kernel<D, EMIT, false>, p);
+    const dim3 grid((unsigned)(team ? rows * (D / 64) : (rows + 7) / 8));
+    return launch_early(team ? merge_kernel<D, EMIT, true> : merge_kernel<D, EMIT, false>, grid, 256, 0, stream, p);
 }
 
 template <int D>

@@ -32,6 +32,7 @@
 #include "ua_fp4.cuh"
 #include "ua_fp4.h"
 #include "ua_fp4_tiles.cuh"
+#include "ua_launch.h"
 #include "ua_prefill_common.cuh"
 #include "ua_ptx.cuh"
 #include "ua_tc.cuh"
@@ -463,6 +464,7 @@ fp4_weights_kernel(const FwdParams p, const float* in_w, float* out_w, int64_t s
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 256);
     }
+    griddep_wait();                          // runs beside the combine, and ends after it
 }
 
 template <int D>
@@ -474,8 +476,7 @@ cudaError_t launch_key_weights(const FwdParams& p, int num_sms, const float* in_
     if (e != cudaSuccess) return e;
     const double tiles = (double)((p.max_seqlen_k + kKeysW - 1) / kKeysW) * p.hk * p.num_seqs;
     const int ctas = (int)std::max(1., std::min(tiles, (double)num_sms * KCfg<D>::kCtas));
-    kern<<<(unsigned)ctas, kThreadsW, KCfg<D>::kSmem, stream>>>(p, in_w, out_w, stride, decay);
-    return cudaGetLastError();
+    return launch_early(kern, dim3((unsigned)ctas), kThreadsW, KCfg<D>::kSmem, stream, p, in_w, out_w, stride, decay);
 }
 
 }  // namespace

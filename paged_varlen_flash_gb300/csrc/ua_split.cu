@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const FwdParams p) {
     constexpr int DPL = D / 32;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
+    griddep_launch();                        // a key-weight kernel may run beside this one
     if (row >= p.total_q * p.hq) return;
     const int64_t token = row / p.hq;
     const int h = (int)(row % p.hq);

@@ -12,6 +12,7 @@
 #include <cstdint>
 
 #include "ua_common.cuh"
+#include "ua_launch.h"
 #include "ua_ptx.cuh"
 #include "ua_weights.h"
 
@@ -24,16 +25,22 @@ constexpr int kAhead = 8;             // rows loaded ahead
 constexpr int kBatch = 64;            // rows whose constants are in shared memory at a time
 
 __global__ void __launch_bounds__(kThreads)
-weights_kernel(const FwdParams p, const float* in_w, float* out_w, int64_t stride, float decay) {
+weights_kernel(const FwdParams p, const float* in_w, float* out_w, int64_t stride, float decay, bool merged) {
     __shared__ float lse[kBatch];         // log2 of the row's denominator; +inf: a row without weight
     __shared__ int lo[kBatch], hi[kBatch];
     __shared__ int64_t at_row[kBatch];
     const int s = blockIdx.z, hkv = blockIdx.y;
+    // After the merge kernel, which writes the statistics, or beside the combine
+    // kernel, which only reads them.
+    if (merged) griddep_wait();
     int sq, sk;
     int64_t q0;
     const uint32_t st = seq_status(p, s, sq, sk, q0);
     const int64_t first = (int64_t)blockIdx.x * kKeys;
-    if (st || sq <= 0 || first >= sk) return;
+    if (st || sq <= 0 || first >= sk) {
+        griddep_wait();
+        return;
+    }
     const int key = (int)first + threadIdx.x * 4;
     const int ctx = sk - sq, g = p.g;
     const int n = seq_segments(p, st, sk);
@@ -85,15 +92,15 @@ weights_kernel(const FwdParams p, const float* in_w, float* out_w, int64_t strid
         if (in_w && decay != 0.f && key + e < ctx) w[e] = fmaf(decay, in_w[at + e], w[e]);
         out_w[at + e] = w[e];
     }
+    griddep_wait();
 }
 
 }  // namespace
 
 cudaError_t launch_weights(const FwdParams& p, const float* in_w, float* out_w, int64_t stride, float decay,
-                           cudaStream_t stream) {
+                           bool merged, cudaStream_t stream) {
     dim3 grid((unsigned)((p.max_seqlen_k + (int64_t)kKeys - 1) / kKeys), (unsigned)p.hk, (unsigned)p.num_seqs);
-    weights_kernel<<<grid, kThreads, 0, stream>>>(p, in_w, out_w, stride, decay);
-    return cudaGetLastError();
+    return launch_early(weights_kernel, grid, kThreads, 0, stream, p, in_w, out_w, stride, decay, merged);
 }
 
 }  // namespace ua

@@ -9,11 +9,12 @@ namespace ua {
 // out_w = decay * in_w (keys of the context) + the rows' softmax weights, from
 // the scores in p.scores and the segment statistics in p.part_ml.  in_w may be
 // null (zeros) or out_w itself; rows of `stride` floats per (sequence, KV head).
+// Runs beside the combine kernel in front of it or, `merged`, after the merge kernel.
 cudaError_t launch_weights(const FwdParams& p, const float* in_w, float* out_w, int64_t stride, float decay,
-                           cudaStream_t stream);
+                           bool merged, cudaStream_t stream);
 
 // The same for a 4-bit cache and calls of the tcgen05 attention kernel: scores
-// are computed again (p.scores is not read).
+// are computed again (p.scores is not read).  Runs beside the combine kernel.
 cudaError_t launch_fp4_weights(const FwdParams& p, int num_sms, const float* in_w, float* out_w, int64_t stride,
                                float decay, cudaStream_t stream);
 
