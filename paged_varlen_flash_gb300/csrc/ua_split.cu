@@ -18,6 +18,7 @@
 #include <cstdint>
 
 #include "ua_common.cuh"
+#include "ua_launch.h"
 #include "ua_ptx.cuh"
 #include "ua_split.h"
 
@@ -398,6 +399,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const FwdParams p) {
     constexpr int DPL = D / 32;
     const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
+    griddep_wait();                          // the partials are complete
     griddep_launch();                        // a key-weight kernel may run beside this one
     if (row >= p.total_q * p.hq) return;
     const int64_t token = row / p.hq;
@@ -527,12 +529,11 @@ cudaError_t launch_combine(const FwdParams& p, cudaStream_t stream) {
     const unsigned blocks = (unsigned)((rows + 7) / 8);
     if (blocks == 0) return cudaSuccess;
     switch (p.d) {
-        case 64: combine_kernel<64><<<blocks, 256, 0, stream>>>(p); break;
-        case 128: combine_kernel<128><<<blocks, 256, 0, stream>>>(p); break;
-        case 256: combine_kernel<256><<<blocks, 256, 0, stream>>>(p); break;
+        case 64: return launch_early(combine_kernel<64>, dim3(blocks), 256, 0, stream, p);
+        case 128: return launch_early(combine_kernel<128>, dim3(blocks), 256, 0, stream, p);
+        case 256: return launch_early(combine_kernel<256>, dim3(blocks), 256, 0, stream, p);
         default: return cudaErrorInvalidValue;
     }
-    return cudaGetLastError();
 }
 
 }  // namespace ua
