@@ -581,19 +581,25 @@ bool plan_fp4_rows(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4R
     if (p.g > kRows || p.max_seqlen_k > 1 << 30 || (int64_t)p.g * p.max_seqlen_q < kFp4RowsMin) return false;
     const int ppt = kRows / p.g;
     const int64_t tiles = (p.max_seqlen_q + ppt - 1) / ppt;
-    // Segments.  A CTA (one per SM) costs its key tiles plus about seven tiles'
-    // time to start and finish.  The host knows the longest sequence only, so
-    // the number taken is the one whose time is least over two batches: all
-    // that long (whole waves of CTAs), and lengths spread evenly below it
-    // (half the CTAs of every further segment leave at once).
+    // Segments.  A CTA (one per SM) costs its key tiles plus about ten tiles' time
+    // to start and finish, a segment about one more in the join.  The host knows
+    // the longest sequence only, so the number taken is the one whose time is
+    // least over two batches: all that long (whole waves of CTAs), and lengths
+    // spread evenly below it (half the CTAs of every further segment leave at
+    // once; beyond one wave the work is shared out, with a tail).  Measured, key
+    // weights included, 8 KV heads, 128 rows (us at 2 / 3 / 4 / 6 / 8 segments): 8
+    // sequences of 12000 keys 148 / 179 / 161 / 171 / 179, of 1000 to 12000 120 /
+    // 105 / 118 / 113 / 118; 4 of 12000 120 / 105 / 95 / 116 / 108, of 1000 to 12000
+    // 108 / 93 / 83 / 97 / 91.
     const int64_t base = (int64_t)p.hk * p.num_seqs * tiles;
     const int64_t key_tiles = (p.max_seqlen_k + 127) / 128;
     int64_t splits = 1;
     double best = 0.;
     for (int64_t s = 1; s <= std::min<int64_t>(64, std::max<int64_t>(1, key_tiles / 4)); ++s) {
-        const double each = 7. + (double)((key_tiles + s - 1) / s);
+        const double each = 10. + (double)((key_tiles + s - 1) / s), live = (double)base * (s + 1) / 2.;
+        const double work = (double)base * ((double)key_tiles + 10. * (s + 1)) / (2. * num_sms);
         const double cost = (double)((base * s + num_sms - 1) / num_sms) * each +
-                            std::max(1., (double)(base * (s + 1)) / (2. * num_sms)) * each;
+                            (live <= num_sms ? each : std::max(each, work + 0.6 * each)) + (double)s;
         if (s == 1 || cost < best) {
             best = cost;
             splits = s;

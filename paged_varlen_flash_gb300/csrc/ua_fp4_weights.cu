@@ -6,11 +6,12 @@
 // second time instead, from the K pages alone, with keys on the MMA's M: a thread
 // owns a key and adds the weights 2^(x - lse) of its rows from the tile's columns,
 // in row order -- no atomics, one order, nothing stored but the sum.  Whole calls,
-// us, scores stored / computed again (32 / 8 heads, d = 128 where not said): 8
-// sequences of 1000 to 12000 keys, 8 to 32 query tokens, 133 / 125; 16 of 4096, 32
-// tokens, 172 / 137; 2 of 6000, 200 tokens, 357 / 190; one prompt of 1000 tokens
-// 1095 / 205; one of 30000 keys, 8 tokens, 61 / 76; 4 of 9000, 2 KV heads, d = 256,
-// 96 / 88 and with a softcap (a second tanh per score) 119 / 144.
+// us, scores stored / computed again (32 / 8 heads, d = 128 where not said; the
+// first with the attention kernel's earlier segments): 8 sequences of 1000 to 12000
+// keys, 8 to 32 query tokens, 133 / 124; 16 of 4096, 32 tokens, 172 / 122; 2 of 6000,
+// 200 tokens, 357 / 179; one prompt of 1000 tokens 1095 / 210; one of 30000 keys, 8
+// tokens, 61 / 65; 4 of 9000, 2 KV heads, d = 256, 96 / 81 and with a softcap (a
+// second tanh per score) 119 / 138.
 // What bounds it: a CTA starts in 5 us (Q, the rows' denominators, the first
 // pages); then 1.3 us per key tile with two CTAs on the SM, half conversion and
 // half exponentials.
