@@ -26,8 +26,8 @@
 //
 // Measured: 1.55 us per tile of 128 x 128 at d = 128 (MMAs alone 0.52), the chain
 // convert -> QK^T -> softmax -> P.V; 16 sequences of 4096 keys and 8 KV heads, 64
-// rows each, 49 us; 8 of 1000 to 12000 keys, 67 us, of which a third is a tail of
-// CTAs with longer sequences than the others'.  Codes held in registers by the
+// rows each, 49 us; 8 of 1000 to 12000 keys in four segments 67 us, of which a
+// third is a tail of CTAs with longer sequences than the others'.  Codes held in registers by the
 // converters instead of the staged ring: 106 to 128 us for the latter.
 // Tensor memory: S(0), S(1) in columns [0, 256), O in [256, 256 + d).
 #include <algorithm>
