@@ -40,6 +40,21 @@ bool encode_cache_map(CUtensorMap* m, const void* base, const ua_problem_desc& d
                                 d.kv_dtype == UA_DTYPE_FP8_E4M3, box_rows);
 }
 
+// Two fresh buffers as zeros, complete on return: the problem's first call may
+// come on any stream.  cudaMemset only queues its work on the legacy default
+// stream, which a non-blocking stream does not wait for; a stream of its own
+// does not wait for what the default stream still has to do either.
+cudaError_t clear_now(void* a, size_t a_bytes, void* b, size_t b_bytes) {
+    cudaStream_t st;
+    cudaError_t e = cudaStreamCreateWithFlags(&st, cudaStreamNonBlocking);
+    if (e != cudaSuccess) return e;
+    e = cudaMemsetAsync(a, 0, a_bytes, st);
+    if (e == cudaSuccess && b_bytes) e = cudaMemsetAsync(b, 0, b_bytes, st);
+    const cudaError_t done = cudaStreamSynchronize(st);
+    cudaStreamDestroy(st);
+    return e == cudaSuccess ? done : e;
+}
+
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 }  // namespace
@@ -201,8 +216,7 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
         delete p;
         return UA_ERR_OUT_OF_MEMORY;
     }
-    e = cudaMemset(p->d_err, 0, sizeof(int32_t));
-    if (e == cudaSuccess && piece_bytes) e = cudaMemset(p->d_pieces, 0, piece_bytes);
+    e = clear_now(p->d_err, sizeof(int32_t), p->d_pieces, piece_bytes);
     if (e != cudaSuccess) {
         note_cuda(e, "ua_problem_create");
         cudaFree(p->d_err);
