@@ -166,6 +166,15 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
     if (d->split_partials != UA_PARTIALS_F32 && d->split_partials != UA_PARTIALS_BF16)
         return UA_ERR_INVALID_ARG;
 
+    // Rows that the workspace is sized for, and the bytes of one partial.  Sizes
+    // that 64 bits could not count are more than any device holds.
+    const double rows = (double)d->max_total_q * d->num_q_heads;
+    const size_t row_bytes = size_t(d->head_size + 2) * sizeof(float);
+    const size_t keys = ((size_t)d->max_blocks_per_seq * d->block_size + 127) / 128 * 128;
+    if (((d->flags & UA_FLAG_KEY_WEIGHTS) && rows * std::max((double)row_bytes, 4. * keys) >= 0x1p62) ||
+        (d->kv_dtype == UA_DTYPE_FP4_E2M1 && rows * row_bytes * 512 >= 0x1p62))
+        return UA_ERR_OUT_OF_MEMORY;
+
     ua_problem* p = new (std::nothrow) ua_problem();
     if (!p) return UA_ERR_OUT_OF_MEMORY;
     p->desc = *d;
@@ -177,14 +186,12 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
         delete p;
         return UA_ERR_CUDA;
     }
-    const size_t row_bytes = size_t(d->head_size + 2) * sizeof(float);
-    const size_t want = size_t(d->max_total_q) * d->num_q_heads * row_bytes * 16;
-    p->ws_bytes = std::min(want, kWorkspaceCap);
+    const bool capped = rows * row_bytes * 16 >= (double)kWorkspaceCap;
+    p->ws_bytes = capped ? kWorkspaceCap : size_t(d->max_total_q) * d->num_q_heads * row_bytes * 16;
     if (d->flags & UA_FLAG_KEY_WEIGHTS) {
         // Key weights always go through partials: room for one segment of every
         // row, and the rows' scores.
         p->ws_bytes = std::max(p->ws_bytes, size_t(d->max_total_q) * d->num_q_heads * row_bytes);
-        const size_t keys = ((size_t)d->max_blocks_per_seq * d->block_size + 127) / 128 * 128;
         p->scores_elems = size_t(d->max_total_q) * d->num_q_heads * keys;
     }
     size_t piece_bytes = 0;

@@ -55,3 +55,21 @@ for kv in (ua.UA_DTYPE_BF16, ua.UA_DTYPE_FP4_E2M1):
     assert fake.fake_pending() == 0
     ua.ua_destroy(p)
 """)
+
+
+def test_sizes_past_64_bits_are_refused(run):
+    """Workspaces whose byte counts wrap around are no small workspaces."""
+    run("""
+KW, FP4 = ua.UA_FLAG_CAUSAL | ua.UA_FLAG_KEY_WEIGHTS, ua.UA_DTYPE_FP4_E2M1
+for tokens in (1 << 50, 1 << 52, (1 << 57) + 1, (1 << 62) + 1):
+    assert status(max_total_q=tokens, flags=KW, num_q_heads=64, num_kv_heads=64, max_blocks_per_seq=512) == 4, tokens
+    assert status(max_total_q=tokens, kv_dtype=FP4, num_q_heads=64, num_kv_heads=64) == 4, tokens
+# Not so large: as before, the partials of a plain problem under their cap.
+before = fake.fake_allocated()
+assert status(max_total_q=1 << 62) == 0
+assert (128 << 20) <= fake.fake_allocated() - before < (10 << 30)
+before = fake.fake_allocated()
+assert status(max_total_q=8, flags=KW) == 0
+scores, work = 4 * 8 * 8 * 128, fake.fake_allocated() - before
+assert 4 * 8 * 8 * 16 * 130 + scores < work < 4 * 8 * 8 * 16 * 130 + scores + (1 << 20)
+""")
