@@ -277,6 +277,22 @@ def _weight_stride(t, name):
     raise ValueError("%s must be [num_seqs, H_k, n] with evenly spaced rows" % name)
 
 
+def _check(t, name, kind, like):
+    """Refuse a tensor of another element type, or on another device than ``like``."""
+    if str(t.dtype) != kind or t.device != like.device:
+        raise ValueError("%s must be %s on %s" % (name, kind, like.device))
+
+
+def _weight_rows(t, name, num_seqs, num_kv_heads, n, like):
+    """Row stride of key weights that hold at least n keys of num_seqs sequences."""
+    stride = _weight_stride(t, name)
+    shape = t.shape
+    if shape[0] < num_seqs or shape[1] != num_kv_heads or shape[2] < n:
+        raise ValueError("%s must be [num_seqs, H_k, n] with a column per key" % name)
+    _check(t, name, "torch.float32", like)
+    return stride
+
+
 def ua_forward_host(problem, q_host, k_cache, v_cache, block_table_host, cu_seqlens_q_host,
                     seqused_k_host, num_seqs, total_q, max_seqlen_q, max_seqlen_k, flags,
                     sinks_host, alibi_host, out_host, stream=None):
@@ -396,8 +412,9 @@ class Problem:
         """``forward`` that also writes decay * weights_in plus this call's
         attention weights to ``weights_out`` (fp32 [num_seqs, H_k, n >= max_seqlen_k];
         ``weights_in`` may be the same tensor, or None for zeros)."""
-        stride = _weight_stride(weights_out, "weights_out")
-        if weights_in is not None and _weight_stride(weights_in, "weights_in") != stride:
+        rows = num_seqs, self.num_kv_heads, max_seqlen_k, q
+        stride = _weight_rows(weights_out, "weights_out", *rows)
+        if weights_in is not None and _weight_rows(weights_in, "weights_in", *rows) != stride:
             raise ValueError("weights_in and weights_out must share a row stride")
         if out is None:
             import torch
@@ -440,8 +457,9 @@ class Problem:
                     dst_block_table=None, stream=None):
         """Keep ``budget`` keys of every (sequence, KV head) by weight, in place
         or into ``dst_block_table``; ``kept`` int32 [num_seqs, H_k, budget]."""
-        stride = _weight_stride(weights_in, "weights_in")
-        if _weight_stride(weights_out, "weights_out") != stride:
+        rows = num_seqs, self.num_kv_heads, max_seqlen_k, block_table
+        stride = _weight_rows(weights_in, "weights_in", *rows)
+        if _weight_rows(weights_out, "weights_out", *rows) != stride:
             raise ValueError("weights_in and weights_out must share a row stride")
         if tuple(kept.shape) != (num_seqs, self.num_kv_heads, budget) or not kept.is_contiguous():
             raise ValueError("kept must be a contiguous [num_seqs, H_k, budget]")

@@ -1,0 +1,90 @@
+"""What the cache methods of ``Problem`` refuse before the library is called: shapes,
+strides and element types that the kernels would read or write past.  CPU only: the
+problem has no handle, so that a call whose arguments pass ends in the library's
+"invalid argument"."""
+import pytest
+import torch
+
+import paged_varlen_flash_gb300 as ua
+from paged_varlen_flash_gb300 import build as ua_build
+
+N, HQ, HK, D, B, WIDTH, BLOCKS, KEYS = 3, 8, 2, 64, 16, 4, 20, 50
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    ua_build.build()
+    ua.load_library()
+
+
+@pytest.fixture()
+def p():
+    x = ua.Problem.__new__(ua.Problem)
+    x.handle = None
+    x.flags, x.head_size, x.num_q_heads, x.num_kv_heads = ua.UA_FLAG_CAUSAL, D, HQ, HK
+    x.block_size, x.max_blocks_per_seq = B, WIDTH
+    return x
+
+
+def reaches_the_library(call, **over):
+    with pytest.raises(ua.UAError) as e:
+        call(**over)
+    assert e.value.status == 1
+
+
+def base():
+    cache = torch.zeros(BLOCKS, B, HK, D, dtype=torch.bfloat16)
+    return dict(q=torch.zeros(N, HQ, D, dtype=torch.bfloat16), k=cache, v=cache.clone(),
+                table=torch.zeros(N, WIDTH, dtype=torch.int32), cu=torch.zeros(N + 1, dtype=torch.int32),
+                used=torch.zeros(N, dtype=torch.int32), w=torch.zeros(N, HK, KEYS + 5))
+
+
+def weights_call(p, w_in, w_out, num_seqs=N, keys=KEYS):
+    t = base()
+    p.forward_weights(t["q"], t["k"], t["v"], t["table"], t["cu"], t["used"], num_seqs, N, 1, keys,
+                      ua.UA_FLAG_CAUSAL, w_in, w_out, stream=0)
+
+
+BAD_WEIGHTS = [
+    torch.zeros(N, HK, KEYS - 1),                        # a key without a column
+    torch.zeros(N, HK - 1, KEYS),                        # too few heads
+    torch.zeros(N, HK + 1, KEYS),
+    torch.zeros(N - 1, HK, KEYS),                        # too few sequences
+    torch.zeros(N, HK, KEYS, dtype=torch.float64),
+    torch.zeros(N, HK, KEYS, dtype=torch.bfloat16),
+    torch.zeros(N, HK, KEYS, device="meta"),             # not where q is
+    torch.zeros(N, HK * KEYS),
+]
+
+
+@pytest.mark.parametrize("case", range(len(BAD_WEIGHTS)))
+def test_key_weights_of_other_shapes_and_types(p, case):
+    bad, good = BAD_WEIGHTS[case], torch.zeros(N, HK, KEYS)
+    for w_in, w_out in ((None, bad), (bad, bad), (bad, good), (good, bad)):
+        with pytest.raises(ValueError):
+            weights_call(p, w_in, w_out)
+
+
+def test_key_weights_that_fit(p):
+    big = torch.zeros(N + 2, HK, KEYS + 9)
+    for w in (torch.zeros(N, HK, KEYS), big, big[1:, :, :KEYS]):
+        reaches_the_library(weights_call, p=p, w_in=None, w_out=w)
+        reaches_the_library(weights_call, p=p, w_in=w, w_out=w)
+
+
+def evict_call(p, w_in=None, w_out=None, budget=10, kept=None, used=None, dst=None, keys=KEYS):
+    t = base()
+    w_in = t["w"] if w_in is None else w_in
+    w_out = t["w"] if w_out is None else w_out
+    kept = torch.zeros(N, HK, budget, dtype=torch.int32) if kept is None else kept
+    p.cache_evict(t["k"], t["v"], t["table"], t["used"], N, keys, w_in, w_out, budget, 2, kept,
+                  t["used"] if used is None else used, dst_block_table=dst, stream=0)
+
+
+@pytest.mark.parametrize("case", range(len(BAD_WEIGHTS)))
+def test_evicted_weights_of_other_shapes_and_types(p, case):
+    reaches_the_library(evict_call, p=p)
+    for w in (dict(w_in=BAD_WEIGHTS[case]), dict(w_out=BAD_WEIGHTS[case]),
+              dict(w_in=BAD_WEIGHTS[case], w_out=BAD_WEIGHTS[case])):
+        with pytest.raises(ValueError):
+            evict_call(p, **w)
