@@ -463,6 +463,10 @@ class Problem:
             raise ValueError("weights_in and weights_out must share a row stride")
         if tuple(kept.shape) != (num_seqs, self.num_kv_heads, budget) or not kept.is_contiguous():
             raise ValueError("kept must be a contiguous [num_seqs, H_k, budget]")
+        _check(kept, "kept", "torch.int32", block_table)
+        if seqused_out.numel() < num_seqs or not seqused_out.is_contiguous():
+            raise ValueError("seqused_out must be a contiguous [num_seqs]")
+        _check(seqused_out, "seqused_out", "torch.int32", block_table)
         st = ua_cache_evict(self.handle, k_cache, v_cache, block_table, dst_block_table, seqused_k,
                             num_seqs, max_seqlen_k, weights_in, weights_out, stride, budget,
                             recent, kept, seqused_out, stream)

@@ -88,3 +88,18 @@ def test_evicted_weights_of_other_shapes_and_types(p, case):
               dict(w_in=BAD_WEIGHTS[case], w_out=BAD_WEIGHTS[case])):
         with pytest.raises(ValueError):
             evict_call(p, **w)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(kept=torch.zeros(N, HK, 10, dtype=torch.int16)), dict(kept=torch.zeros(N, HK, 10, dtype=torch.int64)),
+    dict(kept=torch.zeros(N, HK, 10)), dict(kept=torch.zeros(N, HK, 9, dtype=torch.int32)),
+    dict(kept=torch.zeros(N, HK, 20, dtype=torch.int32)[:, :, ::2]),
+    dict(kept=torch.zeros(N, HK, 10, dtype=torch.int32, device="meta")),
+    dict(used=torch.zeros(N - 1, dtype=torch.int32)), dict(used=torch.zeros(N, dtype=torch.int16)),
+    dict(used=torch.zeros(N, dtype=torch.int64)), dict(used=torch.zeros(2 * N, dtype=torch.int32)[::2]),
+    dict(used=torch.zeros(N, dtype=torch.int32, device="meta")),
+])
+def test_eviction_results_of_other_shapes_and_types(p, bad):
+    with pytest.raises(ValueError):
+        evict_call(p, **bad)
+    reaches_the_library(evict_call, p=p, used=torch.zeros(N + 4, dtype=torch.int32))
