@@ -363,6 +363,8 @@ class Problem:
                                         kv_dtype, k_scale, v_scale, split_partials)
         self.flags = flags
         self.head_size = head_size
+        self.block_size = block_size
+        self.max_blocks_per_seq = max_blocks_per_seq
         self.num_q_heads = num_q_heads
         self.num_kv_heads = num_kv_heads
 
@@ -467,6 +469,14 @@ class Problem:
         if seqused_out.numel() < num_seqs or not seqused_out.is_contiguous():
             raise ValueError("seqused_out must be a contiguous [num_seqs]")
         _check(seqused_out, "seqused_out", "torch.int32", block_table)
+        if dst_block_table is not None:
+            # Read with block_table's row stride, one id per block of kept keys.
+            shape, step = dst_block_table.shape, dst_block_table.stride()
+            blocks = -(-min(budget, max_seqlen_k) // self.block_size)
+            if (len(shape) != 2 or shape[0] < num_seqs or shape[1] < blocks or (shape[1] > 1 and step[1] != 1) or
+                    (num_seqs > 1 and step[0] != self.max_blocks_per_seq)):
+                raise ValueError("dst_block_table must be laid out like block_table")
+            _check(dst_block_table, "dst_block_table", "torch.int32", block_table)
         st = ua_cache_evict(self.handle, k_cache, v_cache, block_table, dst_block_table, seqused_k,
                             num_seqs, max_seqlen_k, weights_in, weights_out, stride, budget,
                             recent, kept, seqused_out, stream)

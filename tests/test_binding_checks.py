@@ -103,3 +103,27 @@ def test_eviction_results_of_other_shapes_and_types(p, bad):
     with pytest.raises(ValueError):
         evict_call(p, **bad)
     reaches_the_library(evict_call, p=p, used=torch.zeros(N + 4, dtype=torch.int32))
+
+
+INT = torch.int32
+
+
+@pytest.mark.parametrize("bad", [
+    torch.zeros(N, 1, dtype=INT),                            # compact: ceil(budget / b) ids a row
+    torch.zeros(N, WIDTH + 1, dtype=INT),
+    torch.zeros(N - 1, WIDTH, dtype=INT), torch.zeros(N * WIDTH, dtype=INT),
+    torch.zeros(WIDTH, N, dtype=INT).T, torch.zeros(N, WIDTH, dtype=torch.int64),
+    torch.zeros(N, WIDTH, dtype=torch.int16), torch.zeros(N, WIDTH, dtype=INT, device="meta"),
+])
+def test_destination_tables_of_another_layout(p, bad):
+    with pytest.raises(ValueError):
+        evict_call(p, dst=bad)
+
+
+def test_destination_tables_that_fit(p):
+    full = torch.zeros(N + 1, WIDTH, dtype=INT)
+    for dst in (full, full[1:], full[:, :1], full[:, 1:]):   # 10 kept keys are one block of 16
+        reaches_the_library(evict_call, p=p, dst=dst)
+    with pytest.raises(ValueError):
+        evict_call(p, budget=17, dst=full[:, :1])            # two blocks
+    reaches_the_library(evict_call, p=p, budget=17, keys=16, dst=full[:, :1])
