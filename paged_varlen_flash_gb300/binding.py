@@ -134,11 +134,10 @@ def ua_status_string(status):
 
 
 def _ptr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
+    try:
+        return t.data_ptr()
+    except AttributeError:               # None or an address
         return t
-    return t.data_ptr()
 
 
 def _stream(stream):
@@ -256,12 +255,17 @@ def cache_shape(num_blocks, num_kv_heads, head_size, block_size, kv_dtype=UA_DTY
     return (num_blocks, block_size, num_kv_heads, head_size)
 
 
-def _token_stride(t, name):
-    """Elements between the tokens of a [total, H_k, d] tensor whose rows are contiguous."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2]):
+def _token_stride(t, name, total_q=0, num_kv_heads=None, head_size=None):
+    """Elements between the tokens of a [total, H_k, d] tensor whose rows are contiguous
+    (of at least total_q tokens, and those heads and dims)."""
+    stride = t.stride()
+    if len(stride) != 3:
+        raise ValueError("%s must be [total_q, H_k, d]" % name)
+    n, heads, dims = t.shape
+    if (stride[2] != 1 or (heads > 1 and stride[1] != dims) or n < total_q or
+            (num_kv_heads is not None and (heads != num_kv_heads or dims != head_size))):
         raise ValueError("%s must be [total_q, H_k, d] with contiguous heads" % name)
-    return stride[0] if shape[0] > 1 else max(stride[0], shape[1] * shape[2])
+    return stride[0] if n > 1 else max(stride[0], heads * dims)
 
 
 def _weight_stride(t, name):
@@ -433,8 +437,10 @@ class Problem:
                     num_seqs, total_q, max_seqlen_q, max_seqlen_k, stream=None):
         """Write a chunk's rows (bf16 [total_q, H_k, d]; tokens may be strided)
         to the positions ``forward`` expects them at."""
-        stride = _token_stride(k_new, "k_new")
-        if _token_stride(v_new, "v_new") != stride:
+        stride = _token_stride(k_new, "k_new", total_q, self.num_kv_heads, self.head_size)
+        _check(k_new, "k_new", "torch.bfloat16", k_cache)
+        _check(v_new, "v_new", "torch.bfloat16", k_cache)
+        if _token_stride(v_new, "v_new", total_q, self.num_kv_heads, self.head_size) != stride:
             raise ValueError("k_new and v_new must share a token stride")
         st = ua_cache_store(self.handle, k_new, v_new, stride, k_cache, v_cache, block_table,
                             cu_seqlens_q, seqused_k, num_seqs, total_q, max_seqlen_q,

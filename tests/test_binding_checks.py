@@ -127,3 +127,30 @@ def test_destination_tables_that_fit(p):
     with pytest.raises(ValueError):
         evict_call(p, budget=17, dst=full[:, :1])            # two blocks
     reaches_the_library(evict_call, p=p, budget=17, keys=16, dst=full[:, :1])
+
+
+def store_call(p, k_new, v_new, total_q=N):
+    t = base()
+    p.cache_store(k_new, v_new, t["k"], t["v"], t["table"], t["cu"], t["used"], N, total_q, 1, KEYS, stream=0)
+
+
+BF = torch.bfloat16
+
+
+@pytest.mark.parametrize("bad", [
+    torch.zeros(N - 1, HK, D, dtype=BF), torch.zeros(N, HK - 1, D, dtype=BF), torch.zeros(N, HK + 1, D, dtype=BF),
+    torch.zeros(N, HK, D // 2, dtype=BF), torch.zeros(N, HK, 2 * D, dtype=BF),
+    torch.zeros(N, HK, D, dtype=torch.float16), torch.zeros(N, HK, D), torch.zeros(N, HK, D, dtype=torch.uint8),
+    torch.zeros(N, HK, D, dtype=BF, device="meta"),
+])
+def test_new_rows_of_other_shapes_and_types(p, bad):
+    good = torch.zeros(N, HK, D, dtype=BF)
+    for k_new, v_new in ((bad, bad), (good, bad), (bad, good)):
+        with pytest.raises(ValueError):
+            store_call(p, k_new, v_new)
+
+
+def test_new_rows_that_fit(p):
+    fused = torch.zeros(N + 3, 2 * HK + 1, D, dtype=BF)      # a padded batch of a fused projection
+    reaches_the_library(store_call, p=p, k_new=fused[:, :HK], v_new=fused[:, HK:2 * HK])
+    reaches_the_library(store_call, p=p, k_new=fused[:, :HK], v_new=fused[:, HK:2 * HK], total_q=N + 3)
