@@ -281,10 +281,14 @@ def _weight_stride(t, name):
     raise ValueError("%s must be [num_seqs, H_k, n] with evenly spaced rows" % name)
 
 
-def _check(t, name, kind, like):
-    """Refuse a tensor of another element type, or on another device than ``like``."""
-    if str(t.dtype) != kind or t.device != like.device:
-        raise ValueError("%s must be %s on %s" % (name, kind, like.device))
+_type_names = {}
+
+
+def _check(t, name, kind, device):
+    """Refuse a tensor of another element type, or not on that device (as get_device counts)."""
+    dtype = t.dtype
+    if (_type_names.get(dtype) or _type_names.setdefault(dtype, str(dtype))) != kind or t.get_device() != device:
+        raise ValueError("%s must be %s, on the device of the other tensors" % (name, kind))
 
 
 def _weight_rows(t, name, num_seqs, num_kv_heads, n, like):
@@ -293,7 +297,7 @@ def _weight_rows(t, name, num_seqs, num_kv_heads, n, like):
     shape = t.shape
     if shape[0] < num_seqs or shape[1] != num_kv_heads or shape[2] < n:
         raise ValueError("%s must be [num_seqs, H_k, n] with a column per key" % name)
-    _check(t, name, "torch.float32", like)
+    _check(t, name, "torch.float32", like.get_device())
     return stride
 
 
@@ -438,8 +442,9 @@ class Problem:
         """Write a chunk's rows (bf16 [total_q, H_k, d]; tokens may be strided)
         to the positions ``forward`` expects them at."""
         stride = _token_stride(k_new, "k_new", total_q, self.num_kv_heads, self.head_size)
-        _check(k_new, "k_new", "torch.bfloat16", k_cache)
-        _check(v_new, "v_new", "torch.bfloat16", k_cache)
+        device = k_cache.get_device()
+        _check(k_new, "k_new", "torch.bfloat16", device)
+        _check(v_new, "v_new", "torch.bfloat16", device)
         if _token_stride(v_new, "v_new", total_q, self.num_kv_heads, self.head_size) != stride:
             raise ValueError("k_new and v_new must share a token stride")
         st = ua_cache_store(self.handle, k_new, v_new, stride, k_cache, v_cache, block_table,
@@ -452,11 +457,24 @@ class Problem:
                      v_out, out_block_table, begin=None, stream=None):
         """Expand the keys from ``begin`` (or 0) on into the bf16 pages
         ``k_out`` / ``v_out`` [blocks, b, H_k, d]."""
-        if out_block_table.dim() != 2 or out_block_table.stride(1) != 1:
+        step, device = out_block_table.stride(), k_cache.get_device()
+        if len(step) != 2 or step[1] != 1 or out_block_table.shape[0] < num_seqs:
             raise ValueError("out_block_table must be [num_seqs, n] with unit inner stride")
+        shape = k_out.shape
+        if (len(shape) != 4 or shape[1] != self.block_size or shape[2] != self.num_kv_heads or
+                shape[3] != self.head_size or v_out.shape != shape or not k_out.is_contiguous() or
+                not v_out.is_contiguous()):
+            raise ValueError("k_out and v_out must be contiguous [blocks, b, H_k, d]")
+        _check(k_out, "k_out", "torch.bfloat16", device)
+        _check(v_out, "v_out", "torch.bfloat16", device)
+        _check(out_block_table, "out_block_table", "torch.int32", device)
+        if begin is not None:
+            if begin.numel() < num_seqs or not begin.is_contiguous():
+                raise ValueError("begin must be a contiguous [num_seqs]")
+            _check(begin, "begin", "torch.int32", device)
         st = ua_cache_expand(self.handle, k_cache, v_cache, block_table, seqused_k, begin,
                              num_seqs, max_keys, k_out, v_out, out_block_table,
-                             out_block_table.stride(0), k_out.shape[0], stream)
+                             step[0], shape[0], stream)
         if st != UA_OK:
             raise UAError(st, "ua_cache_expand")
 
@@ -471,10 +489,10 @@ class Problem:
             raise ValueError("weights_in and weights_out must share a row stride")
         if tuple(kept.shape) != (num_seqs, self.num_kv_heads, budget) or not kept.is_contiguous():
             raise ValueError("kept must be a contiguous [num_seqs, H_k, budget]")
-        _check(kept, "kept", "torch.int32", block_table)
+        _check(kept, "kept", "torch.int32", block_table.get_device())
         if seqused_out.numel() < num_seqs or not seqused_out.is_contiguous():
             raise ValueError("seqused_out must be a contiguous [num_seqs]")
-        _check(seqused_out, "seqused_out", "torch.int32", block_table)
+        _check(seqused_out, "seqused_out", "torch.int32", block_table.get_device())
         if dst_block_table is not None:
             # Read with block_table's row stride, one id per block of kept keys.
             shape, step = dst_block_table.shape, dst_block_table.stride()
@@ -482,7 +500,7 @@ class Problem:
             if (len(shape) != 2 or shape[0] < num_seqs or shape[1] < blocks or (shape[1] > 1 and step[1] != 1) or
                     (num_seqs > 1 and step[0] != self.max_blocks_per_seq)):
                 raise ValueError("dst_block_table must be laid out like block_table")
-            _check(dst_block_table, "dst_block_table", "torch.int32", block_table)
+            _check(dst_block_table, "dst_block_table", "torch.int32", block_table.get_device())
         st = ua_cache_evict(self.handle, k_cache, v_cache, block_table, dst_block_table, seqused_k,
                             num_seqs, max_seqlen_k, weights_in, weights_out, stride, budget,
                             recent, kept, seqused_out, stream)

@@ -11,6 +11,16 @@ from paged_varlen_flash_gb300 import build as ua_build
 N, HQ, HK, D, B, WIDTH, BLOCKS, KEYS = 3, 8, 2, 64, 16, 4, 20, 50
 
 
+class Elsewhere(torch.Tensor):
+    def get_device(self):
+        return 3
+
+
+def elsewhere(t):
+    """A tensor that says it is on another device."""
+    return t.as_subclass(Elsewhere)
+
+
 @pytest.fixture(scope="module", autouse=True)
 def _built():
     ua_build.build()
@@ -52,7 +62,7 @@ BAD_WEIGHTS = [
     torch.zeros(N - 1, HK, KEYS),                        # too few sequences
     torch.zeros(N, HK, KEYS, dtype=torch.float64),
     torch.zeros(N, HK, KEYS, dtype=torch.bfloat16),
-    torch.zeros(N, HK, KEYS, device="meta"),             # not where q is
+    elsewhere(torch.zeros(N, HK, KEYS)),             # not where q is
     torch.zeros(N, HK * KEYS),
 ]
 
@@ -94,10 +104,10 @@ def test_evicted_weights_of_other_shapes_and_types(p, case):
     dict(kept=torch.zeros(N, HK, 10, dtype=torch.int16)), dict(kept=torch.zeros(N, HK, 10, dtype=torch.int64)),
     dict(kept=torch.zeros(N, HK, 10)), dict(kept=torch.zeros(N, HK, 9, dtype=torch.int32)),
     dict(kept=torch.zeros(N, HK, 20, dtype=torch.int32)[:, :, ::2]),
-    dict(kept=torch.zeros(N, HK, 10, dtype=torch.int32, device="meta")),
+    dict(kept=elsewhere(torch.zeros(N, HK, 10, dtype=torch.int32))),
     dict(used=torch.zeros(N - 1, dtype=torch.int32)), dict(used=torch.zeros(N, dtype=torch.int16)),
     dict(used=torch.zeros(N, dtype=torch.int64)), dict(used=torch.zeros(2 * N, dtype=torch.int32)[::2]),
-    dict(used=torch.zeros(N, dtype=torch.int32, device="meta")),
+    dict(used=elsewhere(torch.zeros(N, dtype=torch.int32))),
 ])
 def test_eviction_results_of_other_shapes_and_types(p, bad):
     with pytest.raises(ValueError):
@@ -113,7 +123,7 @@ INT = torch.int32
     torch.zeros(N, WIDTH + 1, dtype=INT),
     torch.zeros(N - 1, WIDTH, dtype=INT), torch.zeros(N * WIDTH, dtype=INT),
     torch.zeros(WIDTH, N, dtype=INT).T, torch.zeros(N, WIDTH, dtype=torch.int64),
-    torch.zeros(N, WIDTH, dtype=torch.int16), torch.zeros(N, WIDTH, dtype=INT, device="meta"),
+    torch.zeros(N, WIDTH, dtype=torch.int16), elsewhere(torch.zeros(N, WIDTH, dtype=INT)),
 ])
 def test_destination_tables_of_another_layout(p, bad):
     with pytest.raises(ValueError):
@@ -141,7 +151,7 @@ BF = torch.bfloat16
     torch.zeros(N - 1, HK, D, dtype=BF), torch.zeros(N, HK - 1, D, dtype=BF), torch.zeros(N, HK + 1, D, dtype=BF),
     torch.zeros(N, HK, D // 2, dtype=BF), torch.zeros(N, HK, 2 * D, dtype=BF),
     torch.zeros(N, HK, D, dtype=torch.float16), torch.zeros(N, HK, D), torch.zeros(N, HK, D, dtype=torch.uint8),
-    torch.zeros(N, HK, D, dtype=BF, device="meta"),
+    elsewhere(torch.zeros(N, HK, D, dtype=BF)),
 ])
 def test_new_rows_of_other_shapes_and_types(p, bad):
     good = torch.zeros(N, HK, D, dtype=BF)
@@ -154,3 +164,38 @@ def test_new_rows_that_fit(p):
     fused = torch.zeros(N + 3, 2 * HK + 1, D, dtype=BF)      # a padded batch of a fused projection
     reaches_the_library(store_call, p=p, k_new=fused[:, :HK], v_new=fused[:, HK:2 * HK])
     reaches_the_library(store_call, p=p, k_new=fused[:, :HK], v_new=fused[:, HK:2 * HK], total_q=N + 3)
+
+
+def expand_call(p, k_out=None, v_out=None, table=None, begin=None):
+    t = base()
+    k_out = torch.zeros(6, B, HK, D, dtype=BF) if k_out is None else k_out
+    v_out = torch.zeros(6, B, HK, D, dtype=BF) if v_out is None else v_out
+    table = torch.zeros(N, 9, dtype=INT) if table is None else table
+    p.cache_expand(t["k"], t["v"], t["table"], t["used"], N, KEYS, k_out, v_out, table, begin=begin, stream=0)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(v_out=torch.zeros(5, B, HK, D, dtype=BF)),          # fewer blocks than k_out names
+    dict(k_out=torch.zeros(5, B, HK, D, dtype=BF)),
+    dict(k_out=torch.zeros(6, B, HK, D)), dict(v_out=torch.zeros(6, B, HK, D, dtype=torch.uint8)),
+    dict(k_out=torch.zeros(6, B // 2, HK, D, dtype=BF), v_out=torch.zeros(6, B // 2, HK, D, dtype=BF)),
+    dict(k_out=torch.zeros(6, B, 1, D, dtype=BF), v_out=torch.zeros(6, B, 1, D, dtype=BF)),
+    dict(k_out=torch.zeros(6, B, HK, 2 * D, dtype=BF)[..., :D]), dict(v_out=torch.zeros(12, B, HK, D, dtype=BF)[::2]),
+    dict(k_out=torch.zeros(6, B * HK * D, dtype=BF), v_out=torch.zeros(6, B * HK * D, dtype=BF)),
+    dict(k_out=elsewhere(torch.zeros(6, B, HK, D, dtype=BF)),
+         v_out=elsewhere(torch.zeros(6, B, HK, D, dtype=BF))),
+    dict(table=torch.zeros(N - 1, 9, dtype=INT)), dict(table=torch.zeros(N, 9, dtype=torch.int64)),
+    dict(table=torch.zeros(N, 9, dtype=torch.int16)), dict(table=torch.zeros(9, N, dtype=INT).T),
+    dict(table=elsewhere(torch.zeros(N, 9, dtype=INT))),
+    dict(begin=torch.zeros(N - 1, dtype=INT)), dict(begin=torch.zeros(N, dtype=torch.int64)),
+    dict(begin=torch.zeros(N, dtype=torch.int16)),
+])
+def test_pages_and_tables_to_expand_into_of_other_shapes_and_types(p, bad):
+    with pytest.raises(ValueError):
+        expand_call(p, **bad)
+
+
+def test_pages_and_tables_to_expand_into_that_fit(p):
+    reaches_the_library(expand_call, p=p)
+    reaches_the_library(expand_call, p=p, table=torch.zeros(N + 2, 12, dtype=INT)[1:, 3:],
+                        begin=torch.zeros(N + 1, dtype=INT))
