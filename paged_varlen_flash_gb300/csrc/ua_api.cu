@@ -293,6 +293,12 @@ ua_status ua_set_profile_events(ua_problem* p, void* ev_begin, void* ev_end) {
 
 namespace {
 
+// Every pointer is null or aligned to 4 bytes (the kernels' int32 and fp32 arrays).
+template <typename... P>
+bool words(const P*... ptr) {
+    return ((reinterpret_cast<uintptr_t>(ptr) | ...) & 3u) == 0;
+}
+
 // Host checks shared by the forward entry points, then the kernel parameters.
 // Returns UA_OK with *skip set when the call has nothing to compute.
 ua_status prepare_call(ua_problem* p, const void* q, const void* k_cache, const void* v_cache,
@@ -324,6 +330,7 @@ ua_status prepare_call(ua_problem* p, const void* q, const void* k_cache, const 
     if (num_seqs > 65535) return UA_ERR_UNSUPPORTED;   // grids index sequences on gridDim.z
     if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens_q || !seqused_k || !out)
         return UA_ERR_INVALID_ARG;
+    if (!words(block_table, cu_seqlens_q, seqused_k, sinks, alibi_slopes)) return UA_ERR_INVALID_ARG;
     auto misaligned = [](const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) != 0; };
     if (misaligned(q) || misaligned(out) || misaligned(k_cache) || misaligned(v_cache))
         return UA_ERR_INVALID_ARG;
@@ -727,9 +734,7 @@ ua_status ua_forward_weights(ua_problem* p, const void* q, const void* k_cache, 
         weight_stride < max_seqlen_k || !on_device(p))
         return UA_ERR_INVALID_ARG;
     if (skip) return UA_OK;
-    if (!weights_out || (reinterpret_cast<uintptr_t>(weights_out) & 3u) != 0 ||
-        (reinterpret_cast<uintptr_t>(weights_in) & 3u) != 0)
-        return UA_ERR_INVALID_ARG;
+    if (!weights_out || !words(weights_in, weights_out)) return UA_ERR_INVALID_ARG;
     if (d.path != UA_PATH_AUTO || d.num_kv_heads > 65535 || max_seqlen_k > 1 << 30) return UA_ERR_UNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     fp.scores = p->d_scores;
@@ -787,7 +792,8 @@ ua_status ua_cache_store(ua_problem* p, const void* k_new, const void* v_new, in
     if (num_seqs == 0 || total_q == 0 || max_seqlen_q == 0) return UA_OK;
     if (num_seqs > 65535) return UA_ERR_UNSUPPORTED;
     if (!k_new || !v_new || !k_cache || !v_cache || !block_table || !cu_seqlens_q || !seqused_k ||
-        !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache))
+        !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !words(block_table, cu_seqlens_q, seqused_k))
         return UA_ERR_INVALID_ARG;
     ua::StoreParams sp{};
     sp.c = cache_params(p, k_cache, v_cache, block_table, seqused_k, num_seqs);
@@ -823,7 +829,8 @@ ua_status ua_cache_expand(ua_problem* p, const void* k_cache, const void* v_cach
     if (num_seqs == 0 || max_keys == 0) return UA_OK;
     if (num_seqs > 65535 || out_num_blocks > (int64_t(1) << 31) - 1) return UA_ERR_UNSUPPORTED;
     if (!k_cache || !v_cache || !block_table || !seqused_k || !k_out || !v_out || !out_block_table ||
-        !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out))
+        !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(k_out) || !aligned16(v_out) ||
+        !words(block_table, seqused_k, begin, out_block_table))
         return UA_ERR_INVALID_ARG;
     ua::ExpandParams ep{};
     ep.c = cache_params(p, k_cache, v_cache, block_table, seqused_k, num_seqs);
@@ -861,8 +868,7 @@ ua_status ua_cache_evict(ua_problem* p, void* k_cache, void* v_cache, const int3
     if (num_seqs > 65535 || d.num_kv_heads > 32767 || max_seqlen_k > 1 << 30) return UA_ERR_UNSUPPORTED;
     if (!k_cache || !v_cache || !block_table || !seqused_k || !weights_in || !weights_out || !kept ||
         !seqused_out || !aligned16(k_cache) || !aligned16(v_cache) ||
-        (reinterpret_cast<uintptr_t>(weights_in) & 3u) != 0 ||
-        (reinterpret_cast<uintptr_t>(weights_out) & 3u) != 0)
+        !words(block_table, dst_block_table, seqused_k, weights_in, weights_out, kept, seqused_out))
         return UA_ERR_INVALID_ARG;
     ua::EvictParams ep{};
     ep.c = cache_params(p, k_cache, v_cache, block_table, seqused_k, num_seqs);

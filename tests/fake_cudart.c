@@ -20,7 +20,6 @@ int fake_pending(void) {
 size_t fake_allocated(void) { return allocated; }
 
 int cudaGetDevice(int *d) { *d = 0; return 0; }
-int cudaGetLastError(void) { return 0; }
 int cudaDeviceGetAttribute(int *v, int attr, int dev) { (void)attr; (void)dev; *v = 152; return 0; }
 int cudaMalloc(void **p, size_t n) {
     allocated += n;

@@ -73,3 +73,36 @@ assert status(max_total_q=8, flags=KW) == 0
 scores, work = 4 * 8 * 8 * 128, fake.fake_allocated() - before
 assert 4 * 8 * 8 * 16 * 130 + scores < work < 4 * 8 * 8 * 16 * 130 + scores + (1 << 20)
 """)
+
+
+def test_misaligned_arrays_are_refused(run):
+    """int32 and fp32 arrays off their 4-byte boundary; nothing is launched (a call
+    that passes the checks ends in a CUDA error here)."""
+    run("""
+p = create(flags=ua.UA_FLAG_CAUSAL | ua.UA_FLAG_KEY_WEIGHTS | ua.UA_FLAG_SINKS | ua.UA_FLAG_ALIBI,
+           kv_dtype=ua.UA_DTYPE_FP4_E2M1)
+A = 1 << 12                                   # an address that only the checks look at
+flags = ua.UA_FLAG_CAUSAL | ua.UA_FLAG_SINKS | ua.UA_FLAG_ALIBI
+
+def forward(table=A, cu=A, used=A, sinks=A, alibi=A):
+    return ua.ua_forward(p, A, A, A, table, cu, used, 2, 2, 1, 40, flags, sinks, alibi, A, stream=0)
+
+def weights(table=A, cu=A, used=A, sinks=A, alibi=A, w_in=A, w_out=A):
+    return ua.ua_forward_weights(p, A, A, A, table, cu, used, 2, 2, 1, 40, flags, sinks, alibi, w_in, w_out, 40, 1.0,
+                                 A, stream=0)
+
+def store(table=A, cu=A, used=A):
+    return ua.ua_cache_store(p, A, A, 256, A, A, table, cu, used, 2, 2, 1, 40, stream=0)
+
+def expand(table=A, used=A, begin=A, out=A):
+    return ua.ua_cache_expand(p, A, A, table, used, begin, 2, 40, A, A, out, 8, 64, stream=0)
+
+def evict(table=A, dst=A + 64, used=A, w_in=A, w_out=A, kept=A, used_out=A):
+    return ua.ua_cache_evict(p, A, A, table, dst, used, 2, 40, w_in, w_out, 40, 10, 2, kept, used_out, stream=0)
+
+for call in (forward, weights, store, expand, evict):
+    assert call() == 3, (call.__name__, call())
+    for name in call.__code__.co_varnames[:call.__code__.co_argcount]:
+        for off in (1, 2, 3):
+            assert call(**{name: A + off}) == 1, (call.__name__, name)
+""")
