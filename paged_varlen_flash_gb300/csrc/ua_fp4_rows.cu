@@ -394,8 +394,10 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
         float m = -INFINITY, l = 0.f;
         bool ok = wwait(q_full, 0);              // q_scale
         const float tau = p.scale * p.k_scale * q_scale[r];
-        // The score chain is in log2 units from the products on.
-        const float cap = p.softcap * kLog2e, fac = tau * (softcap ? 1.f / p.softcap : kLog2e);
+        // The score chain is in log2 units from the products on.  A factor of zero
+        // (tau below fp32: tiny k_scale and query) would make NaN of masked scores;
+        // at the smallest normal number every score still is 0 to 2^-100.
+        const float cap = p.softcap * kLog2e, fac = fmaxf(tau * (softcap ? 1.f / p.softcap : kLog2e), 0x1p-126f);
         for (int j = 0; ok && j < n; ++j) {
             if (!(ok = wwait(s_full0 + 8 * (j & 1), (j >> 1) & 1))) break;
             const int key0 = (t_begin + j) * kBN;
