@@ -199,3 +199,22 @@ def test_pages_and_tables_to_expand_into_that_fit(p):
     reaches_the_library(expand_call, p=p)
     reaches_the_library(expand_call, p=p, table=torch.zeros(N + 2, 12, dtype=INT)[1:, 3:],
                         begin=torch.zeros(N + 1, dtype=INT))
+
+
+def test_current_stream_with_and_without_the_short_accessors():
+    """The stream of whatever device is current at the call; the public API where torch
+    lacks the accessors."""
+    from types import SimpleNamespace as NS
+    from paged_varlen_flash_gb300.binding import _stream_reader
+    now = dict(device=0, streams={0: 11, 1: 22})
+    cuda = NS(current_device=lambda: now["device"],
+              current_stream=lambda: NS(cuda_stream=now["streams"][now["device"]]))
+    raw = dict(_cuda_getDevice=lambda: now["device"], _cuda_getCurrentRawStream=lambda d: now["streams"][d])
+    for c in (raw, {}, dict(_cuda_getDevice=raw["_cuda_getDevice"])):
+        read = _stream_reader(NS(cuda=cuda, _C=NS(**c)))
+        now.update(device=0, streams={0: 11, 1: 22})
+        assert read() == 11
+        now["device"] = 1
+        assert read() == 22
+        now["streams"][1] = 33
+        assert read() == 33
