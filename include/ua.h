@@ -364,7 +364,8 @@ ua_status ua_forward_noalloc(const ua_problem_desc *desc, const void *q, const v
  *
  * The calls below are asynchronous on `stream`, allocate nothing, launch
  * nothing when they return an error, need the problem's device to be current
- * (else UA_ERR_INVALID_ARG), and report malformed metadata through the
+ * and int32 and fp32 arrays on 4-byte boundaries (else UA_ERR_INVALID_ARG), and
+ * report malformed metadata through the
  * problem's device error word like ua_forward.  Calls on one problem share
  * its workspace: calls (or graph replays) that may overlap on the GPU need a
  * problem each.
@@ -397,7 +398,8 @@ ua_status ua_cache_store(ua_problem *p, const void *k_new, const void *v_new, in
 
 /*
  * ua_cache_expand -- the values of the cached keys begin[s] <= j < S_k of
- * every sequence (begin NULL: from 0), rounded once to bf16, into bf16 pages
+ * every sequence (begin NULL: from 0), the fp32 product of code, scale and
+ * k_scale or v_scale rounded to bf16, into bf16 pages
  * [out_num_blocks, b, H_k, d] at block out_block_table[s][j / b] (rows of
  * out_table_stride ids), slot j % b.  A bf16 problem with these pages runs the
  * prefill kernels over what a 4-bit or fp8 cache holds.  Exact when the scale
@@ -459,7 +461,8 @@ ua_status ua_forward_weights(ua_problem *p, const void *q, const void *k_cache,
  * order, to positions 0, 1, ... of dst_block_table, each KV head with its own
  * choice; positions afterwards are ranks, not the original positions, so
  * ALiBi and windows no longer mean distances.
- *   dst_block_table  same layout as block_table.  NULL or block_table itself
+ *   dst_block_table  same layout as block_table, its row stride
+ *                    (max_blocks_per_seq) too.  NULL or block_table itself
  *                    evicts in place; any other table must name blocks that
  *                    block_table does not name (the sources stay as they are,
  *                    so a prefix shared with another sequence survives).

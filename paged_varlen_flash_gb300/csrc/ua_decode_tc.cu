@@ -112,7 +112,10 @@ __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t& lo, uint32
 // EMIT (key weights): the grid also covers row tiles of floor(16 / g) positions,
 // every row's scores are stored for the key-weight kernel, partials are written
 // even for one segment, and the exponentials are fp32 (the weights are fp32
-// results; f16 exponentials are 2^-11 off each, and their arguments too).
+// results; f16 exponentials are 2^-11 off each, and their arguments too).  P is
+// rounded to bf16 for the P.V MMA over a bf16 V, whose element type it has to have
+// (2^-8 off each: outputs are 0.0023 of their scale off where fp32 products give
+// 0.0017, their rounding to bf16 included); the row sums and the key weights take the fp32 values.
 template <int D, int NSK, int NSV, int NR, bool PLAIN, bool F8, bool EMIT>
 __global__ void __launch_bounds__(F8 ? kThreadsF8 : kThreadsD, F8 ? 2 : 1)   // two CTAs per SM
 decode_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,

@@ -22,11 +22,15 @@
 // boundary cuts has several pieces; each leaves (m, l, o) in the workspace and
 // merge_kernel joins them in piece order.
 //
-// Measured: the 64-request decode batch (270 k keys, 32 / 8 heads, d = 128, 346 MB)
-// takes 78 us and 82 per call with the merge, 4.2 TB/s.  The copies alone take
-// about 80: 20 us to start, to drain unevenly and to merge, then 6.4 TB/s; the
-// instructions (360 per warp and 16 keys: K about 107, V 134) fill 58 % of the
-// issue slots of the 12 warps that 162 registers leave an SM.  Four CTAs per SM
+// Measured: calls on the 64-request decode batch (270 k keys, 32 / 8 heads, d =
+// 128, 346 MB) take 83 us with the merge, 4.2 TB/s; with two and four times the
+// requests 15 us and 5.1 TB/s.  The same calls with the products and the softmax
+// left out take 63 us, or 10 us and 6.5 TB/s (4 requests of 30,000 to 65,535 keys
+// at d = 256: 42 and 31; one request of 1,000 keys: 12.5 and 10.4).  What the
+// instructions add is latency as much as issue: 360 per warp and 16 keys (K about
+// 107, V 134) fill 58 % of the issue slots of the 12 warps that 162 registers
+// leave an SM, and a warp's two stages of copies cover little more than one step
+// of them.  Four CTAs per SM
 // were slower (115 us against 104 then), and so was claiming the last quarter of
 // the steps dynamically (124 against 86: a change of piece waits 4 us).
 //
@@ -699,7 +703,8 @@ fp4_kernel(const FwdParams p) {
             }
 
             // P = 2^(x - m): fp32 into the row sums, f16 into the MMA (11 bits;
-            // m trails the maximum by at most 8, so P <= 2^8).
+            // m trails the maximum by at most 8, so P <= 2^8.  P below 2^-14 is off
+            // by up to 2^-25, of a row sum that is at least 1).
             uint32_t pb[2][NT][2];
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt)

@@ -29,7 +29,10 @@ cudaError_t launch_fp4(const Fp4Plan& plan, const FwdParams& p, cudaStream_t str
 // (us, register / tcgen05): 16 sequences of 4096 keys, 8 KV heads, d = 128, 16
 // rows 43 / 49, 32 rows 59 / 49, 64 rows 100 / 49; 4 of 30000, 2 heads, d = 256,
 // 16 rows 58 / 78, 32 rows 86 / 80; 32 of 2000, 2 heads, d = 64, 32 rows 24 / 27,
-// 64 rows 31 / 27.
+// 64 rows 31 / 27.  One limit for every d: at d = 64 the crossing lies between 32
+// and 64 rows, and calls between pay up to 12 % for it.  The choice is the call's,
+// by its longest chunk: a batch of single tokens with one chunk in it takes
+// 128-row tiles for all.
 constexpr int kFp4RowsMin = 25;
 
 struct Fp4RowsPlan {

@@ -453,7 +453,8 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                     alpha = fast_exp2(m - top);
                     m = top;
                 }
-                // Second pass: P = 2^(x - m), fp32 into the row sum, f16 over
+                // Second pass: P = 2^(x - m), fp32 into the row sum, f16 (below
+                // 2^-14 off by up to 2^-25, of a sum that is at least 1) over
                 // columns of S that have been read (16 of P for 32 of S).
                 const float mu = m == -INFINITY ? 0.f : m;
                 const float2 f2 = make_float2(GEN ? 1.f : fac, GEN ? 1.f : fac), nm2 = make_float2(-mu, -mu);
@@ -592,7 +593,9 @@ bool plan_fp4_rows(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4R
     // weights included, 8 KV heads, 128 rows (us at 2 / 3 / 4 / 6 / 8 segments): 8
     // sequences of 12000 keys 148 / 179 / 161 / 171 / 179, of 1000 to 12000 120 /
     // 105 / 118 / 113 / 118; 4 of 12000 120 / 105 / 95 / 116 / 108, of 1000 to 12000
-    // 108 / 93 / 83 / 97 / 91.
+    // 108 / 93 / 83 / 97 / 91.  (All at d = 128: at d = 256, where a tile is 64 keys,
+    // the count is as if two tiles were one.  A window is not looked at: segments
+    // that hold none of its keys leave at once, the others share it.)
     const int64_t base = (int64_t)p.hk * p.num_seqs * tiles;
     const int64_t key_tiles = (p.max_seqlen_k + 127) / 128;
     int64_t splits = 1;

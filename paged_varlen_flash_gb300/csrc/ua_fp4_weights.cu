@@ -11,7 +11,8 @@
 // keys, 8 to 32 query tokens, 133 / 124; 16 of 4096, 32 tokens, 172 / 122; 2 of 6000,
 // 200 tokens, 357 / 179; one prompt of 1000 tokens 1095 / 210; one of 30000 keys, 8
 // tokens, 61 / 65; 4 of 9000, 2 KV heads, d = 256, 96 / 81 and with a softcap (a
-// second tanh per score) 119 / 138.
+// second tanh per score) 119 / 138.  Every call of the tcgen05 attention kernel
+// takes this one, the two slower kinds with it: that kernel stores no scores.
 // What bounds it: a CTA starts in 5 us (Q, the rows' denominators, the first
 // pages); then 1.3 us per key tile with two CTAs on the SM, half conversion and
 // half exponentials.
