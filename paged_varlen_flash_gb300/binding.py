@@ -463,9 +463,11 @@ class Problem:
         _check(v_new, "v_new", "torch.bfloat16", device)
         if _token_stride(v_new, "v_new", total_q, self.num_kv_heads, self.head_size) != stride:
             raise ValueError("k_new and v_new must share a token stride")
-        st = ua_cache_store(self.handle, k_new, v_new, stride, k_cache, v_cache, block_table,
-                            cu_seqlens_q, seqused_k, num_seqs, total_q, max_seqlen_q,
-                            max_seqlen_k, stream)
+        # A decode step's store waits for the host: no call more than it takes.
+        st = load_library().ua_cache_store(
+            self.handle, k_new.data_ptr(), v_new.data_ptr(), stride, k_cache.data_ptr(),
+            v_cache.data_ptr(), block_table.data_ptr(), cu_seqlens_q.data_ptr(),
+            seqused_k.data_ptr(), num_seqs, total_q, max_seqlen_q, max_seqlen_k, _stream(stream))
         if st != UA_OK:
             raise UAError(st, "ua_cache_store")
 
@@ -488,9 +490,10 @@ class Problem:
             if begin.numel() < num_seqs or not begin.is_contiguous():
                 raise ValueError("begin must be a contiguous [num_seqs]")
             _check(begin, "begin", "torch.int32", device)
-        st = ua_cache_expand(self.handle, k_cache, v_cache, block_table, seqused_k, begin,
-                             num_seqs, max_keys, k_out, v_out, out_block_table,
-                             step[0], shape[0], stream)
+        st = load_library().ua_cache_expand(
+            self.handle, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+            seqused_k.data_ptr(), _ptr(begin), num_seqs, max_keys, k_out.data_ptr(),
+            v_out.data_ptr(), out_block_table.data_ptr(), step[0], shape[0], _stream(stream))
         if st != UA_OK:
             raise UAError(st, "ua_cache_expand")
 
@@ -498,7 +501,8 @@ class Problem:
                     weights_in, weights_out, budget, recent, kept, seqused_out,
                     dst_block_table=None, stream=None):
         """Keep ``budget`` keys of every (sequence, KV head) by weight, in place
-        or into ``dst_block_table``; ``kept`` int32 [num_seqs, H_k, budget]."""
+        or into ``dst_block_table`` (rows as far apart as block_table's); ``kept``
+        int32 [num_seqs, H_k, budget]."""
         rows = num_seqs, self.num_kv_heads, max_seqlen_k, block_table
         stride = _weight_rows(weights_in, "weights_in", *rows)
         if _weight_rows(weights_out, "weights_out", *rows) != stride:
