@@ -149,3 +149,46 @@ def test_graphs_of_one_problem_replayed_in_turn():
     assert p.check_device_error() == 0
     for (w, o), (ww, wo) in zip(results, want):
         assert torch.equal(w, ww) and torch.equal(o.view(torch.int16), wo.view(torch.int16))
+
+
+@pytest.mark.parametrize("kind,nq", [("fp4", 1), ("fp4", 40), ("bf16", 1), ("bf16", 9), ("fp8", 2)])
+def test_the_same_calls_on_blocks_past_4_gib(kind, nq):
+    """Store, weighed attention, eviction (into other blocks, then in place) and expansion on
+    blocks beyond 2^32 bytes of the cache: the bits of the same calls on a small cache."""
+    sk = (130, 70, 200)
+    bt = Batch(380, kind, 8, 2, 128, 16, (nq,) * 3, sk, 0.5, 0.25, spare=40).device()
+    shift = (1 << 32) // (bt.d_k[0].numel() * bt.d_k.element_size()) + 3
+    pages = torch.zeros(bt.blocks, 16, 2, 128, dtype=torch.bfloat16, device="cuda")
+    kn, vn = bt.new_rows("k"), bt.new_rows("v")
+    dst = torch.full_like(bt.d_table, -1)
+    dst[:, :6] = torch.from_numpy(bt.spare_ids[:18].astype(np.int32)).cuda().view(3, 6)
+    results = []
+    for off in (0, shift):
+        k, v = (torch.zeros(off + bt.blocks, *c.shape[1:], dtype=c.dtype, device="cuda") for c in (bt.d_k, bt.d_v))
+        k[off:], v[off:] = bt.d_k, bt.d_v
+        move = lambda t: torch.where(t >= 0, t + off, -1).to(torch.int32)     # noqa: E731
+        table, to = move(bt.d_table), move(dst)
+        p = ua.Problem(8, 2, 128, 16, off + bt.blocks, 3, bt.width, 3 * nq,
+                       ua.UA_FLAG_CAUSAL | ua.UA_FLAG_KEY_WEIGHTS, bt.scale, kv_dtype=ua_dtype(kind),
+                       k_scale=bt.kscale, v_scale=bt.vscale)
+        w, kept = torch.zeros(3, 2, 200, device="cuda"), torch.zeros(3, 2, 90, dtype=torch.int32, device="cuda")
+        kept2 = torch.zeros(3, 2, 33, dtype=torch.int32, device="cuda")
+        used, out = bt.d_sk.clone(), torch.zeros_like(bt.d_q)
+        ko, vo = pages.clone(), pages.clone()
+        p.cache_store(kn, vn, k, v, table, bt.d_cu, used, 3, 3 * nq, nq, 200)
+        p.forward_weights(bt.d_q, k, v, table, bt.d_cu, used, 3, 3 * nq, nq, 200, ua.UA_FLAG_CAUSAL, None, w, out=out)
+        p.cache_evict(k, v, table, used, 3, 200, w, w, 90, 7, kept, used, dst_block_table=to)
+        p.cache_evict(k, v, to, used, 3, 90, w, w, 33, 5, kept2, used)
+        p.cache_expand(k, v, to, used, 3, 33, ko, vo, dst)
+        assert p.check_device_error() == 0
+        assert not bool(k[:off].view(torch.uint8).any()) and not bool(v[:off].view(torch.uint8).any())
+        results.append([t.clone().view(torch.uint8) for t in (k[off:], v[off:], out, w, kept, kept2, used, ko, vo)])
+        if off == 0:
+            compare(bt, out, None, bf16_p=kind == "bf16")
+        del k, v
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+
+
+def ua_dtype(kind):
+    return {"bf16": ua.UA_DTYPE_BF16, "fp8": ua.UA_DTYPE_FP8_E4M3, "fp4": ua.UA_DTYPE_FP4_E2M1}[kind]

@@ -279,3 +279,17 @@ def test_long_evictions(case, dst):
         touched[to[s, :kblk[s]].long()] = True
     for now, old in ((k, k0), (v, v0)):
         assert torch.equal(now[~touched].view(torch.uint8), old[~touched].view(torch.uint8))
+
+
+def test_scores_past_2_to_the_31():
+    """A prompt chunk whose stored scores are more elements than 32 bits count."""
+    sq, sk, hq = 1000, 140000, 16
+    bt = LongBatch(490, "bf16", hq, 4, 64, 64, (sq,), (sk,))
+    assert sq * hq * sk > 1 << 31
+    p = bt.problem(ua.UA_FLAG_CAUSAL | ua.UA_FLAG_KEY_WEIGHTS)
+    w = torch.full((1, 4, sk), -7.0, device="cuda")
+    out = p.forward_weights(*bt.args(), ua.UA_FLAG_CAUSAL, None, w)
+    assert p.check_device_error() == 0
+    ref = bt.reference(0)
+    check(bt, 0, out, ref, bf16_p=True)
+    check_weights(bt, 0, w[0], torch.zeros_like(ref[3]), ref)
