@@ -85,7 +85,10 @@ enum {
     UA_DEVERR_BOUNDS = 1u << 3,   /* S_q > max_seqlen_q or S_k > max_seqlen_k or
                                      S_k > max_blocks_per_seq * b: rows of s written as 0
                                      where addressable */
-    UA_DEVERR_TIMEOUT = 1u << 4   /* a bounded on-chip wait gave up; results unspecified */
+    UA_DEVERR_TIMEOUT = 1u << 4,  /* a bounded on-chip wait gave up; results unspecified */
+    UA_DEVERR_TREE = 1u << 5,     /* a draft tree's parent, accepted node or position out of range */
+    UA_DEVERR_POOL = 1u << 6      /* ua_plan_step: a pool count outside [0, num_blocks], or more
+                                     blocks given back than the pool has room for */
 };
 
 /* Element types.  Q, O: bf16.  K/V caches: bf16, or fp8 e4m3 codes (one byte
@@ -256,8 +259,8 @@ ua_status ua_check_device_error(ua_problem *p, void *stream, int32_t *code);
 
 /*
  * Number of kernel launches the most recent ua_forward, ua_forward_host,
- * ua_forward_topk, ua_forward_weights or ua_cache_* call enqueued (for launch
- * accounting in benchmarks).
+ * ua_forward_topk, ua_forward_weights, ua_forward_tree, ua_plan_step, ua_rope_store
+ * or ua_cache_* call enqueued (for launch accounting in benchmarks).
  */
 int32_t ua_last_launch_count(const ua_problem *p);
 
@@ -485,6 +488,148 @@ ua_status ua_cache_evict(ua_problem *p, void *k_cache, void *v_cache, const int3
                          int32_t num_seqs, int32_t max_seqlen_k, const float *weights_in,
                          float *weights_out, int64_t weight_stride, int32_t budget,
                          int32_t recent, int32_t *kept, int32_t *seqused_out, void *stream);
+
+/*
+ * ---- a step of speculative decoding: blocks and slots, rotary store, draft trees ----
+ * (Additions of this library.)
+ *
+ * A serving step hands out blocks and slots (ua_plan_step), rotates q and k and
+ * stores k and v (ua_rope_store), attends (ua_forward, or ua_forward_tree for a tree
+ * of drafted tokens), and keeps the accepted branch (ua_cache_accept).  What the
+ * cache calls above say about streams, workspace, alignment and errors holds here.
+ *
+ * A draft tree is given by its nodes' parents: int32, one row per sequence,
+ * parents[s * parents_stride + i] for node i, which is the i-th query row of sequence
+ * s.  A parent stands in front of its children; -1 marks a node without one (there may
+ * be several).  A tree has at most 1024 nodes.
+ *
+ * ua_plan_step -- give the sequences of a step their blocks and tokens.  Sequence s
+ * has ctx_lens[s] cached keys and wants new_lens[s] more; it needs
+ * ceil((ctx + new) / b) blocks.
+ *   block_table    int32 [num_seqs, max_blocks_per_seq], in and out: ids of new blocks
+ *                  are written behind the held ones
+ *   blocks_held    int32 [num_seqs], in and out: blocks that the sequences have
+ *   free_blocks    int32 [num_blocks], in and out: a stack of *free_count block ids
+ *   free_count     int32 [1], in and out
+ * Sequences that hold more than they need give their last blocks back, and these lie on
+ * the stack with the first of them on top (first sequence, lowest position); then
+ * sequences in their order take what they lack from the top.  A sequence that needs
+ * more blocks than are left, counting what those in front of it asked for, gets no
+ * tokens and keeps what it has; sequences that need no further block always get theirs.
+ * (A finished request passes ctx = new = 0, rejected drafts simply a smaller ctx in
+ * the next step.  A step that is followed by one with new = 0 leaves the pool as it
+ * was.)
+ *   parents        draft trees of the new tokens, parents_stride >= their number; or
+ *                  NULL: chains
+ *   granted        int32 [num_seqs] out: new_lens[s], or 0; may be new_lens
+ *   cu_seqlens_q   int32 [num_seqs + 1] out: prefix sums of granted
+ *   seqused_k      int32 [num_seqs] out: ctx + granted; may be ctx_lens
+ *   positions      int32 [max_tokens] out: ctx + depth in the tree (a chain: ctx + i) of
+ *                  every packed token
+ *   slots          int64 [max_tokens] out: block * b + slot of every packed token's key
+ *   tree_mask      uint32 [max_tokens, mask_stride] out, or NULL: bit c % 32 of word
+ *                  c / 32 of a token's row is set for the nodes c on its branch; rows of
+ *                  tokens that are not there are left as they are
+ *   max_tokens     host-side bound on the tokens, <= max_total_q; places behind the last
+ *                  token get position 0 and slot -1
+ * Malformed lengths (negative, past max_blocks_per_seq * b, past parents_stride or 32 *
+ * mask_stride, or tokens past max_tokens) get nothing (UA_DEVERR_BOUNDS), a bad block id
+ * the slot -1 (UA_DEVERR_BLOCK_ID), a bad parent ends its branch (UA_DEVERR_TREE).
+ * Needs num_seqs <= 16384 (else UA_ERR_UNSUPPORTED).  Arrays may not overlap otherwise.
+ */
+ua_status ua_plan_step(ua_problem *p, int32_t *block_table, int32_t *blocks_held,
+                       int32_t *free_blocks, int32_t *free_count, const int32_t *ctx_lens,
+                       const int32_t *new_lens, const int32_t *parents, int64_t parents_stride,
+                       int32_t num_seqs, int64_t max_tokens, int32_t *granted,
+                       int32_t *cu_seqlens_q, int32_t *seqused_k, int32_t *positions,
+                       int64_t *slots, uint32_t *tree_mask, int32_t mask_stride, void *stream);
+
+/* Which dims of a head form a rotated pair, with n frequencies. */
+enum {
+    UA_ROPE_HALF = 0,    /* (i, i + n) */
+    UA_ROPE_PAIRS = 1    /* (2i, 2i + 1) */
+};
+
+/*
+ * ua_set_rope -- the rotary frequencies of later ua_rope_store calls: inv_freq[i]
+ * (host array, radians per position, 0 <= inv_freq[i] <= 6) for pair i < n, where 2n is
+ * the number of rotated dims: a multiple of 16, at most d (else UA_ERR_UNSUPPORTED).
+ * Scalings for long contexts are other frequencies and, where they have one, a factor
+ * `magnitude` (finite) on cos and sin.  The values are copied; calls that were captured
+ * into a graph keep those they were captured with.
+ */
+ua_status ua_set_rope(ua_problem *p, const double *inv_freq, int32_t n, uint32_t layout,
+                      float magnitude);
+
+/*
+ * ua_rope_store -- rotate q and k by the tokens' positions and write k and v into the
+ * caches.  A pair (x, y) with angle phi = position * inv_freq[i] becomes
+ *     magnitude * (x cos phi - y sin phi, x sin phi + y cos phi)
+ * in fp32, rounded once to bf16; other dims stay.  The angle keeps its fraction of a
+ * turn to 2^-32 at any position.  Keys are then stored like ua_cache_store does, from
+ * the rounded values.
+ *   q              bf16 [total_q, H_q, d], tokens q_stride elements apart
+ *   k_new, v_new   bf16 [total_q, H_k, d], tokens kv_stride elements apart
+ *   q_out          bf16 [total_q, H_q, d], tokens out_stride elements apart; q itself
+ *                  with the same stride, or disjoint from every input
+ *   positions      int32 [total_q]
+ *   slots          int64 [total_q]: block * b + slot; negative: k and v are not stored
+ *                  (q is rotated all the same).  A slot past the cache is dropped
+ *                  (UA_DEVERR_BLOCK_ID); no slot may be named twice
+ * Strides are multiples of 8 and at least a token's row; q, k_new, v_new, q_out and the
+ * caches are 16-byte aligned.  ua_set_rope comes first (else UA_ERR_INVALID_ARG).
+ */
+ua_status ua_rope_store(ua_problem *p, const void *q, int64_t q_stride, const void *k_new,
+                        const void *v_new, int64_t kv_stride, const int32_t *positions,
+                        const int64_t *slots, int64_t total_q, void *q_out, int64_t out_stride,
+                        void *k_cache, void *v_cache, void *stream);
+
+/*
+ * ua_forward_tree -- ua_forward where a query row sees all ctx keys of its context and,
+ * of its chunk's own keys, those that its row of tree_mask names: bit c % 32 of word
+ * c / 32 stands for key ctx + c, c < S_q.  Any mask will do; a row that sees nothing
+ * gets O = 0.
+ *   tree_mask      uint32 [total_q, mask_stride], 32 * mask_stride >= max_seqlen_q
+ *   positions      int32 [total_q], positions of the query rows, within [ctx, S_k)
+ *                  (others are moved there, UA_DEVERR_TREE); needed with
+ *                  UA_FLAG_WINDOW or UA_FLAG_ALIBI, else not read.  A context key's
+ *                  position is j, a chunk key's that of its row: the window keeps keys
+ *                  from position(row) - W + 1 on, ALiBi adds slope * (position - ctx)
+ * The mask takes the place of the causal rule: flags must have UA_FLAG_CAUSAL (else
+ * UA_ERR_INVALID_ARG); UA_FLAG_QQ_BIAS is not served (UA_ERR_UNSUPPORTED).  Needs a bf16
+ * cache, path AUTO, g <= 128, max_seqlen_q <= 1024, max_seqlen_k <= 2^30 and H_k <= 65535
+ * (else UA_ERR_UNSUPPORTED).  A value that is not finite reaches the rows that see its
+ * key and no others.
+ */
+ua_status ua_forward_tree(ua_problem *p, const void *q, const void *k_cache, const void *v_cache,
+                          const int32_t *block_table, const int32_t *cu_seqlens_q,
+                          const int32_t *seqused_k, int32_t num_seqs, int64_t total_q,
+                          int32_t max_seqlen_q, int32_t max_seqlen_k, const uint32_t *tree_mask,
+                          int32_t mask_stride, const int32_t *positions, uint32_t flags,
+                          const float *sinks, const float *alibi_slopes, void *out, void *stream);
+
+/*
+ * ua_cache_accept -- keep one branch of every draft tree: the nodes from the root to
+ * last[s].  With the branch r_0 < r_1 < ... the K and V rows of key ctx + r_t move to
+ * key ctx + t, where ctx = S_k - S_q; other rows are left as they are.  (Keys stored by
+ * ua_rope_store with a node's position are rotated for where they arrive.)
+ *   parents        the trees, parents_stride >= max_seqlen_q
+ *   last           int32 [num_seqs]: the deepest accepted node, -1: none; not read for
+ *                  sequences without query rows
+ *   path           int32 [num_seqs, path_stride] out: r_0, r_1, ..., then -1
+ *   accepted       int32 [num_seqs] out: length of the branch
+ *   seqused_out    int32 [num_seqs] out: ctx + accepted; may be seqused_k
+ * A bad parent or last node accepts nothing (UA_DEVERR_TREE), nor does a branch longer
+ * than path_stride (UA_DEVERR_BOUNDS); malformed lengths get seqused_out 0.  Rows whose
+ * block id is out of range are not moved (UA_DEVERR_BLOCK_ID).  Needs max_seqlen_q <=
+ * 1024 (else UA_ERR_UNSUPPORTED).
+ */
+ua_status ua_cache_accept(ua_problem *p, void *k_cache, void *v_cache, const int32_t *block_table,
+                          const int32_t *cu_seqlens_q, const int32_t *seqused_k,
+                          const int32_t *parents, int64_t parents_stride, const int32_t *last,
+                          int32_t num_seqs, int64_t total_q, int32_t max_seqlen_q,
+                          int32_t max_seqlen_k, int32_t *path, int32_t path_stride,
+                          int32_t *accepted, int32_t *seqused_out, void *stream);
 
 /* Free the workspace and the problem.  NULL is a no-op. */
 void ua_destroy(ua_problem *p);

@@ -6,6 +6,7 @@ in that library's CUDA kernels.  Tensors are torch tensors (device memory for
 streams or raw ``cudaStream_t`` integers.
 """
 import ctypes
+import math
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -27,6 +28,11 @@ UA_DEVERR_BLOCK_ID = 1 << 1
 UA_DEVERR_CU_SEQLENS = 1 << 2
 UA_DEVERR_BOUNDS = 1 << 3
 UA_DEVERR_TIMEOUT = 1 << 4
+UA_DEVERR_TREE = 1 << 5
+UA_DEVERR_POOL = 1 << 6
+
+UA_ROPE_HALF = 0
+UA_ROPE_PAIRS = 1
 
 UA_DTYPE_BF16 = 0
 UA_DTYPE_FP8_E4M3 = 1
@@ -113,6 +119,16 @@ def load_library():
     lib.ua_cache_expand.restype = ctypes.c_int
     lib.ua_cache_evict.argtypes = [vp] * 6 + [i32, i32, vp, vp, i64, i32, i32, vp, vp, vp]
     lib.ua_cache_evict.restype = ctypes.c_int
+    lib.ua_plan_step.argtypes = [vp] * 8 + [i64, i32, i64] + [vp] * 6 + [i32, vp]
+    lib.ua_plan_step.restype = ctypes.c_int
+    lib.ua_set_rope.argtypes = [vp, ctypes.POINTER(ctypes.c_double), i32, u32, f32]
+    lib.ua_set_rope.restype = ctypes.c_int
+    lib.ua_rope_store.argtypes = [vp, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp, vp]
+    lib.ua_rope_store.restype = ctypes.c_int
+    lib.ua_forward_tree.argtypes = [vp] * 7 + [i32, i64, i32, i32, vp, i32, vp, u32, vp, vp, vp, vp]
+    lib.ua_forward_tree.restype = ctypes.c_int
+    lib.ua_cache_accept.argtypes = [vp] * 7 + [i64, vp, i32, i64, i32, i32, vp, i32, vp, vp, vp]
+    lib.ua_cache_accept.restype = ctypes.c_int
     lib.ua_set_qq_bias.argtypes = [vp, vp, ctypes.c_int64, ctypes.c_int64]
     lib.ua_set_qq_bias.restype = ctypes.c_int
     lib.ua_debug_stall_data_waits.argtypes = [vp, i32, i64]
@@ -263,6 +279,93 @@ def ua_cache_evict(problem, k_cache, v_cache, block_table, dst_block_table, sequ
         weight_stride, budget, recent, _ptr(kept), _ptr(seqused_out), _stream(stream))
 
 
+def ua_plan_step(problem, block_table, blocks_held, free_blocks, free_count, ctx_lens, new_lens, parents,
+                 parents_stride, num_seqs, max_tokens, granted, cu_seqlens_q, seqused_k, positions, slots,
+                 tree_mask, mask_stride, stream=None):
+    """Enqueue the hand-out of a step's blocks, slots, positions and ancestor masks.
+    Returns the status."""
+    return load_library().ua_plan_step(
+        problem, _ptr(block_table), _ptr(blocks_held), _ptr(free_blocks), _ptr(free_count), _ptr(ctx_lens),
+        _ptr(new_lens), _ptr(parents), parents_stride, num_seqs, max_tokens, _ptr(granted), _ptr(cu_seqlens_q),
+        _ptr(seqused_k), _ptr(positions), _ptr(slots), _ptr(tree_mask), mask_stride, _stream(stream))
+
+
+def ua_set_rope(problem, inv_freq, layout=UA_ROPE_HALF, magnitude=1.0):
+    """Set the rotary frequencies (a sequence of floats, radians per position) of
+    later ``ua_rope_store`` calls.  Returns the status."""
+    values = (ctypes.c_double * len(inv_freq))(*inv_freq)
+    return load_library().ua_set_rope(problem, values, len(inv_freq), layout, magnitude)
+
+
+def ua_rope_store(problem, q, q_stride, k_new, v_new, kv_stride, positions, slots, total_q, q_out, out_stride,
+                  k_cache, v_cache, stream=None):
+    """Enqueue the rotation of q and k and the store of k and v.  Returns the status."""
+    return load_library().ua_rope_store(
+        problem, _ptr(q), q_stride, _ptr(k_new), _ptr(v_new), kv_stride, _ptr(positions), _ptr(slots), total_q,
+        _ptr(q_out), out_stride, _ptr(k_cache), _ptr(v_cache), _stream(stream))
+
+
+def ua_forward_tree(problem, q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, num_seqs, total_q,
+                    max_seqlen_q, max_seqlen_k, tree_mask, mask_stride, positions, flags, sinks, alibi_slopes, out,
+                    stream=None):
+    """Enqueue attention for trees of drafted tokens.  Returns the status."""
+    return load_library().ua_forward_tree(
+        problem, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(cu_seqlens_q), _ptr(seqused_k),
+        num_seqs, total_q, max_seqlen_q, max_seqlen_k, _ptr(tree_mask), mask_stride, _ptr(positions), flags,
+        _ptr(sinks), _ptr(alibi_slopes), _ptr(out), _stream(stream))
+
+
+def ua_cache_accept(problem, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, parents, parents_stride, last,
+                    num_seqs, total_q, max_seqlen_q, max_seqlen_k, path, path_stride, accepted, seqused_out,
+                    stream=None):
+    """Enqueue the move of the accepted branches.  Returns the status."""
+    return load_library().ua_cache_accept(
+        problem, _ptr(k_cache), _ptr(v_cache), _ptr(block_table), _ptr(cu_seqlens_q), _ptr(seqused_k), _ptr(parents),
+        parents_stride, _ptr(last), num_seqs, total_q, max_seqlen_q, max_seqlen_k, _ptr(path), path_stride,
+        _ptr(accepted), _ptr(seqused_out), _stream(stream))
+
+
+def rope_frequencies(rotated, base=10000.0, scaling=None, factor=1.0, trained=0, low=1.0, high=4.0):
+    """Frequencies (radians per position) of ``rotated`` dims and the factor on cos
+    and sin, for ``Problem.set_rope``: base^(-2i / rotated), and with ``scaling``
+
+    * ``"linear"``  all divided by ``factor`` (positions interpolated);
+    * ``"ntk"``     the base raised to base * factor^(rotated / (rotated - 2)), which
+                    divides the lowest frequency by ``factor`` and keeps the highest;
+    * ``"bands"``   divided by ``factor`` where fewer than ``low`` turns fit the
+                    ``trained`` context, kept from ``high`` turns on, linear between;
+    * ``"yarn"``    the same between the dims of ``high`` and ``low`` turns, linear in
+                    the dim, and cos and sin times 0.1 ln(factor) + 1.
+    """
+    n = rotated // 2
+    if rotated < 2 or rotated % 2 or base <= 0 or factor <= 0:
+        raise ValueError("rotated must be even and positive, base and factor positive")
+    if scaling == "ntk":
+        if rotated < 4:
+            raise ValueError("ntk needs at least two pairs")
+        base *= factor ** (rotated / (rotated - 2))
+    freq = [base ** (-i / n) for i in range(n)]
+    if scaling in (None, "ntk"):
+        return freq, 1.0
+    if scaling == "linear":
+        return [f / factor for f in freq], 1.0
+    if scaling not in ("bands", "yarn"):
+        raise ValueError("scaling must be None, 'linear', 'ntk', 'bands' or 'yarn'")
+    if trained <= 0 or not 0 < low < high:
+        raise ValueError("%s needs the trained context and 0 < low < high" % scaling)
+    turns = [trained * f / (2 * math.pi) for f in freq]
+    if scaling == "bands":
+        keep = [(t - low) / (high - low) for t in turns]
+    else:
+        # The (fractional) dim at which `turns` turns fit the trained context.
+        dim = lambda t: n * math.log(trained / (2 * math.pi * t)) / math.log(base)  # noqa: E731
+        first, end = max(math.floor(dim(high)), 0), min(math.ceil(dim(low)), n - 1)
+        keep = [1 - (i - first) / max(end - first, 1e-3) for i in range(n)]
+    keep = [min(1.0, max(0.0, k)) for k in keep]
+    return ([f * (k + (1 - k) / factor) for f, k in zip(freq, keep)],
+            0.1 * math.log(factor) + 1.0 if scaling == "yarn" and factor > 1 else 1.0)
+
+
 def cache_shape(num_blocks, num_kv_heads, head_size, block_size, kv_dtype=UA_DTYPE_BF16):
     """Shape of one K or V cache: bf16 or uint8 [num_blocks, b, H_k, d], or for
     the 4-bit format uint8 [num_blocks, H_k, bytes of a (block, KV head) page]."""
@@ -305,6 +408,33 @@ def _check(t, name, kind, device):
     dtype = t.dtype
     if (_type_names.get(dtype) or _type_names.setdefault(dtype, str(dtype))) != kind or t.get_device() != device:
         raise ValueError("%s must be %s, on the device of the other tensors" % (name, kind))
+
+
+def _vector(t, name, n, kind, device):
+    """Refuse all but a contiguous tensor of at least n elements of that type there."""
+    if t.numel() < n or not t.is_contiguous():
+        raise ValueError("%s must be contiguous, with at least %d elements" % (name, n))
+    _check(t, name, kind, device)
+
+
+def _tree_rows(parents, num_seqs, device):
+    """Elements between the rows of the trees' parents [num_seqs, n]."""
+    shape, stride = parents.shape, parents.stride()
+    if len(shape) != 2 or shape[0] < num_seqs or shape[1] < 1 or (shape[1] > 1 and stride[1] != 1) or (
+            shape[0] > 1 and stride[0] < shape[1]):
+        raise ValueError("parents must be [num_seqs, nodes] with unit inner stride")
+    _check(parents, "parents", "torch.int32", device)
+    return stride[0] if shape[0] > 1 else shape[1]
+
+
+def _mask_stride(mask, tokens, device):
+    """Words between the rows of a tree mask [tokens, words]."""
+    shape, stride = mask.shape, mask.stride()
+    if len(shape) != 2 or shape[0] < tokens or shape[1] < 1 or (shape[1] > 1 and stride[1] != 1) or (
+            shape[0] > 1 and stride[0] != shape[1]):
+        raise ValueError("tree_mask must be a contiguous [tokens, words]")
+    _check(mask, "tree_mask", "torch.uint32" if str(mask.dtype) == "torch.uint32" else "torch.int32", device)
+    return shape[1]
 
 
 def _weight_rows(t, name, num_seqs, num_kv_heads, n, like):
@@ -388,6 +518,7 @@ class Problem:
         self.flags = flags
         self.head_size = head_size
         self.block_size = block_size
+        self.num_blocks = num_blocks
         self.max_blocks_per_seq = max_blocks_per_seq
         self.num_q_heads = num_q_heads
         self.num_kv_heads = num_kv_heads
@@ -526,6 +657,111 @@ class Problem:
                             recent, kept, seqused_out, stream)
         if st != UA_OK:
             raise UAError(st, "ua_cache_evict")
+
+    def plan_step(self, block_table, blocks_held, free_blocks, free_count, ctx_lens, new_lens, num_seqs, max_tokens,
+                  granted, cu_seqlens_q, seqused_k, positions, slots, parents=None, tree_mask=None, stream=None):
+        """Give the sequences of a step their blocks and tokens: ``new_lens`` tokens
+        behind ``ctx_lens`` keys, drafted as chains or as trees (``parents`` int32
+        [num_seqs, nodes], -1 for a node without parent).  In and out: ``block_table``,
+        ``blocks_held``, ``free_blocks`` (a stack of ``free_count`` ids); out:
+        ``granted``, ``cu_seqlens_q``, ``seqused_k``, and per packed token ``positions``,
+        ``slots`` (int64) and ``tree_mask`` (int32 or uint32 [max_tokens, words])."""
+        device = block_table.get_device()
+        shape, step = block_table.shape, block_table.stride()
+        if (len(shape) != 2 or shape[0] < num_seqs or shape[1] > self.max_blocks_per_seq or
+                (shape[1] < self.max_blocks_per_seq and num_seqs > 0) or (shape[1] > 1 and step[1] != 1) or
+                (num_seqs > 1 and step[0] != self.max_blocks_per_seq)):
+            raise ValueError("block_table must be [num_seqs, max_blocks_per_seq]")
+        _check(block_table, "block_table", "torch.int32", device)
+        for t, name, n in ((blocks_held, "blocks_held", num_seqs), (free_blocks, "free_blocks", self.num_blocks),
+                           (free_count, "free_count", 1), (ctx_lens, "ctx_lens", num_seqs),
+                           (new_lens, "new_lens", num_seqs), (granted, "granted", num_seqs),
+                           (cu_seqlens_q, "cu_seqlens_q", num_seqs + 1), (seqused_k, "seqused_k", num_seqs),
+                           (positions, "positions", max_tokens)):
+            _vector(t, name, n, "torch.int32", device)
+        _vector(slots, "slots", max_tokens, "torch.int64", device)
+        stride = _tree_rows(parents, num_seqs, device) if parents is not None else 0
+        words = _mask_stride(tree_mask, max_tokens, device) if tree_mask is not None else 0
+        st = ua_plan_step(self.handle, block_table, blocks_held, free_blocks, free_count, ctx_lens, new_lens, parents,
+                          stride, num_seqs, max_tokens, granted, cu_seqlens_q, seqused_k, positions, slots, tree_mask,
+                          words, stream)
+        if st != UA_OK:
+            raise UAError(st, "ua_plan_step")
+
+    def set_rope(self, inv_freq, layout=UA_ROPE_HALF, magnitude=1.0):
+        """Set the rotary frequencies of later ``rope_store`` calls: radians per
+        position of every pair (``rope_frequencies`` computes them), which dims form
+        a pair, and the factor on cos and sin."""
+        st = ua_set_rope(self.handle, inv_freq, layout, magnitude)
+        if st != UA_OK:
+            raise UAError(st, "ua_set_rope")
+
+    def rope_store(self, q, k_new, v_new, positions, slots, total_q, k_cache, v_cache, q_out=None, stream=None):
+        """Rotate q and k (bf16 [total_q, heads, d]; tokens may be strided) by
+        ``positions`` and write k and v to ``slots`` (int64; negative: not stored).
+        Returns the rotated q (``q_out``, which may be q)."""
+        device = k_cache.get_device()
+        q_stride = _token_stride(q, "q", total_q, self.num_q_heads, self.head_size)
+        stride = _token_stride(k_new, "k_new", total_q, self.num_kv_heads, self.head_size)
+        if _token_stride(v_new, "v_new", total_q, self.num_kv_heads, self.head_size) != stride:
+            raise ValueError("k_new and v_new must share a token stride")
+        if q_out is None:
+            import torch
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out_stride = _token_stride(q_out, "q_out", total_q, self.num_q_heads, self.head_size)
+        for t, name in ((q, "q"), (k_new, "k_new"), (v_new, "v_new"), (q_out, "q_out")):
+            _check(t, name, "torch.bfloat16", device)
+        _vector(positions, "positions", total_q, "torch.int32", device)
+        _vector(slots, "slots", total_q, "torch.int64", device)
+        st = load_library().ua_rope_store(
+            self.handle, q.data_ptr(), q_stride, k_new.data_ptr(), v_new.data_ptr(), stride, positions.data_ptr(),
+            slots.data_ptr(), total_q, q_out.data_ptr(), out_stride, k_cache.data_ptr(), v_cache.data_ptr(),
+            _stream(stream))
+        if st != UA_OK:
+            raise UAError(st, "ua_rope_store")
+        return q_out
+
+    def forward_tree(self, q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, num_seqs, total_q, max_seqlen_q,
+                     max_seqlen_k, flags, tree_mask, positions=None, sinks=None, alibi_slopes=None, out=None,
+                     stream=None):
+        """``forward`` for trees of drafted tokens: of its chunk's own keys a row sees
+        those whose bits its row of ``tree_mask`` (int32 or uint32 [total_q, words])
+        has.  ``positions`` (int32 [total_q]) are needed with a window or ALiBi."""
+        device = q.get_device()
+        words = _mask_stride(tree_mask, total_q, device)
+        if positions is not None:
+            _vector(positions, "positions", total_q, "torch.int32", device)
+        if out is None:
+            import torch
+            out = torch.empty_like(q)
+        st = ua_forward_tree(self.handle, q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, num_seqs, total_q,
+                             max_seqlen_q, max_seqlen_k, tree_mask, words, positions, flags, sinks, alibi_slopes, out,
+                             stream)
+        if st != UA_OK:
+            raise UAError(st, "ua_forward_tree")
+        return out
+
+    def cache_accept(self, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, parents, last, num_seqs, total_q,
+                     max_seqlen_q, max_seqlen_k, path, accepted, seqused_out, stream=None):
+        """Keep the branch that ends at node ``last`` of every tree: its rows move
+        right behind the context.  Out: ``path`` (int32 [num_seqs, n], -1 behind the
+        branch), ``accepted`` (its length) and ``seqused_out``."""
+        device = k_cache.get_device()
+        stride = _tree_rows(parents, num_seqs, device)
+        if parents.shape[1] < max_seqlen_q:
+            raise ValueError("parents must have a column per node")
+        if path.dim() != 2 or path.shape[0] != num_seqs or path.shape[1] < 1 or not path.is_contiguous():
+            raise ValueError("path must be a contiguous [num_seqs, n]")
+        _check(path, "path", "torch.int32", device)
+        for t, name, n in ((cu_seqlens_q, "cu_seqlens_q", num_seqs + 1), (seqused_k, "seqused_k", num_seqs),
+                           (last, "last", num_seqs), (accepted, "accepted", num_seqs),
+                           (seqused_out, "seqused_out", num_seqs)):
+            _vector(t, name, n, "torch.int32", device)
+        st = ua_cache_accept(self.handle, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, parents, stride, last,
+                             num_seqs, total_q, max_seqlen_q, max_seqlen_k, path, path.shape[1], accepted, seqused_out,
+                             stream)
+        if st != UA_OK:
+            raise UAError(st, "ua_cache_accept")
 
     def forward_workload(self, w, out=None, stream=None):
         """Forward on a device-resident ``workloads.Workload`` (through

@@ -12,15 +12,19 @@
 #include <cstring>
 #include <mutex>
 
+#include "ua_accept.h"
 #include "ua_cache.h"
 #include "ua_common.cuh"
 #include "ua_decode_tc.h"
 #include "ua_fp4.cuh"
 #include "ua_fp4.h"
+#include "ua_plan.h"
 #include "ua_prefill.h"
+#include "ua_rope.h"
 #include "ua_split.h"
 #include "ua_tmap.h"
 #include "ua_topk.h"
+#include "ua_tree.h"
 #include "ua_weights.h"
 
 namespace {
@@ -63,7 +67,7 @@ struct ua_problem {
     ua_problem_desc desc;
     int device = 0;
     int num_sms = 0;
-    int32_t* d_err = nullptr;
+    int32_t* d_err = nullptr;      // the error word, then ua_plan_step's count of finished CTAs
     float* d_ws = nullptr;
     size_t ws_bytes = 0;
     // scores of ua_forward_weights (UA_FLAG_KEY_WEIGHTS problems only)
@@ -87,6 +91,8 @@ struct ua_problem {
     const float* qq_bias = nullptr;
     int64_t qq_n = 0;
     int64_t qq_stride = 0;
+    // rotary frequencies set by ua_set_rope (n = 0: none)
+    ua::RopeTable rope{};
     // tensor maps of the most recent caches (re-encoded when the pointers change)
     const void* map_k_ptr = nullptr;
     const void* map_v_ptr = nullptr;
@@ -210,7 +216,7 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
                                           int64_t(1) << 30);
     p->work_cap = (int32_t)cap;
     const size_t work_bytes = (size_t)cap * sizeof(int2) + (size_t)(d->max_num_seqs + 1) * 4 + 16;
-    if (cudaMalloc(&p->d_err, sizeof(int32_t)) != cudaSuccess ||
+    if (cudaMalloc(&p->d_err, 2 * sizeof(int32_t)) != cudaSuccess ||
         cudaMalloc(&p->d_ws, p->ws_bytes) != cudaSuccess ||
         cudaMalloc(&p->d_work, work_bytes) != cudaSuccess ||
         (piece_bytes && cudaMalloc(&p->d_pieces, piece_bytes) != cudaSuccess) ||
@@ -223,7 +229,7 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
         delete p;
         return UA_ERR_OUT_OF_MEMORY;
     }
-    e = clear_now(p->d_err, sizeof(int32_t), p->d_pieces, piece_bytes);
+    e = clear_now(p->d_err, 2 * sizeof(int32_t), p->d_pieces, piece_bytes);
     if (e != cudaSuccess) {
         note_cuda(e, "ua_problem_create");
         cudaFree(p->d_err);
@@ -889,6 +895,198 @@ ua_status ua_cache_evict(ua_problem* p, void* k_cache, void* v_cache, const int3
     }
     p->last_launches = 2;
     p->last_path = ep.in_place ? "evict_in_place" : "evict";
+    return UA_OK;
+}
+
+ua_status ua_plan_step(ua_problem* p, int32_t* block_table, int32_t* blocks_held, int32_t* free_blocks,
+                       int32_t* free_count, const int32_t* ctx_lens, const int32_t* new_lens,
+                       const int32_t* parents, int64_t parents_stride, int32_t num_seqs, int64_t max_tokens,
+                       int32_t* granted, int32_t* cu_seqlens_q, int32_t* seqused_k, int32_t* positions,
+                       int64_t* slots, uint32_t* tree_mask, int32_t mask_stride, void* stream) {
+    if (!p) return UA_ERR_INVALID_ARG;
+    p->last_launches = 0;
+    p->last_path = "none";
+    const ua_problem_desc& d = p->desc;
+    if (num_seqs < 0 || num_seqs > d.max_num_seqs || max_tokens < 0 || max_tokens > d.max_total_q ||
+        (parents && parents_stride < 1) || (tree_mask && mask_stride < 1) || !on_device(p))
+        return UA_ERR_INVALID_ARG;
+    if (num_seqs == 0 && max_tokens == 0) return UA_OK;
+    if (num_seqs > ua::kMaxPlanSeqs || max_tokens > 0x7fffffff || (parents && parents_stride > 0x7fffffff))
+        return UA_ERR_UNSUPPORTED;
+    if (!free_blocks || !free_count || !cu_seqlens_q || (max_tokens && (!positions || !slots)) ||
+        (num_seqs && (!block_table || !blocks_held || !ctx_lens || !new_lens || !granted || !seqused_k)) ||
+        !words(block_table, blocks_held, free_blocks, free_count, ctx_lens, new_lens, parents, granted, cu_seqlens_q,
+               seqused_k, positions, tree_mask) ||
+        (reinterpret_cast<uintptr_t>(slots) & 7u) != 0)
+        return UA_ERR_INVALID_ARG;
+    ua::PlanParams pp{};
+    pp.block_table = block_table;
+    pp.held = blocks_held;
+    pp.pool = free_blocks;
+    pp.pool_count = free_count;
+    pp.ctx_lens = ctx_lens;
+    pp.new_lens = new_lens;
+    pp.parents = parents;
+    pp.granted = granted;
+    pp.cu = cu_seqlens_q;
+    pp.used = seqused_k;
+    pp.positions = positions;
+    pp.slots = slots;
+    pp.mask = tree_mask;
+    pp.err = p->d_err;
+    pp.ticket = p->d_err + 1;
+    pp.parents_stride = parents_stride;
+    pp.num_blocks = d.num_blocks;
+    pp.max_tokens = max_tokens;
+    pp.mask_stride = mask_stride;
+    pp.num_seqs = num_seqs;
+    pp.bt_stride = d.max_blocks_per_seq;
+    pp.b_log2 = d.block_size == 16 ? 4 : d.block_size == 32 ? 5 : 6;
+    const cudaError_t e = ua::launch_plan(pp, p->num_sms, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+        note_cuda(e, "plan kernel launch");
+        return UA_ERR_CUDA;
+    }
+    p->last_launches = 1;
+    p->last_path = "plan";
+    return UA_OK;
+}
+
+ua_status ua_set_rope(ua_problem* p, const double* inv_freq, int32_t n, uint32_t layout, float magnitude) {
+    if (!p || !inv_freq || n < 1 || layout > UA_ROPE_PAIRS || !std::isfinite(magnitude)) return UA_ERR_INVALID_ARG;
+    if (2 * (int64_t)n > p->desc.head_size || n % 8 != 0) return UA_ERR_UNSUPPORTED;
+    ua::RopeTable t{};
+    for (int i = 0; i < n; ++i) {
+        if (!(inv_freq[i] >= 0. && inv_freq[i] <= 6.)) return UA_ERR_INVALID_ARG;
+        // Below one turn, so that the product is below 2^64.
+        t.turn[i] = (uint64_t)(inv_freq[i] * (0x1p63 / 3.14159265358979323846));
+    }
+    t.n = n;
+    t.pairs = layout == UA_ROPE_PAIRS;
+    t.magnitude = magnitude;
+    p->rope = t;
+    return UA_OK;
+}
+
+ua_status ua_rope_store(ua_problem* p, const void* q, int64_t q_stride, const void* k_new, const void* v_new,
+                        int64_t kv_stride, const int32_t* positions, const int64_t* slots, int64_t total_q,
+                        void* q_out, int64_t out_stride, void* k_cache, void* v_cache, void* stream) {
+    if (!p) return UA_ERR_INVALID_ARG;
+    p->last_launches = 0;
+    p->last_path = "none";
+    const ua_problem_desc& d = p->desc;
+    const int64_t q_row = (int64_t)d.num_q_heads * d.head_size, kv_row = (int64_t)d.num_kv_heads * d.head_size;
+    if (total_q < 0 || total_q > d.max_total_q || q_stride < q_row || out_stride < q_row || kv_stride < kv_row ||
+        q_stride % 8 != 0 || out_stride % 8 != 0 || kv_stride % 8 != 0 || p->rope.n == 0 || !on_device(p))
+        return UA_ERR_INVALID_ARG;
+    if (total_q == 0) return UA_OK;
+    if (total_q > 0x7fffffff || q_row + 2 * kv_row > 0x3fffffff) return UA_ERR_UNSUPPORTED;
+    if (!q || !k_new || !v_new || !positions || !slots || !q_out || !k_cache || !v_cache || !aligned16(q) ||
+        !aligned16(k_new) || !aligned16(v_new) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !words(positions) || (reinterpret_cast<uintptr_t>(slots) & 7u) != 0 || (q_out == q && out_stride != q_stride))
+        return UA_ERR_INVALID_ARG;
+    ua::RopeParams rp{};
+    rp.c = cache_params(p, k_cache, v_cache, nullptr, nullptr, 0);
+    rp.q = static_cast<const __nv_bfloat16*>(q);
+    rp.k_new = static_cast<const __nv_bfloat16*>(k_new);
+    rp.v_new = static_cast<const __nv_bfloat16*>(v_new);
+    rp.q_out = static_cast<__nv_bfloat16*>(q_out);
+    rp.positions = positions;
+    rp.slots = slots;
+    rp.q_stride = q_stride;
+    rp.kv_stride = kv_stride;
+    rp.out_stride = out_stride;
+    rp.total_q = total_q;
+    rp.hq = d.num_q_heads;
+    const cudaError_t e = ua::launch_rope_store(rp, p->rope, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+        note_cuda(e, "rope store kernel launch");
+        return UA_ERR_CUDA;
+    }
+    p->last_launches = 1;
+    p->last_path = "rope_store";
+    return UA_OK;
+}
+
+ua_status ua_forward_tree(ua_problem* p, const void* q, const void* k_cache, const void* v_cache,
+                          const int32_t* block_table, const int32_t* cu_seqlens_q, const int32_t* seqused_k,
+                          int32_t num_seqs, int64_t total_q, int32_t max_seqlen_q, int32_t max_seqlen_k,
+                          const uint32_t* tree_mask, int32_t mask_stride, const int32_t* positions, uint32_t flags,
+                          const float* sinks, const float* alibi_slopes, void* out, void* stream) {
+    ua::FwdParams fp;
+    bool skip = false;
+    ua_status rs = prepare_call(p, q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, num_seqs, total_q,
+                                max_seqlen_q, max_seqlen_k, flags, sinks, alibi_slopes, out, &fp, &skip);
+    if (rs != UA_OK) return rs;
+    if (!(flags & UA_FLAG_CAUSAL) || mask_stride < 1 || 32LL * mask_stride < max_seqlen_q || !on_device(p))
+        return UA_ERR_INVALID_ARG;
+    const ua_problem_desc& d = p->desc;
+    if ((flags & UA_FLAG_QQ_BIAS) || d.kv_dtype != UA_DTYPE_BF16 || d.path != UA_PATH_AUTO ||
+        max_seqlen_q > ua::kMaxTree)
+        return UA_ERR_UNSUPPORTED;
+    if (skip) return UA_OK;
+    const bool places = (flags & (UA_FLAG_WINDOW | UA_FLAG_ALIBI)) != 0;
+    if (!tree_mask || (places && !positions) || !words(tree_mask, positions)) return UA_ERR_INVALID_ARG;
+    fp.tree_mask = tree_mask;
+    fp.mask_stride = mask_stride;
+    fp.positions = positions;
+    ua::TreePlan plan;
+    if (!ua::plan_tree(fp, p->num_sms, p->ws_bytes, &plan)) return UA_ERR_UNSUPPORTED;
+    rs = encode_maps(p, k_cache, v_cache, true);
+    if (rs != UA_OK) return rs;
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    set_partials(p, &fp, plan.splits, plan.chunk);
+    prof_mark(p, true, st);
+    const cudaError_t e = ua::launch_tree(plan, p->map_kp, p->map_vp, fp, st);
+    prof_mark(p, false, st);
+    if (e != cudaSuccess) {
+        note_cuda(e, "tree kernel launch");
+        return UA_ERR_CUDA;
+    }
+    p->last_launches = plan.splits > 1 ? 2 : 1;
+    p->last_path = plan.splits > 1 ? "tree+combine" : "tree";
+    return plan.splits > 1 ? run_combine(fp, st) : UA_OK;
+}
+
+ua_status ua_cache_accept(ua_problem* p, void* k_cache, void* v_cache, const int32_t* block_table,
+                          const int32_t* cu_seqlens_q, const int32_t* seqused_k, const int32_t* parents,
+                          int64_t parents_stride, const int32_t* last, int32_t num_seqs, int64_t total_q,
+                          int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t* path, int32_t path_stride,
+                          int32_t* accepted, int32_t* seqused_out, void* stream) {
+    if (!p) return UA_ERR_INVALID_ARG;
+    p->last_launches = 0;
+    p->last_path = "none";
+    const ua_problem_desc& d = p->desc;
+    if (num_seqs < 0 || num_seqs > d.max_num_seqs || total_q < 0 || total_q > d.max_total_q || max_seqlen_q < 0 ||
+        max_seqlen_k < max_seqlen_q || (int64_t)max_seqlen_k > (int64_t)d.max_blocks_per_seq * d.block_size ||
+        parents_stride < std::max(1, max_seqlen_q) || path_stride < 1 || !on_device(p))
+        return UA_ERR_INVALID_ARG;
+    if (num_seqs == 0) return UA_OK;
+    if (max_seqlen_q > ua::kMaxTree) return UA_ERR_UNSUPPORTED;
+    if (!k_cache || !v_cache || !block_table || !cu_seqlens_q || !seqused_k || !parents || !last || !path || !accepted ||
+        !seqused_out || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !words(block_table, cu_seqlens_q, seqused_k, parents, last, path, accepted, seqused_out))
+        return UA_ERR_INVALID_ARG;
+    ua::AcceptParams ap{};
+    ap.c = cache_params(p, k_cache, v_cache, block_table, seqused_k, num_seqs);
+    ap.cu_seqlens_q = cu_seqlens_q;
+    ap.parents = parents;
+    ap.last = last;
+    ap.path = path;
+    ap.accepted = accepted;
+    ap.seqused_out = seqused_out;
+    ap.parents_stride = parents_stride;
+    ap.total_q = total_q;
+    ap.path_stride = path_stride;
+    ap.max_seqlen_q = max_seqlen_q;
+    ap.max_seqlen_k = max_seqlen_k;
+    const cudaError_t e = ua::launch_accept(ap, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) {
+        note_cuda(e, "accept kernel launch");
+        return UA_ERR_CUDA;
+    }
+    p->last_launches = 1;
+    p->last_path = "accept";
     return UA_OK;
 }
 

@@ -67,6 +67,11 @@ struct FwdParams {
     // every row's number of pieces, once per 64 dims (0 between calls).
     float* piece_ml;               // [total_q * hq, splits, 2]
     int4* row_pieces;              // [total_q * hq]
+    // Draft trees: bit c of row t says that chunk token t sees its chunk's key c;
+    // positions of the chunk's tokens (with ALiBi or a window).  Null elsewhere.
+    const uint32_t* tree_mask;     // [total_q, mask_stride]
+    const int32_t* positions;      // [total_q]
+    int32_t mask_stride;
 };
 
 // Per-sequence metadata check.  Returns UA_DEVERR_* bits (0 = well formed) and

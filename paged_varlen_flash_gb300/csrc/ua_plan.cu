@@ -1,0 +1,280 @@
+// ua_plan.cu -- block tables, slots, positions and ancestor masks of a step, from the
+// requests' lengths and a pool of free blocks.
+//
+// A sequence needs ceil((ctx + new) / b) blocks.  Those that hold more give the last
+// ones back; those that hold fewer take the difference from the pool, in their order,
+// as long as the running demand is covered.  With T blocks taken and R returned, and
+// the pool a stack of n blocks, taken block k (counted over the sequences) is
+//     returned block k          for k < R,
+//     pool[n + R - 1 - k]       otherwise,
+// and the returned blocks from T on stay, block r at pool[n + R - 1 - r]: the returned
+// blocks lie on the stack with the first one on top.  (A step that is taken back leaves
+// the pool as it was.)  So every id follows from prefix sums over the sequences, and no
+// write of the call touches a pool entry that it reads.
+//
+// Every CTA computes the prefix sums itself (12 bytes a sequence, from L2), then takes
+// its share of the tokens, the taken blocks and the returned ones; the last CTA to finish
+// writes what replaces an input (held, pool_count, used), when nobody reads it any more.
+#include <algorithm>
+#include <cstdint>
+
+#include "../../include/ua.h"
+#include "ua_plan.h"
+
+namespace ua {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+
+struct Sums {          // of the sequences in front of a thread's, or of all
+    int64_t a, b, c;
+};
+
+// Exclusive prefix over the CTA's threads; *total gets the sum.
+__device__ __forceinline__ Sums prefix(Sums v, Sums* warp_sums, Sums* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    Sums x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, x.a, o), b = __shfl_up_sync(0xffffffffu, x.b, o),
+                      c = __shfl_up_sync(0xffffffffu, x.c, o);
+        if (lane >= o) {
+            x.a += a;
+            x.b += b;
+            x.c += c;
+        }
+    }
+    __syncthreads();                       // warp_sums may still be read from the call before
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    Sums before{0, 0, 0}, all{0, 0, 0};
+    for (int w = 0; w < kWarps; ++w) {
+        const Sums y = warp_sums[w];
+        if (w < warp) {
+            before.a += y.a;
+            before.b += y.b;
+            before.c += y.c;
+        }
+        all.a += y.a;
+        all.b += y.b;
+        all.c += y.c;
+    }
+    *total = all;
+    return {before.a + x.a - v.a, before.b + x.b - v.b, before.c + x.c - v.c};
+}
+
+// What a sequence asks for.  Malformed lengths ask for nothing and give nothing back.
+struct Ask {
+    int ctx, fresh, held, more, back;
+    bool bad;
+};
+
+__device__ __forceinline__ Ask ask_of(const PlanParams& p, int s) {
+    Ask a{p.ctx_lens[s], p.new_lens[s], p.held[s], 0, 0, false};
+    const int64_t end = (int64_t)a.ctx + a.fresh;
+    a.bad = a.ctx < 0 || a.fresh < 0 || a.held < 0 || a.held > p.bt_stride || end > (int64_t)p.bt_stride << p.b_log2 ||
+            (p.parents && a.fresh > p.parents_stride) || (p.mask && (int64_t)a.fresh > 32LL * p.mask_stride);
+    if (a.bad) {
+        a.ctx = a.fresh = 0;
+        return a;
+    }
+    const int need = (int)((end + (1 << p.b_log2) - 1) >> p.b_log2);
+    a.more = max(need - a.held, 0);
+    a.back = max(a.held - need, 0);
+    return a;
+}
+
+// Last s with first[s] <= x (first[0] = 0, x < first[n]).
+__device__ __forceinline__ int owner_of(const int32_t* first, int n, int32_t x) {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
+    extern __shared__ int32_t smem[];
+    __shared__ Sums warp_sums[kWarps];
+    __shared__ int last;
+    const int n = p.num_seqs, tid = threadIdx.x;
+    int32_t* tok = smem;             // tokens in front of a sequence
+    int32_t* take = tok + n + 1;     // blocks taken in front of it
+    int32_t* give = take + n + 1;    // blocks returned in front of it
+    const int per = (n + kThreads - 1) / kThreads;
+    const int s0 = min(n, tid * per), s1 = min(n, s0 + per);
+
+    // 1. What is asked for, and which sequences get it.
+    Sums mine{0, 0, 0}, all;
+    uint32_t err = 0;
+    for (int s = s0; s < s1; ++s) {
+        const Ask a = ask_of(p, s);
+        if (a.bad) err |= UA_DEVERR_BOUNDS;
+        mine.a += a.more;
+        mine.b += a.back;
+        mine.c += a.fresh;
+    }
+    const Sums before = prefix(mine, warp_sums, &all);
+    int64_t count = *p.pool_count;
+    // A pool of another size than the cache's, or more blocks given back than there are:
+    // nothing is taken or nothing is given back.
+    const bool sane = count >= 0 && count <= p.num_blocks;
+    const bool returns = sane && count + all.b <= p.num_blocks;
+    if (!sane) count = 0;
+    if (!returns) err |= UA_DEVERR_POOL;
+    const int64_t R = returns ? all.b : 0;
+    // 2. Prefix sums of what is given out.
+    Sums got{0, 0, 0}, sum;
+    {
+        int64_t more = before.a, fresh = before.c;
+        for (int s = s0; s < s1; ++s) {
+            const Ask a = ask_of(p, s);
+            more += a.more;
+            fresh += a.fresh;
+            const bool fits = fresh <= p.max_tokens;
+            if (!fits && a.fresh) err |= UA_DEVERR_BOUNDS;
+            const bool ok = fits && (a.more == 0 || more <= count + R);
+            got.a += ok ? a.more : 0;
+            got.b += returns ? a.back : 0;
+            got.c += ok ? a.fresh : 0;
+        }
+    }
+    Sums at = prefix(got, warp_sums, &sum);
+    {
+        int64_t more = before.a, fresh = before.c;
+        for (int s = s0; s < s1; ++s) {
+            const Ask a = ask_of(p, s);
+            more += a.more;
+            fresh += a.fresh;
+            const bool ok = fresh <= p.max_tokens && (a.more == 0 || more <= count + R);
+            take[s] = (int32_t)at.a;
+            give[s] = (int32_t)at.b;
+            tok[s] = (int32_t)at.c;
+            at.a += ok ? a.more : 0;
+            at.b += returns ? a.back : 0;
+            at.c += ok ? a.fresh : 0;
+        }
+    }
+    if (tid == 0) {
+        take[n] = (int32_t)sum.a;
+        give[n] = (int32_t)sum.b;
+        tok[n] = (int32_t)sum.c;
+    }
+    __syncthreads();
+    const int T = (int)sum.a, total = (int)sum.c;
+    const int b = 1 << p.b_log2;
+    const int64_t first = (int64_t)blockIdx.x * kThreads + tid, step = (int64_t)gridDim.x * kThreads;
+
+    auto returned = [&](int r) -> int32_t {
+        const int s = owner_of(give, n, r);
+        const int keep = p.held[s] - (give[s + 1] - give[s]);
+        return p.block_table[(int64_t)s * p.bt_stride + keep + (r - give[s])];
+    };
+    auto taken = [&](int k) -> int32_t { return k < R ? returned(k) : p.pool[count + R - 1 - k]; };
+
+    // 3. Taken blocks into the tables, returned ones that nobody took onto the pool.
+    for (int64_t k = first; k < T; k += step) {
+        const int s = owner_of(take, n, (int)k);
+        const int32_t id = taken((int)k);
+        if (id < 0 || (int64_t)id >= p.num_blocks) err |= UA_DEVERR_BLOCK_ID;
+        p.block_table[(int64_t)s * p.bt_stride + p.held[s] + ((int)k - take[s])] = id;
+    }
+    for (int64_t r = T + first; r < R; r += step) p.pool[count + R - 1 - r] = returned((int)r);
+
+    // 4. Tokens.
+    for (int64_t t = first; t < p.max_tokens; t += step) {
+        if (t >= total) {
+            p.positions[t] = 0;
+            p.slots[t] = -1;
+            continue;
+        }
+        const int s = owner_of(tok, n, (int)t);
+        const int i = (int)t - tok[s], ctx = p.ctx_lens[s];
+        const int place = ctx + i, blk = place >> p.b_log2, held = p.held[s];
+        const int32_t id =
+            blk < held ? p.block_table[(int64_t)s * p.bt_stride + blk] : taken(take[s] + blk - held);
+        const bool good = id >= 0 && (int64_t)id < p.num_blocks;
+        if (!good) err |= UA_DEVERR_BLOCK_ID;
+        p.slots[t] = good ? (int64_t)id * b + (place & (b - 1)) : -1;
+        int depth = i;
+        if (p.parents) {
+            // Up to the root; the bits of a word of the mask are complete when the
+            // walk leaves it, since parents stand in front of their children.
+            const int32_t* up = p.parents + (int64_t)s * p.parents_stride;
+            uint32_t* row = p.mask ? p.mask + t * p.mask_stride : nullptr;
+            int w = p.mask_stride - 1, node = i;
+            uint32_t bits = 0;
+            depth = -1;
+            while (node >= 0) {
+                if (row) {
+                    for (; w > node >> 5; --w) {
+                        row[w] = bits;
+                        bits = 0;
+                    }
+                    bits |= 1u << (node & 31);
+                }
+                ++depth;
+                const int q = __ldg(up + node);
+                if (q < -1 || q >= node) {
+                    err |= UA_DEVERR_TREE;
+                    break;
+                }
+                node = q;
+            }
+            if (row)
+                for (; w >= 0; --w) {
+                    row[w] = bits;
+                    bits = 0;
+                }
+        } else if (p.mask) {
+            for (int w = 0; w < p.mask_stride; ++w) {
+                const int over = i + 1 - 32 * w;
+                p.mask[t * p.mask_stride + w] = over >= 32 ? 0xffffffffu : over > 0 ? (1u << over) - 1 : 0u;
+            }
+        }
+        p.positions[t] = ctx + depth;
+    }
+    if (err) atomicOr(p.err, (int)err);
+
+    // 5. The last CTA replaces the state.
+    if (gridDim.x > 1) {
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();
+            last = atomicAdd(p.ticket, 1) == (int)gridDim.x - 1;
+        }
+        __syncthreads();
+        if (!last) return;
+        __threadfence();
+        if (tid == 0) *p.ticket = 0;
+    } else {
+        __syncthreads();
+    }
+    for (int s = tid; s < n; s += kThreads) {
+        const Ask a = ask_of(p, s);
+        const int fresh = tok[s + 1] - tok[s];
+        p.granted[s] = fresh;
+        p.cu[s] = tok[s];
+        p.used[s] = a.ctx + fresh;
+        if (!a.bad) p.held[s] = a.held + (take[s + 1] - take[s]) - (give[s + 1] - give[s]);
+    }
+    if (tid == 0) {
+        p.cu[n] = total;
+        if (sane) *p.pool_count = (int32_t)(count + R - T);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_plan(const PlanParams& p, int num_sms, cudaStream_t stream) {
+    const size_t smem = (size_t)3 * (p.num_seqs + 1) * sizeof(int32_t);
+    cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(num_sms, (p.max_tokens + kThreads - 1) / kThreads));
+    plan_kernel<<<(unsigned)ctas, kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace ua
