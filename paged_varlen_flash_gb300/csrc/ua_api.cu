@@ -70,6 +70,7 @@ struct ua_problem {
     int32_t* d_err = nullptr;      // the error word, then ua_plan_step's count of finished CTAs
     float* d_ws = nullptr;
     size_t ws_bytes = 0;
+    size_t tree_bytes = 0;         // of the same buffer, what ua_forward_tree may use
     // scores of ua_forward_weights (UA_FLAG_KEY_WEIGHTS problems only)
     float* d_scores = nullptr;
     size_t scores_elems = 0;
@@ -209,6 +210,12 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
                       size_t(d->max_total_q) * d->num_q_heads * 2 * sizeof(float) + 16;
         piece_bytes = size_t(d->max_total_q) * d->num_q_heads * sizeof(int4);
     }
+    // Draft trees cut their work into one share per CTA of the device, with two partials
+    // each.  (Key-weight problems have the size that is documented for them, and fewer
+    // shares.)
+    p->tree_bytes = p->ws_bytes;
+    if (d->kv_dtype == UA_DTYPE_BF16 && !(d->flags & UA_FLAG_KEY_WEIGHTS))
+        p->tree_bytes = std::max(p->ws_bytes, ua::tree_workspace_bytes(*d, p->num_sms));
     // Work-list entries: every call's (total_q / (2 ppt) + num_seqs) entries
     // without a KV split, and room for the splits the planner makes when the
     // grid is small (about 4 x 152 units per KV head x up to 64 segments).
@@ -217,7 +224,7 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
     p->work_cap = (int32_t)cap;
     const size_t work_bytes = (size_t)cap * sizeof(int2) + (size_t)(d->max_num_seqs + 1) * 4 + 16;
     if (cudaMalloc(&p->d_err, 2 * sizeof(int32_t)) != cudaSuccess ||
-        cudaMalloc(&p->d_ws, p->ws_bytes) != cudaSuccess ||
+        cudaMalloc(&p->d_ws, p->tree_bytes) != cudaSuccess ||
         cudaMalloc(&p->d_work, work_bytes) != cudaSuccess ||
         (piece_bytes && cudaMalloc(&p->d_pieces, piece_bytes) != cudaSuccess) ||
         (p->scores_elems && cudaMalloc(&p->d_scores, p->scores_elems * sizeof(float)) != cudaSuccess)) {
@@ -1031,11 +1038,10 @@ ua_status ua_forward_tree(ua_problem* p, const void* q, const void* k_cache, con
     fp.mask_stride = mask_stride;
     fp.positions = positions;
     ua::TreePlan plan;
-    if (!ua::plan_tree(fp, p->num_sms, p->ws_bytes, &plan)) return UA_ERR_UNSUPPORTED;
+    if (!ua::plan_tree(&fp, p->num_sms, p->d_ws, p->tree_bytes, &plan)) return UA_ERR_UNSUPPORTED;
     rs = encode_maps(p, k_cache, v_cache, true);
     if (rs != UA_OK) return rs;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    set_partials(p, &fp, plan.splits, plan.chunk);
     prof_mark(p, true, st);
     const cudaError_t e = ua::launch_tree(plan, p->map_kp, p->map_vp, fp, st);
     prof_mark(p, false, st);
@@ -1043,9 +1049,9 @@ ua_status ua_forward_tree(ua_problem* p, const void* q, const void* k_cache, con
         note_cuda(e, "tree kernel launch");
         return UA_ERR_CUDA;
     }
-    p->last_launches = plan.splits > 1 ? 2 : 1;
-    p->last_path = plan.splits > 1 ? "tree+combine" : "tree";
-    return plan.splits > 1 ? run_combine(fp, st) : UA_OK;
+    p->last_launches = plan.ctas > 1 ? 2 : 1;
+    p->last_path = plan.ctas > 1 ? "tree+merge" : "tree";
+    return UA_OK;
 }
 
 ua_status ua_cache_accept(ua_problem* p, void* k_cache, void* v_cache, const int32_t* block_table,

@@ -6,21 +6,34 @@
 // cached value is used that often, which is less than the tensor cores could do per
 // byte of HBM (about 277 rows), so a batch of trees is bound by reading K and V once.
 //
-// One CTA per (row tile of floor(128 / g) nodes, KV segment, KV head, sequence), the
-// row tiles of a segment next to each other (they read the same K and V, from L2 after
-// the first).  S = Q K^T and O += P V are tcgen05.mma with M = 128 rows; P goes over
-// its own S in tensor memory.  At d = 64 and 128 a CTA keeps one S tile (256 columns of
-// tensor memory with O) and few K/V stages, so that two CTAs share an SM: while one
-// waits for its copies or for its softmax, the other one's copies are in flight.  At
-// d = 256 Q and the tiles (64 keys) fill an SM's shared memory, and one CTA overlaps
-// its own softmax and MMAs over two S tiles.
+// Work.  An item is (row tile of floor(128 / g) nodes, sequence, KV head); it has as many
+// steps as key tiles that its rows see.  All items' steps behind each other (row tile
+// first, so that the row tiles of a batch read the same keys at about the same time) are
+// cut into equal shares, one for every CTA that fits the machine.  A CTA walks through
+// its share item by item; an item that lies in one share is written at once, one that is
+// cut leaves a partial (m, l, o) in every share that it touches, joined by
+// tree_merge_kernel in the order of the shares.  So no SM waits for a longer
+// sequence of another one, and a batch has at most two partials per CTA.
+//
+// S = Q K^T and O += P V are tcgen05.mma with M = 128 rows; P goes over its own S in
+// tensor memory.  At d = 64 and 128 a CTA keeps one S tile (256 columns of tensor memory
+// with O) and few K/V stages, so that two CTAs share an SM: while one waits for its copies
+// or for its softmax, the other one's copies are in flight.  At d = 256 Q and the tiles
+// (64 keys) fill an SM's shared memory, and one CTA overlaps its own softmax and MMAs over
+// two S tiles.  Barriers, tensor memory and the K/V ring live on from item to item: the
+// next item's copies and first Q K^T run under the epilogue of the one before.
 //
 // Roles (7 warps):
 //   warps 0-3  softmax and epilogue: thread r owns row r (tensor-memory lane r); two
-//              passes over the tile's columns (maximum, then P), 64 at a time;
-//   warp 4     copies (TMA): Q, then the K and V tiles, one lane per paged block;
+//              passes over the tile's columns (maximum, then P);
+//   warp 4     walks through the share and copies (TMA): Q, then the K and V tiles, one
+//              lane per paged block;
 //   warp 5     MMA issuer and owner of tensor memory;
 //   warp 6     looks through V tiles with keys that some row does not see.
+// The softmax loops are kept short (32 or 64 columns, masks and score terms in a loop of
+// their own): unrolled over a row's 128 columns with every term they missed the
+// instruction cache (48 small trees with a softcap at d = 64: 88 us, of which 50 us the
+// cap).
 //
 // Masked keys: their scores are replaced, whatever K holds.  Their V rows reach the
 // product with P = 0, and 0 times an infinity or NaN is NaN; so warp 6 clears values
@@ -30,6 +43,7 @@
 #include <cstdint>
 
 #include "ua_common.cuh"
+#include "ua_launch.h"
 #include "ua_prefill_common.cuh"
 #include "ua_ptx.cuh"
 #include "ua_tc.cuh"
@@ -46,6 +60,24 @@ constexpr int kWarpCopy = 4;
 constexpr int kWarpMmaT = 5;
 constexpr int kWarpFix = 6;
 constexpr int kCols = 64;          // columns of S a softmax thread holds at a time
+constexpr int kUnitReaders = 130;  // MMA and fix warps (a lane each), softmax threads
+
+// Score chains: the scale alone, a softcap, ALiBi with or without a softcap.
+enum { kPlain = 0, kCap = 1, kAlibi = 2 };
+
+// A piece of an item, written by the copy warp into a two-slot ring.
+struct TreeUnit {
+    int32_t live;          // 0: the share is done
+    int32_t zero;          // malformed lengths: rows written as zeros
+    int32_t s, hkv;
+    int32_t q0, sq, sk;
+    int32_t first, last;   // nodes of the tile
+    int32_t t_begin, n;    // key tiles
+    int32_t slot;          // of the partial, -1: the whole item
+    int32_t odd;           // values that are not finite were cleared in V
+    int32_t pad[3];
+};
+static_assert(sizeof(TreeUnit) == 64, "unit descriptor");
 
 template <int D>
 struct TCfg {
@@ -61,11 +93,12 @@ struct TCfg {
     static constexpr int kOffK = kPanels * kQPanel;
     static constexpr int kOffV = kOffK + kStages * kTile;
     static constexpr int kOffBar = kOffV + kStages * kTile;
-    // q_full, {k_full, k_empty, v_full, v_ready, v_empty}[kStages], s_full[2],
-    // p_full[2], o_done[2], drain, never
-    static constexpr int kNumBars = 1 + 5 * kStages + 8;
-    static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr int kSmem = kOffMisc + 16 + 1024;
+    // q_full, q_empty, {k_full, k_empty, v_full, v_ready, v_empty}[kStages], s_full[2],
+    // p_full[2], o_done[2], o_free, u_full[2], u_empty[2], drain, never
+    static constexpr int kNumBars = 2 + 5 * kStages + 13;
+    static constexpr int kOffUnit = (kOffBar + kNumBars * 8 + 63) / 64 * 64;
+    static constexpr int kOffMisc = kOffUnit + 2 * (int)sizeof(TreeUnit);
+    static constexpr int kSmem = kOffMisc + 128 + 1024;
     static constexpr int kTmemO = kBufs * kBN;
     static constexpr uint32_t kCols2 = D == 256 ? 512 : 256;    // tensor-memory columns
     static_assert(kTmemO + D <= (int)kCols2, "tensor memory budget");
@@ -117,10 +150,23 @@ __device__ __noinline__ void add_unbounded(const FwdParams& p, int s, int hkv, i
     }
 }
 
-template <int D, bool GEN>
+// Steps (key tiles) of the items of sequence s in row tile r: 0 where it has no such
+// tile, 1 for malformed lengths (rows of zeros).
+template <int BN>
+__device__ __forceinline__ int item_steps(const FwdParams& p, int s, int r, uint32_t& st) {
+    int sq, sk;
+    int64_t q0;
+    st = seq_status(p, s, sq, sk, q0);
+    if ((st & UA_DEVERR_CU_SEQLENS) || r * (kRows / p.g) >= sq) return 0;
+    if (st) return 1;
+    const int beg = (p.flags & UA_FLAG_WINDOW) ? max(0, sk - sq - p.window + 1) : 0;
+    return (sk + BN - 1) / BN - beg / BN;
+}
+
+template <int D, int MODE>
 __global__ void __launch_bounds__(kThreadsT, TCfg<D>::kCtas)
 tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-            const __grid_constant__ CUtensorMap tm_v, const FwdParams p, int tiles) {
+            const __grid_constant__ CUtensorMap tm_v, const FwdParams p, const TreeShares w) {
     using C = TCfg<D>;
     constexpr int kBN = C::kBN;
     extern __shared__ uint8_t smem_raw[];
@@ -128,67 +174,27 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int s = blockIdx.z;
-    const int hkv = blockIdx.y;
-    const int tile = blockIdx.x % tiles;
-    const int seg = blockIdx.x / tiles;
-    const bool split = p.splits > 1;
     const int g = p.g;
     const int ppt = kRows / g;                   // nodes per tile
-    const int first = tile * ppt;
-
-    int sq, sk;
-    int64_t q0;
-    const uint32_t st = seq_status(p, s, sq, sk, q0);
-    if (st && hkv == 0 && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, (int)st);
-    if (st & UA_DEVERR_CU_SEQLENS) return;
-    if (first >= sq) return;
-    if (seg >= (split ? seq_segments(p, st, sk) : 1)) return;
-    const int last = min(first + ppt, sq) - 1;
-    const int ctx = sk - sq;
     const bool window = (p.flags & UA_FLAG_WINDOW) != 0;
-    // Positions of the chunk lie in [ctx, sk): keys in front of ctx - W + 1 are seen by
-    // no row, those from sk - W on by every row, up to the chunk.
-    const int vis_beg = window ? max(0, ctx - p.window + 1) : 0;
-    int k_beg = vis_beg, k_end = sk;
-    if (split) {
-        k_beg = max(k_beg, seg * p.chunk);
-        k_end = (int)min((int64_t)k_end, (int64_t)seg * p.chunk + p.chunk);
-    }
-    if (st || k_beg >= k_end) {
-        // Malformed lengths (rows written as zeros) or a segment no row sees.
-        for (int e = threadIdx.x; e < kRows * (D / 8); e += kThreadsT) {
-            const int r = e / (D / 8), c = e % (D / 8), i = first + r / g;
-            if (r >= g * ppt || i > last) continue;
-            const int64_t row = (q0 + i) * p.hq + hkv * g + r % g;
-            if (split) {
-                if (c == 0) {
-                    p.part_ml[(row * p.splits + seg) * 2 + 0] = -INFINITY;
-                    p.part_ml[(row * p.splits + seg) * 2 + 1] = 0.f;
-                }
-            } else {
-                *reinterpret_cast<uint4*>(p.out + row * D + c * 8) = make_uint4(0, 0, 0, 0);
-            }
-        }
-        return;
-    }
-    const int t_begin = k_beg / kBN;
-    const int n = (k_end + kBN - 1) / kBN - t_begin;
-    const int full_lo = window ? max(0, sk - p.window) : 0;     // [full_lo, ctx): seen by every row
 
     uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     constexpr int kS = 8 * C::kStages;
-    const uint32_t q_full = smem_u32(bar_mem);
-    const uint32_t k_full0 = q_full + 8, k_empty0 = k_full0 + kS;
+    const uint32_t q_full = smem_u32(bar_mem), q_empty = q_full + 8;
+    const uint32_t k_full0 = q_full + 16, k_empty0 = k_full0 + kS;
     const uint32_t v_full0 = k_empty0 + kS, v_ready0 = v_full0 + kS, v_empty0 = v_ready0 + kS;
     const uint32_t s_full0 = v_empty0 + kS, p_full0 = s_full0 + 16, o_done0 = s_full0 + 32;
-    const uint32_t drain = s_full0 + 48, never = s_full0 + 56;
+    const uint32_t o_free = s_full0 + 48, u_full0 = s_full0 + 56, u_empty0 = s_full0 + 72;
+    const uint32_t drain = s_full0 + 88, never = s_full0 + 96;
+    TreeUnit* units = reinterpret_cast<TreeUnit*>(smem + C::kOffUnit);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-    volatile int* odd_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
+    int64_t* warp_sums = reinterpret_cast<int64_t*>(smem + C::kOffMisc + 16);   // [7]
+    int32_t* start = reinterpret_cast<int32_t*>(smem + C::kOffMisc + 80);       // entry, KV head, step
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(k_full0 + 8 * i, 1);
             mbar_init(k_empty0 + 8 * i, 1);
@@ -200,86 +206,221 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             mbar_init(s_full0 + 8 * i, 1);
             mbar_init(p_full0 + 8 * i, kRows);
             mbar_init(o_done0 + 8 * i, 1);
+            mbar_init(u_full0 + 8 * i, 1);
+            mbar_init(u_empty0 + 8 * i, kUnitReaders);
         }
+        mbar_init(o_free, kRows);
         mbar_init(drain, 1);
         mbar_init(never, 1);
         *abort_flag = 0;
-        *odd_flag = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMmaT) {
         tc::tmem_alloc(smem_u32(tmem_slot), C::kCols2);
         tc::tmem_relinquish();
     }
+    // This CTA's share: entries (row tile, sequence) in order, each thread a run of them.
+    const int64_t entries = (int64_t)w.tiles * p.num_seqs;
+    const int64_t per = (entries + kThreadsT - 1) / kThreadsT;
+    const int64_t e_lo = min(entries, threadIdx.x * per), e_hi = min(entries, e_lo + per);
+    int64_t mine = 0;
+    for (int64_t e = e_lo; e < e_hi; ++e) {
+        const int r = (int)(e / p.num_seqs), s = (int)(e - (int64_t)r * p.num_seqs);
+        uint32_t st;
+        mine += item_steps<kBN>(p, s, r, st);
+        if (st && r == 0 && blockIdx.x == 0) atomicOr(p.err, (int)st);
+    }
+    mine *= p.hk;
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+    }
+    if (lane == 31) warp_sums[warp] = upto;
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_slot;
+    int64_t total = 0;
+#pragma unroll
+    for (int i = 0; i < kThreadsT / 32; ++i) {
+        if (i < warp) upto += warp_sums[i];
+        total += warp_sums[i];
+    }
+    // A share has w.least steps at least.
+    const int64_t shares = min((int64_t)gridDim.x, (total + w.least - 1) / w.least);
+    const bool idle = blockIdx.x >= shares;
+    const int64_t x0 = idle ? 0 : total * blockIdx.x / shares, x1 = idle ? 0 : total * (blockIdx.x + 1) / shares;
+    if (!idle && x0 >= upto - mine && x0 < upto) {
+        int64_t at = upto - mine;
+        for (int64_t e = e_lo; e < e_hi; ++e) {
+            const int r = (int)(e / p.num_seqs), s = (int)(e - (int64_t)r * p.num_seqs);
+            uint32_t st;
+            const int steps = item_steps<kBN>(p, s, r, st);
+            const int64_t all = (int64_t)steps * p.hk;
+            if (x0 < at + all) {
+                start[0] = (int32_t)e;
+                start[1] = (int32_t)((x0 - at) / steps);
+                start[2] = (int32_t)((x0 - at) % steps);
+                break;
+            }
+            at += all;
+        }
+    }
+    __syncthreads();
     const uint32_t sQ = smem_u32(smem + C::kOffQ);
     const uint32_t sK = smem_u32(smem + C::kOffK);
     const uint32_t sV = smem_u32(smem + C::kOffV);
     auto wwait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, p.err));
     };
-    // Tiles with a key that some row does not see.
-    auto edge_tile = [&](int key0) { return key0 < full_lo || key0 + kBN > ctx; };
 
     if (warp == kWarpCopy) {
-        // --------------------------------- copies ---------------------------------
+        // ------------------------ the share's pieces, and copies ------------------------
         if (lane == 0) {
             tma_prefetch_desc(&tm_q);
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
-            mbar_arrive_expect_tx(q_full, (uint32_t)(g * ppt) * 128u * C::kPanels);
-#pragma unroll
-            for (int pn = 0; pn < C::kPanels; ++pn)
-                tma_load_3d(sQ + pn * C::kQPanel, &tm_q, pn * 64, hkv * g, (int)q0 + first, q_full);
         }
-        __syncwarp();
         const int b = p.b;
-        const int nblk_seq = (sk + b - 1) / b;
-        const int32_t* bt = p.block_table + (int64_t)s * p.bt_stride;
-        auto tile_id = [&](int j) -> int32_t {
-            const int blk0 = (t_begin + j) * kBN / b;
-            return lane < min(kBN / b, nblk_seq - blk0) ? __ldg(bt + blk0 + lane) : 0;
-        };
-        int32_t id_next = tile_id(0);
-        int k_out = 0, v_out = 0;      // tiles whose copies were issued
-        for (int j = 0; j < n; ++j) {
-            const int stg = j % C::kStages;
-            const int blk0 = (t_begin + j) * kBN / b;
-            const int nb = min(kBN / b, nblk_seq - blk0);
-            const uint32_t bytes = (uint32_t)nb * b * 128 * C::kPanels;
-            const int32_t id = id_next;
-            if (j + 1 < n) id_next = tile_id(j + 1);
-            if (lane < nb && (id < 0 || (int64_t)id >= p.num_blocks)) atomicOr(p.err, (int)UA_DEVERR_BLOCK_ID);
-            if (j >= C::kStages && !wwait(k_empty0 + 8 * stg, ((j / C::kStages) + 1) & 1)) break;
-            if (lane == 0) mbar_arrive_expect_tx(k_full0 + 8 * stg, bytes);
-            __syncwarp();
-            if (lane < nb) {
+        int64_t x = x0, e = idle ? 0 : start[0];
+        int hkv = idle ? 0 : start[1], step = idle ? 0 : start[2];
+        int u = 0, qn = 0, kt = 0, k_extra = 0;     // units, Q loads, K/V tiles; a K tile without its V
+        TreeJoin join{0, 0, 0, 0, 0};
+        bool ok = true;
+        for (;; ++u) {
+            const int slot = u & 1;
+            if (u >= 2 && !(ok = wwait(u_empty0 + 8 * slot, ((u >> 1) + 1) & 1))) break;
+            if (x >= x1) {
+                if (lane == 0) {
+                    units[slot].live = 0;
+                    mbar_arrive(u_full0 + 8 * slot);
+                }
+                break;
+            }
+            // The next entry with steps: 32 of them are looked at together.
+            int steps = 0;
+            for (;;) {
+                const int64_t le = e + lane;
+                uint32_t st_l = 0;
+                const int r_l = (int)(le / p.num_seqs), s_l = (int)(le - (int64_t)r_l * p.num_seqs);
+                const int n_l = le < entries ? item_steps<kBN>(p, s_l, r_l, st_l) : 0;
+                const unsigned some = __ballot_sync(0xffffffffu, n_l > 0);
+                if (some) {
+                    const int at = __ffs(some) - 1;
+                    steps = __shfl_sync(0xffffffffu, n_l, at);
+                    e += at;
+                    break;
+                }
+                e += 32;
+                if (e >= entries) break;             // not reached: x < x1 <= total
+            }
+            if (steps == 0) {
+                ok = false;
+                *abort_flag = 1;
+                break;
+            }
+            const int r = (int)(e / p.num_seqs), s = (int)(e - (int64_t)r * p.num_seqs);
+            int sq, sk;
+            int64_t q0;
+            const uint32_t st = seq_status(p, s, sq, sk, q0);
+            const int ctx = sk - sq, first = r * ppt;
+            const int n = (int)min((int64_t)(steps - step), x1 - x);
+            const int t_begin = (st || !window ? 0 : max(0, ctx - p.window + 1) / kBN) + step;
+            const bool whole = n == steps;
+            if (lane == 0) {
+                TreeUnit& un = units[slot];
+                un.live = 1;
+                un.zero = st != 0;
+                un.s = s;
+                un.hkv = hkv;
+                un.q0 = (int32_t)q0;
+                un.sq = sq;
+                un.sk = sk;
+                un.first = first;
+                un.last = min(first + ppt, sq) - 1;
+                un.t_begin = t_begin;
+                un.n = n;
+                un.slot = whole ? -1 : 2 * (int)blockIdx.x + (x > x0 ? 1 : 0);
+                un.odd = 0;
+                mbar_arrive(u_full0 + 8 * slot);
+            }
+            if (!whole && step == 0) {
+                // The item begins here: its shares up to the one that holds its last step.
+                const int64_t end = x + steps;
+                join.pieces = (int)((end * shares - 1) / total - blockIdx.x) + 1;
+                join.slot = 2 * (int)blockIdx.x + (x > x0 ? 1 : 0);
+                join.row0 = q0 + first;
+                join.nodes = min(first + ppt, sq) - first;
+                join.hkv = hkv;
+            }
+            x += n;
+            step += n;
+            const int h_now = hkv;
+            if (step == steps) {
+                step = 0;
+                if (++hkv == p.hk) {
+                    hkv = 0;
+                    ++e;
+                }
+            }
+            if (st) continue;
+            if (qn >= 1 && !(ok = wwait(q_empty, (qn - 1) & 1))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(q_full, (uint32_t)(g * ppt) * 128u * C::kPanels);
 #pragma unroll
                 for (int pn = 0; pn < C::kPanels; ++pn)
-                    tma_load_4d(sK + stg * C::kTile + pn * C::kPanel + lane * b * 128, &tm_k, pn * 64, hkv, 0, id,
-                                k_full0 + 8 * stg);
+                    tma_load_3d(sQ + pn * C::kQPanel, &tm_q, pn * 64, h_now * g, (int)q0 + first, q_full);
             }
-            k_out = j + 1;
-            if (j >= C::kStages && !wwait(v_empty0 + 8 * stg, ((j / C::kStages) + 1) & 1)) break;
-            if (lane == 0) mbar_arrive_expect_tx(v_full0 + 8 * stg, bytes);
+            ++qn;
             __syncwarp();
-            if (lane < nb) {
+            const int nblk_seq = (sk + b - 1) / b;
+            const int32_t* bt = p.block_table + (int64_t)s * p.bt_stride;
+            auto tile_id = [&](int j) -> int32_t {
+                const int blk0 = (t_begin + j) * kBN / b;
+                return lane < min(kBN / b, nblk_seq - blk0) ? __ldg(bt + blk0 + lane) : 0;
+            };
+            int32_t id_next = tile_id(0);
+            for (int j = 0; j < n; ++j, ++kt) {
+                const int stg = kt % C::kStages;
+                const int blk0 = (t_begin + j) * kBN / b;
+                const int nb = min(kBN / b, nblk_seq - blk0);
+                const uint32_t bytes = (uint32_t)nb * b * 128 * C::kPanels;
+                const int32_t id = id_next;
+                if (j + 1 < n) id_next = tile_id(j + 1);
+                if (lane < nb && (id < 0 || (int64_t)id >= p.num_blocks)) atomicOr(p.err, (int)UA_DEVERR_BLOCK_ID);
+                if (kt >= C::kStages && !(ok = wwait(k_empty0 + 8 * stg, ((kt / C::kStages) + 1) & 1))) break;
+                if (lane == 0) mbar_arrive_expect_tx(k_full0 + 8 * stg, bytes);
+                __syncwarp();
+                if (lane < nb) {
 #pragma unroll
-                for (int pn = 0; pn < C::kPanels; ++pn)
-                    tma_load_4d(sV + stg * C::kTile + pn * C::kPanel + lane * b * 128, &tm_v, pn * 64, hkv, 0, id,
-                                v_full0 + 8 * stg);
+                    for (int pn = 0; pn < C::kPanels; ++pn)
+                        tma_load_4d(sK + stg * C::kTile + pn * C::kPanel + lane * b * 128, &tm_k, pn * 64, h_now, 0, id,
+                                    k_full0 + 8 * stg);
+                }
+                if (kt >= C::kStages && !(ok = wwait(v_empty0 + 8 * stg, ((kt / C::kStages) + 1) & 1))) {
+                    k_extra = 1;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(v_full0 + 8 * stg, bytes);
+                __syncwarp();
+                if (lane < nb) {
+#pragma unroll
+                    for (int pn = 0; pn < C::kPanels; ++pn)
+                        tma_load_4d(sV + stg * C::kTile + pn * C::kPanel + lane * b * 128, &tm_v, pn * 64, h_now, 0, id,
+                                    v_full0 + 8 * stg);
+                }
             }
-            v_out = j + 1;
+            if (!ok) break;
         }
+        if (lane == 0) w.joins[blockIdx.x] = join;
         if (*abort_flag && lane == 0) {
             // Let every copy this warp issued land before the CTA ends.
-            mbar_wait_bounded(q_full, 0);
-            for (int j = max(0, k_out - C::kStages); j < k_out; ++j)
+            if (qn > 0) mbar_wait_bounded(q_full, (qn - 1) & 1);
+            for (int j = max(0, kt + k_extra - C::kStages); j < kt + k_extra; ++j)
                 mbar_wait_bounded(k_full0 + 8 * (j % C::kStages), (j / C::kStages) & 1);
-            for (int j = max(0, v_out - C::kStages); j < v_out; ++j)
+            for (int j = max(0, kt - C::kStages); j < kt; ++j)
                 mbar_wait_bounded(v_full0 + 8 * (j % C::kStages), (j / C::kStages) & 1);
         }
         __syncwarp();
@@ -293,50 +434,68 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint64_t qd = tc::smem_desc_sw128(sQ, 16, 1024);
         const uint64_t kd = tc::smem_desc_sw128(sK, 16, 1024);
         const uint64_t vd = tc::smem_desc_sw128(sV, C::kPanel, 1024);
-        auto issue_qk = [&](int j) -> bool {
-            const int stg = j % C::kStages, buf = j % C::kBufs;
-            // Testing hook: the first K wait waits on a barrier that nothing
-            // completes and gives up after stall_ns.
-            if (p.stall && j == 0 &&
-                !__all_sync(0xffffffffu, wait_or_abort(never, 0, abort_flag, p.err, (uint64_t)p.stall_ns)))
-                return false;
-            if (!wwait(k_full0 + 8 * stg, (j / C::kStages) & 1)) return false;
-            tc::fence_after_sync();
-            if (lane == 0) {
-                const uint64_t kst = kd + (uint64_t)(stg * (C::kTile >> 4));
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    tc::mma_bf16(tmem + buf * kBN, qd + (k >> 2) * (C::kQPanel >> 4) + (k & 3) * 2,
-                                 kst + (k >> 2) * (C::kPanel >> 4) + (k & 3) * 2, idesc_qk, k > 0 ? 1u : 0u);
-                tc::commit(s_full0 + 8 * buf);
-                tc::commit(k_empty0 + 8 * stg);
-            }
+        int gt = 0, qn = 0;                           // key tiles and units with work before this unit
+        bool ok = true;
+        for (int u = 0;; ++u) {
+            const int slot = u & 1;
+            if (!(ok = wwait(u_full0 + 8 * slot, (u >> 1) & 1))) break;
+            const int live = units[slot].live, zero = units[slot].zero, n = units[slot].n;
             __syncwarp();
-            return true;
-        };
-        bool ok = wwait(q_full, 0) && issue_qk(0);
-        for (int j = 0; ok && j < n; ++j) {
-            const int stg = j % C::kStages, buf = j % C::kBufs;
-            // With two S tiles the next one is filled while the softmax has this one.
-            if (C::kBufs == 2 && j + 1 < n && !(ok = issue_qk(j + 1))) break;
-            if (!(ok = wwait(v_ready0 + 8 * stg, (j / C::kStages) & 1))) break;
-            if (!(ok = wwait(p_full0 + 8 * buf, (j / C::kBufs) & 1))) break;
-            tc::fence_after_sync();
-            if (lane == 0) {
-                const uint64_t vst = vd + (uint64_t)(stg * (C::kTile >> 4));
+            if (lane == 0) mbar_arrive(u_empty0 + 8 * slot);
+            if (!live) break;
+            if (zero) continue;
+            auto issue_qk = [&](int j) -> bool {
+                const int kt = gt + j, stg = kt % C::kStages, buf = kt % C::kBufs;
+                // Testing hook: the first K wait waits on a barrier that nothing
+                // completes and gives up after stall_ns.
+                if (p.stall && kt == 0 &&
+                    !__all_sync(0xffffffffu, wait_or_abort(never, 0, abort_flag, p.err, (uint64_t)p.stall_ns)))
+                    return false;
+                if (!wwait(k_full0 + 8 * stg, (kt / C::kStages) & 1)) return false;
+                tc::fence_after_sync();
+                if (lane == 0) {
+                    const uint64_t kst = kd + (uint64_t)(stg * (C::kTile >> 4));
 #pragma unroll
-                for (int k = 0; k < kBN / 16; ++k)
+                    for (int k = 0; k < D / 16; ++k)
+                        tc::mma_bf16(tmem + buf * kBN, qd + (k >> 2) * (C::kQPanel >> 4) + (k & 3) * 2,
+                                     kst + (k >> 2) * (C::kPanel >> 4) + (k & 3) * 2, idesc_qk, k > 0 ? 1u : 0u);
+                    tc::commit(s_full0 + 8 * buf);
+                    tc::commit(k_empty0 + 8 * stg);
+                    if (j + 1 == n) tc::commit(q_empty);      // the last read of Q
+                }
+                __syncwarp();
+                return true;
+            };
+            if (!(ok = wwait(q_full, qn & 1) && issue_qk(0))) break;
+            for (int j = 0; ok && j < n; ++j) {
+                const int kt = gt + j, stg = kt % C::kStages, buf = kt % C::kBufs;
+                // With two S tiles the next one is filled while the softmax has this one.
+                if (C::kBufs == 2 && j + 1 < n && !(ok = issue_qk(j + 1))) break;
+                if (!(ok = wwait(v_ready0 + 8 * stg, (kt / C::kStages) & 1))) break;
+                if (!(ok = wwait(p_full0 + 8 * buf, (kt / C::kBufs) & 1))) break;
+                // The first P V overwrites O: the epilogue in front must have read it.
+                if (j == 0 && qn > 0 && !(ok = wwait(o_free, (qn - 1) & 1))) break;
+                tc::fence_after_sync();
+                if (lane == 0) {
+                    const uint64_t vst = vd + (uint64_t)(stg * (C::kTile >> 4));
 #pragma unroll
-                    for (int h = 0; h < D / kNV; ++h)
-                        // A = P from tensor memory (16 keys = 8 columns), B = V
-                        // MN-major, two 64-dim panels.
-                        tc::mma_bf16_ts(tmem + C::kTmemO + h * kNV, tmem + buf * kBN + k * 8,
-                                        vst + h * 2 * (C::kPanel >> 4) + k * 128, idesc_pv, (j > 0 || k > 0) ? 1u : 0u);
-                tc::commit(o_done0 + 8 * buf);
-                tc::commit(v_empty0 + 8 * stg);
+                    for (int k = 0; k < kBN / 16; ++k)
+#pragma unroll
+                        for (int h = 0; h < D / kNV; ++h)
+                            // A = P from tensor memory (16 keys = 8 columns), B = V
+                            // MN-major, two 64-dim panels.
+                            tc::mma_bf16_ts(tmem + C::kTmemO + h * kNV, tmem + buf * kBN + k * 8,
+                                            vst + h * 2 * (C::kPanel >> 4) + k * 128, idesc_pv,
+                                            (j > 0 || k > 0) ? 1u : 0u);
+                    tc::commit(o_done0 + 8 * buf);
+                    tc::commit(v_empty0 + 8 * stg);
+                }
+                __syncwarp();
+                if (C::kBufs == 1 && j + 1 < n) ok = issue_qk(j + 1);
             }
-            __syncwarp();
-            if (C::kBufs == 1 && j + 1 < n) ok = issue_qk(j + 1);
+            if (!ok) break;
+            gt += n;
+            ++qn;
         }
         if (*abort_flag) {
             // No MMA of this thread may still run when tensor memory is freed.
@@ -346,226 +505,286 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
     } else if (warp == kWarpFix) {
         // ------------------- V values that some rows must not see -------------------
-        for (int j = 0; j < n; ++j) {
-            const int stg = j % C::kStages, key0 = (t_begin + j) * kBN;
-            if (!wwait(v_full0 + 8 * stg, (j / C::kStages) & 1)) break;
-            if (edge_tile(key0)) {
-                uint8_t* v = smem + C::kOffV + stg * C::kTile;
-                bool odd = false;
-                auto clear = [&](int k_lo, int k_hi) {         // keys of the tile
-                    const int words = (k_hi - k_lo) * 8;       // 16 bytes each, per panel
-                    for (int pn = 0; pn < C::kPanels; ++pn)
-                        for (int e = lane; e < words; e += 32) {
-                            uint4* at = reinterpret_cast<uint4*>(v + pn * C::kPanel + k_lo * 128) + e;
-                            uint4 x = *at;
-                            uint32_t* w = &x.x;
-                            bool hit = false;
+        int gt = 0;
+        bool ok = true;
+        for (int u = 0; ok; ++u) {
+            const int slot = u & 1;
+            if (!(ok = wwait(u_full0 + 8 * slot, (u >> 1) & 1))) break;
+            const TreeUnit& un = units[slot];
+            const int live = un.live, zero = un.zero, n = un.n, t_begin = un.t_begin, sk = un.sk, ctx = sk - un.sq;
+            const int full_lo = window ? max(0, sk - p.window) : 0, vis_beg = window ? max(0, ctx - p.window + 1) : 0;
+            for (int j = 0; live && !zero && j < n; ++j, ++gt) {
+                const int stg = gt % C::kStages, key0 = (t_begin + j) * kBN;
+                if (!(ok = wwait(v_full0 + 8 * stg, (gt / C::kStages) & 1))) break;
+                if (key0 < full_lo || key0 + kBN > ctx) {
+                    uint8_t* v = smem + C::kOffV + stg * C::kTile;
+                    bool odd = false;
+                    auto clear = [&](int k_lo, int k_hi) {         // keys of the tile
+                        const int words = (k_hi - k_lo) * 8;       // 16 bytes each, per panel
+                        for (int pn = 0; pn < C::kPanels; ++pn)
+                            for (int e = lane; e < words; e += 32) {
+                                uint4* at = reinterpret_cast<uint4*>(v + pn * C::kPanel + k_lo * 128) + e;
+                                const uint4 x = *at;
+                                uint32_t y[4] = {x.x, x.y, x.z, x.w};
+                                bool hit = false;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                if ((w[i] & 0x7f80u) == 0x7f80u) {
-                                    w[i] &= 0xffff0000u;
-                                    hit = true;
+                                for (int i = 0; i < 4; ++i) {
+                                    if ((y[i] & 0x7f80u) == 0x7f80u) {
+                                        y[i] &= 0xffff0000u;
+                                        hit = true;
+                                    }
+                                    if ((y[i] & 0x7f800000u) == 0x7f800000u) {
+                                        y[i] &= 0xffffu;
+                                        hit = true;
+                                    }
                                 }
-                                if ((w[i] & 0x7f800000u) == 0x7f800000u) {
-                                    w[i] &= 0xffffu;
-                                    hit = true;
-                                }
+                                if (hit) *at = make_uint4(y[0], y[1], y[2], y[3]);
+                                // (What lies in slots that no key has is nobody's.)
+                                const int key = key0 + k_lo + (e >> 3);
+                                odd |= hit && key >= vis_beg && key < sk;
                             }
-                            if (hit) *at = x;
-                            odd |= hit;
-                        }
-                };
-                const int part = min(max(full_lo - key0, 0), kBN);
-                clear(0, part);
-                clear(max(part, min(max(ctx - key0, 0), kBN)), kBN);
-                if (odd) *odd_flag = 1;
-                fence_proxy_async_smem();
+                    };
+                    const int part = min(max(full_lo - key0, 0), kBN);
+                    clear(0, part);
+                    clear(max(part, min(max(ctx - key0, 0), kBN)), kBN);
+                    if (odd) units[slot].odd = 1;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(v_ready0 + 8 * stg);
                 __syncwarp();
             }
-            if (lane == 0) mbar_arrive(v_ready0 + 8 * stg);
-            __syncwarp();
+            // (The slot is given back by the softmax threads behind the epilogue.)
+            if (lane == 0) mbar_arrive(u_empty0 + 8 * slot);
+            if (!live) break;
         }
     } else {
         // ------------------------------ softmax, epilogue ------------------------------
         const int r = threadIdx.x;
-        const int i = first + r / g;
-        const bool valid = r < g * ppt && i <= last;
-        const int head = hkv * g + r % g;
-        const bool live = __any_sync(0xffffffffu, valid);   // else the warp only keeps the barriers going
         const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
-        const bool softcap = GEN && (p.flags & UA_FLAG_SOFTCAP) != 0;
-        const bool alibi = GEN && (p.flags & UA_FLAG_ALIBI) != 0;
-        const float slope = alibi && valid ? __ldg(p.alibi + head) * kLog2e : 0.f;
-        const uint32_t* mask = p.tree_mask + (q0 + min(i, last)) * p.mask_stride;
-        int lo = 0;
-        if (window && valid) {
-            const int at = __ldg(p.positions + q0 + i);
-            if (at < ctx || at >= sk) atomicOr(p.err, (int)UA_DEVERR_TREE);
-            lo = max(0, node_position(p, q0, i, ctx, sk) - p.window + 1);
-        }
-        const int64_t row = (q0 + i) * p.hq + head;
-        float m = -INFINITY, l = 0.f;
-        bool ok = true;
+        const bool softcap = MODE == kCap || (MODE == kAlibi && (p.flags & UA_FLAG_SOFTCAP) != 0);
         // The score chain is in log2 units from the products on (a factor of zero
         // would make NaN of masked scores).
         const float cap = p.softcap * kLog2e, fac = fmaxf(p.scale * (softcap ? 1.f / p.softcap : kLog2e), 0x1p-126f);
-        for (int j = 0; j < n; ++j) {
-            const int buf = j % C::kBufs;
-            if (!(ok = wwait(s_full0 + 8 * buf, (j / C::kBufs) & 1))) break;
-            const int key0 = (t_begin + j) * kBN;
-            const uint32_t s_col = trow + buf * kBN;
-            const bool edge = edge_tile(key0);
-            bool reanchor = false;
-            float alpha = 1.f;
-            if (live) {
-                tc::fence_after_sync();
-                // First pass: the maximum.  Plain scores stay as the MMA left them; a
-                // general score chain or a mask is applied here and written back.
-                float top = -INFINITY;
+        int gt = 0;
+        bool ok = true;
+        for (int u = 0;; ++u) {
+            const int slot_u = u & 1;
+            if (!(ok = wwait(u_full0 + 8 * slot_u, (u >> 1) & 1))) break;
+            const TreeUnit& un = units[slot_u];
+            const int live_u = un.live, zero = un.zero, n = un.n, t_begin = un.t_begin;
+            const int sq = un.sq, sk = un.sk, ctx = sk - sq, last = un.last, hkv = un.hkv, seq = un.s;
+            const int part = un.slot;
+            const int64_t q0 = un.q0;
+            if (!live_u) break;
+            const int i = un.first + r / g;
+            const bool valid = r < g * ppt && i <= last;
+            const int head = hkv * g + r % g;
+            const int64_t row = (q0 + i) * p.hq + head;
+            if (zero) {
+                if (valid) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + row * D);
 #pragma unroll 1
-                for (int c = 0; c < kBN; c += kCols) {
-                    uint32_t x[kCols / 32][32];
-#pragma unroll
-                    for (int h = 0; h < kCols / 32; ++h) tc::ld32(s_col + c + h * 32, x[h]);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int h = 0; h < kCols / 32; ++h) {
-                        const int key = key0 + c + h * 32;
-                        if constexpr (GEN) {
-                            const bool nodes = alibi && key + 32 > ctx;
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                float v = __uint_as_float(x[h][e]) * fac;
-                                if (softcap) v = cap * tanh_from_exp2(v);
-                                if (alibi) {
-                                    int at = key + e;
-                                    if (nodes && at >= ctx && at < sk) at = node_position(p, q0, at - ctx, ctx, sk);
-                                    v += slope * (float)(at - ctx);
-                                }
-                                x[h][e] = __float_as_uint(v);
-                            }
-                        }
-                        if (edge) {
-                            const uint32_t see = seen_keys(p, mask, q0, key, ctx, sq, sk, lo);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!(see >> e & 1u)) x[h][e] = __float_as_uint(-INFINITY);
-                        }
-                        if (GEN || edge) tc::st32(s_col + c + h * 32, x[h]);
-                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-#pragma unroll
-                            for (int a = 0; a < 4; ++a)
-                                mx[a] = fmax3(mx[a], __uint_as_float(x[h][e + 2 * a]), __uint_as_float(x[h][e + 2 * a + 1]));
-                        top = fmax3(top, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    }
+                    for (int c = 0; c < D / 8; ++c) dst[c] = make_uint4(0, 0, 0, 0);
                 }
-                if (GEN || edge) tc::wait_st();
-                if constexpr (!GEN) top *= fac;
-                reanchor = top > m + kLazy;
-                if (reanchor) {
-                    alpha = fast_exp2(m - top);
-                    m = top;
-                }
-                // Second pass: P = 2^(x - m), fp32 into the row sum, bf16 (V's type, as
-                // the MMA wants; 2^-8 off each) over columns of S that have been read.
-                const float mu = m == -INFINITY ? 0.f : m;
-                const float2 f2 = make_float2(GEN ? 1.f : fac, GEN ? 1.f : fac), nm2 = make_float2(-mu, -mu);
-                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-                for (int c = 0; c < kBN; c += kCols) {
-                    uint32_t x[kCols / 32][32];
-#pragma unroll
-                    for (int h = 0; h < kCols / 32; ++h) tc::ld32(s_col + c + h * 32, x[h]);
-                    tc::wait_ld();
-#pragma unroll
-                    for (int h = 0; h < kCols / 32; ++h) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const float2 pr = exp2_pair_f32(
-                                ffma2(make_float2(__uint_as_float(x[h][e]), __uint_as_float(x[h][e + 1])), f2, nm2));
-                            sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], pr);
-                            pk[e / 2] = pack_bf16x2(pr.x, pr.y);
-                        }
-                        tc::st16(s_col + c / 2 + h * 16, pk);
-                    }
-                }
-                const float2 both = fadd2(sum[0], sum[1]);
-                l = l * alpha + (both.x + both.y);
-                tc::wait_st();
+                mbar_arrive(u_empty0 + 8 * slot_u);
+                continue;
             }
-            if (live && j > 0 && __any_sync(0xffffffffu, reanchor)) {
-                // O holds the P V of the tiles up to j - 1.  With one S tile that product
-                // was issued in front of this tile's Q K^T, which is complete.
-                if (C::kBufs == 2 && !(ok = wwait(o_done0 + 8 * ((j - 1) & 1), ((j - 1) >> 1) & 1))) break;
+            const bool live = __any_sync(0xffffffffu, valid);   // else the warp only keeps the barriers going
+            const int full_lo = window ? max(0, sk - p.window) : 0;
+            const float slope = MODE == kAlibi && valid ? __ldg(p.alibi + head) * kLog2e : 0.f;
+            const uint32_t* mask = p.tree_mask + (q0 + min(i, last)) * p.mask_stride;
+            int lo = 0;
+            if (window && valid) {
+                const int at = __ldg(p.positions + q0 + i);
+                if (at < ctx || at >= sk) atomicOr(p.err, (int)UA_DEVERR_TREE);
+                lo = max(0, node_position(p, q0, i, ctx, sk) - p.window + 1);
+            }
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; j < n; ++j) {
+                const int kt = gt + j, buf = kt % C::kBufs;
+                if (!(ok = wwait(s_full0 + 8 * buf, (kt / C::kBufs) & 1))) break;
+                const int key0 = (t_begin + j) * kBN;
+                const uint32_t s_col = trow + buf * kBN;
+                const bool edge = key0 < full_lo || key0 + kBN > ctx;
+                bool reanchor = false;
+                float alpha = 1.f;
+                if (live) {
+                    tc::fence_after_sync();
+                    // First pass: the maximum.  Plain scores stay as the MMA left them;
+                    // score terms and masks are applied here and written back.
+                    float top = -INFINITY;
+                    if (MODE != kPlain || edge) {
+#pragma unroll 1
+                        for (int c = 0; c < kBN; c += 32) {
+                            uint32_t x[32];
+                            tc::ld32(s_col + c, x);
+                            const int key = key0 + c;
+                            const uint32_t see = edge ? seen_keys(p, mask, q0, key, ctx, sq, sk, lo) : 0xffffffffu;
+                            int at = key + lane;                // position of the lane's key
+                            if (MODE == kAlibi && at >= ctx && at < sk) at = node_position(p, q0, at - ctx, ctx, sk);
+                            tc::wait_ld();
+                            if (softcap) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    x[e] = __float_as_uint(cap * tanh_from_exp2(__uint_as_float(x[e]) * fac));
+                            } else if (MODE != kPlain) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * fac);
+                            }
+                            if constexpr (MODE == kAlibi) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    x[e] = __float_as_uint(__uint_as_float(x[e]) +
+                                                           slope * (float)(__shfl_sync(0xffffffffu, at, e) - ctx));
+                            }
+                            if (edge) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(see >> e & 1u)) x[e] = __float_as_uint(-INFINITY);
+                            }
+                            tc::st32(s_col + c, x);
+                            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+#pragma unroll
+                                for (int a = 0; a < 2; ++a)
+                                    mx[a] = fmax3(mx[a], __uint_as_float(x[e + 2 * a]), __uint_as_float(x[e + 2 * a + 1]));
+                            top = fmax3(top, mx[0], mx[1]);
+                        }
+                        tc::wait_st();
+                    } else {
+#pragma unroll 1
+                        for (int c = 0; c < kBN; c += kCols) {
+                            uint32_t x[kCols / 32][32];
+#pragma unroll
+                            for (int h = 0; h < kCols / 32; ++h) tc::ld32(s_col + c + h * 32, x[h]);
+                            tc::wait_ld();
+                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int h = 0; h < kCols / 32; ++h)
+#pragma unroll
+                                for (int e = 0; e < 32; e += 8)
+#pragma unroll
+                                    for (int a = 0; a < 4; ++a)
+                                        mx[a] = fmax3(mx[a], __uint_as_float(x[h][e + 2 * a]),
+                                                      __uint_as_float(x[h][e + 2 * a + 1]));
+                            top = fmax3(top, fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        }
+                    }
+                    if constexpr (MODE == kPlain) top *= fac;
+                    reanchor = top > m + kLazy;
+                    if (reanchor) {
+                        alpha = fast_exp2(m - top);
+                        m = top;
+                    }
+                    // Second pass: P = 2^(x - m), fp32 into the row sum, bf16 (V's type, as
+                    // the MMA wants; 2^-8 off each) over columns of S that have been read.
+                    const float mu = m == -INFINITY ? 0.f : m;
+                    const float f = MODE == kPlain ? fac : 1.f;
+                    const float2 f2 = make_float2(f, f), nm2 = make_float2(-mu, -mu);
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                    for (int c = 0; c < kBN; c += kCols) {
+                        uint32_t x[kCols / 32][32];
+#pragma unroll
+                        for (int h = 0; h < kCols / 32; ++h) tc::ld32(s_col + c + h * 32, x[h]);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int h = 0; h < kCols / 32; ++h) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2) {
+                                const float2 pr = exp2_pair_f32(
+                                    ffma2(make_float2(__uint_as_float(x[h][e]), __uint_as_float(x[h][e + 1])), f2, nm2));
+                                sum[(e >> 1) & 1] = fadd2(sum[(e >> 1) & 1], pr);
+                                pk[e / 2] = pack_bf16x2(pr.x, pr.y);
+                            }
+                            tc::st16(s_col + c / 2 + h * 16, pk);
+                        }
+                    }
+                    const float2 both = fadd2(sum[0], sum[1]);
+                    l = l * alpha + (both.x + both.y);
+                    tc::wait_st();
+                }
+                if (live && j > 0 && __any_sync(0xffffffffu, reanchor)) {
+                    // O holds the P V of the tiles up to j - 1.  With one S tile that product
+                    // was issued in front of this tile's Q K^T, which is complete.
+                    if (C::kBufs == 2 && !(ok = wwait(o_done0 + 8 * ((kt - 1) & 1), ((kt - 1) >> 1) & 1))) break;
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tc::ld32(trow + C::kTmemO + c * 32, o);
+                        tc::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tc::st32(trow + C::kTmemO + c * 32, o);
+                    }
+                    tc::wait_st();
+                }
+                tc::fence_before_sync();
+                mbar_arrive(p_full0 + 8 * buf);
+            }
+            if (!ok) break;
+            gt += n;
+            if (!(ok = wwait(o_done0 + 8 * ((gt - 1) % C::kBufs), ((gt - 1) / C::kBufs) & 1))) break;
+            if (live) {
+                // tcgen05.ld is warp-collective: every lane of a live warp loads.
                 tc::fence_after_sync();
+                const bool odd = *reinterpret_cast<const volatile int32_t*>(&un.odd) != 0;
+                const int64_t prow = (int64_t)part * w.slot_rows + r;
+                float f = 1.f;
+                if (part >= 0) {
+                    if (valid) {
+                        p.part_ml[prow * 2 + 0] = stored_max(m, l);
+                        p.part_ml[prow * 2 + 1] = l;
+                    }
+                } else {
+                    float L = l;
+                    if (p.flags & UA_FLAG_SINKS) {
+                        const float s2 = __ldg(p.sinks + head) * kLog2e;
+                        if (s2 == INFINITY) {
+                            L = 0.f;
+                        } else if (s2 > m) {
+                            f = m == -INFINITY ? 0.f : fast_exp2(m - s2);
+                            L = L * f + 1.0f;
+                        } else if (s2 != -INFINITY) {
+                            L += fast_exp2(s2 - m);
+                        }
+                    }
+                    f = L > 0.f ? f * __frcp_rn(L) : 0.f;
+                }
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
                     tc::ld32(trow + C::kTmemO + c * 32, o);
                     tc::wait_ld();
+                    if (!valid) continue;
+                    if (odd) {
+                        const int beg = t_begin * kBN, end = min((t_begin + n) * kBN, sk);
+                        add_unbounded(p, seq, hkv, q0, mask, beg, min(end, full_lo), ctx, sq, sk, lo, c * 32, o);
+                        add_unbounded(p, seq, hkv, q0, mask, max(beg, max(full_lo, ctx)), end, ctx, sq, sk, lo, c * 32, o);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                    tc::st32(trow + C::kTmemO + c * 32, o);
-                }
-                tc::wait_st();
-            }
-            tc::fence_before_sync();
-            mbar_arrive(p_full0 + 8 * buf);
-        }
-        if (ok) ok = wwait(o_done0 + 8 * ((n - 1) % C::kBufs), ((n - 1) / C::kBufs) & 1);
-        if (ok && live) {
-            // tcgen05.ld is warp-collective: every lane of a live warp loads.
-            tc::fence_after_sync();
-            const bool odd = *odd_flag != 0;
-            float f = 1.f;
-            if (split) {
-                if (valid) {
-                    p.part_ml[(row * p.splits + seg) * 2 + 0] = stored_max(m, l);
-                    p.part_ml[(row * p.splits + seg) * 2 + 1] = l;
-                }
-            } else {
-                float L = l;
-                if (p.flags & UA_FLAG_SINKS) {
-                    const float s2 = __ldg(p.sinks + head) * kLog2e;
-                    if (s2 == INFINITY) {
-                        L = 0.f;
-                    } else if (s2 > m) {
-                        f = m == -INFINITY ? 0.f : fast_exp2(m - s2);
-                        L = L * f + 1.0f;
-                    } else if (s2 != -INFINITY) {
-                        L += fast_exp2(s2 - m);
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                    if (part >= 0) {
+                        part_store32(p, prow * D + c * 32, o);
+                    } else {
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + row * (int64_t)D + c * 32);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            dst[e / 8] = make_uint4(pack_bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
+                                                    pack_bf16x2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
+                                                    pack_bf16x2(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
+                                                    pack_bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
                     }
                 }
-                f = L > 0.f || L != L ? f * __frcp_rn(L) : 0.f;
             }
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tc::ld32(trow + C::kTmemO + c * 32, o);
-                tc::wait_ld();
-                if (!valid) continue;
-                if (odd) {
-                    const int beg = t_begin * kBN, end = min((t_begin + n) * kBN, sk);
-                    add_unbounded(p, s, hkv, q0, mask, beg, min(end, full_lo), ctx, sq, sk, lo, c * 32, o);
-                    add_unbounded(p, s, hkv, q0, mask, max(beg, max(full_lo, ctx)), end, ctx, sq, sk, lo, c * 32, o);
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                if (split) {
-                    part_store32(p, (row * p.splits + seg) * D + c * 32, o);
-                } else {
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + row * (int64_t)D + c * 32);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        dst[e / 8] = make_uint4(pack_bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
-                                                pack_bf16x2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
-                                                pack_bf16x2(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
-                                                pack_bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
-                }
-            }
+            // O has been read: the next unit's first P V may overwrite it.
+            tc::fence_before_sync();
+            mbar_arrive(o_free);
+            mbar_arrive(u_empty0 + 8 * slot_u);
         }
     }
 
@@ -577,38 +796,127 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
 }
 
+// Joins the pieces of the item that begins in share blockIdx.x and is cut by its end, one
+// warp per row; pieces are added in their order.
+template <int D>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const FwdParams p, const TreeShares w) {
+    constexpr int DPL = D / 32;
+    constexpr int kAhead = D == 256 ? 4 : 8;
+    griddep_wait();                          // the partials are complete
+    const TreeJoin join = w.joins[blockIdx.x];
+    const int lane = threadIdx.x & 31;
+    if (join.pieces == 0) return;
+    // Piece k > 0 is the first of share blockIdx.x + k.
+    auto piece = [&](int k) -> int64_t {
+        return (int64_t)(k ? 2 * ((int)blockIdx.x + k) : join.slot) * w.slot_rows;
+    };
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < join.nodes * p.g; r += gridDim.y * 8) {
+        float M = -INFINITY;
+        for (int k = lane; k < join.pieces; k += 32) M = fmaxf(M, ml[piece(k) + r].x);
+#pragma unroll
+        for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+        float o[DPL];
+#pragma unroll
+        for (int t = 0; t < DPL; ++t) o[t] = 0.f;
+        float L = 0.f;
+        if (M != -INFINITY) {
+            float2 mine = make_float2(0.f, 0.f);
+            for (int k0 = 0; k0 < join.pieces; k0 += kAhead) {
+                if (k0 % 32 == 0) mine = ml[piece(min(k0 + lane, join.pieces - 1)) + r];
+                float x[kAhead][DPL];
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q) {
+                    if (k0 + q >= join.pieces) break;
+                    const int64_t po = (piece(k0 + q) + r) * D + lane * DPL;
+#pragma unroll
+                    for (int t = 0; t < DPL; ++t) x[q][t] = part_load(p, po + t);
+                }
+#pragma unroll
+                for (int q = 0; q < kAhead; ++q) {
+                    if (k0 + q >= join.pieces) break;
+                    const float mk = __shfl_sync(0xffffffffu, mine.x, (k0 + q) & 31);
+                    const float lk = __shfl_sync(0xffffffffu, mine.y, (k0 + q) & 31);
+                    if (mk == -INFINITY) continue;   // a piece without keys: its o means nothing
+                    const float a = fast_exp2(mk - M);
+                    L = fmaf(a, lk, L);
+#pragma unroll
+                    for (int t = 0; t < DPL; ++t) o[t] = fmaf(a, x[q][t], o[t]);
+                }
+            }
+        }
+        const int h = join.hkv * p.g + r % p.g;
+        float f = 1.f;
+        if (p.flags & UA_FLAG_SINKS) {
+            const float s2 = __ldg(p.sinks + h) * kLog2e;
+            if (s2 == INFINITY) {
+                L = 0.f;
+            } else if (s2 > M) {
+                f = M == -INFINITY ? 0.f : fast_exp2(M - s2);
+                L = L * f + 1.0f;
+            } else if (s2 != -INFINITY) {
+                L += fast_exp2(s2 - M);
+            }
+        }
+        f = L > 0.f ? f * __frcp_rn(L) : 0.f;
+        __nv_bfloat16* dst = p.out + ((join.row0 + r / p.g) * p.hq + h) * D + lane * DPL;
+#pragma unroll
+        for (int t = 0; t < DPL; ++t) dst[t] = __float2bfloat16_rn(o[t] * f);
+    }
+}
+
 template <int D>
 cudaError_t launch_tree_d(const TreePlan& plan, const CUtensorMap& tq, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                           const FwdParams& p, cudaStream_t stream) {
-    const bool gen = (p.flags & (UA_FLAG_SOFTCAP | UA_FLAG_ALIBI)) != 0;
-    auto kern = gen ? tree_kernel<D, true> : tree_kernel<D, false>;
+    auto kern = (p.flags & UA_FLAG_ALIBI)     ? tree_kernel<D, kAlibi>
+                : (p.flags & UA_FLAG_SOFTCAP) ? tree_kernel<D, kCap>
+                                              : tree_kernel<D, kPlain>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
-    dim3 grid((unsigned)(plan.tiles * plan.splits), (unsigned)p.hk, (unsigned)p.num_seqs);
-    kern<<<grid, kThreadsT, TCfg<D>::kSmem, stream>>>(tq, tm_k, tm_v, p, plan.tiles);
-    return cudaGetLastError();
+    kern<<<(unsigned)plan.ctas, kThreadsT, TCfg<D>::kSmem, stream>>>(tq, tm_k, tm_v, p, plan.shares);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || plan.ctas == 1) return e;
+    return launch_early(tree_merge_kernel<D>, dim3((unsigned)plan.ctas, 4), 256, 0, stream, p, plan.shares);
+}
+
+int tile_keys(int d) { return d == 256 ? 64 : 128; }
+int ctas_per_sm(int d) { return d == 256 ? 1 : 2; }
+
+// Bytes of the partials of `ctas` shares whose tiles have `rows` rows, and of the joins.
+size_t shares_bytes(int64_t ctas, int64_t rows, int d) {
+    return (size_t)ctas * (2 * rows * (d + 2) * sizeof(float) + sizeof(TreeJoin)) + 16;
 }
 
 }  // namespace
 
-bool plan_tree(const FwdParams& p, int num_sms, size_t workspace_bytes, TreePlan* plan) {
+size_t tree_workspace_bytes(const ua_problem_desc& d, int num_sms) {
+    const int64_t g = d.num_q_heads / d.num_kv_heads;
+    if (g > kRows) return 0;
+    const int64_t rows = std::min<int64_t>(kRows / g, d.max_total_q) * g;
+    return shares_bytes((int64_t)ctas_per_sm(d.head_size) * num_sms, rows, d.head_size);
+}
+
+bool plan_tree(FwdParams* fp, int num_sms, void* workspace, size_t workspace_bytes, TreePlan* plan) {
+    const FwdParams& p = *fp;
     *plan = TreePlan();
-    if (p.g > kRows || p.max_seqlen_k > 1 << 30 || p.hk > 65535) return false;
-    const int ppt = kRows / p.g, bn = p.d == 256 ? 64 : 128, per_sm = p.d == 256 ? 1 : 2;
+    if (p.g > kRows || p.max_seqlen_k > 1 << 30) return false;
+    const int ppt = kRows / p.g, bn = tile_keys(p.d);
     const int64_t tiles = (p.max_seqlen_q + ppt - 1) / ppt;
-    const int64_t base = tiles * p.hk * p.num_seqs;
-    const int64_t slots = (int64_t)per_sm * num_sms;
-    // Segments: about four waves of CTAs, each of eight key tiles at least; down to one
-    // tile each while SMs are idle.
-    int64_t splits = std::min<int64_t>((4 * slots + base - 1) / base, std::max<int64_t>(1, p.max_seqlen_k / (8 * bn)));
-    splits = std::max<int64_t>(splits, std::min<int64_t>(slots / base, (p.max_seqlen_k + bn - 1) / bn));
-    const size_t per_split = (size_t)p.total_q * p.hq * (p.d + 2) * sizeof(float);
-    splits = std::max<int64_t>(1, std::min<int64_t>({splits, 64, (int64_t)(workspace_bytes / per_split)}));
-    const int64_t per = (p.max_seqlen_k + splits - 1) / splits;
-    plan->chunk = (int)std::min<int64_t>((per + bn - 1) / bn * bn, 1 << 30);
-    plan->splits = (int)((p.max_seqlen_k + (int64_t)plan->chunk - 1) / plan->chunk);
-    if (tiles * plan->splits > 0x7fffffffLL) return false;
-    plan->tiles = (int)tiles;
+    const int64_t rows = (int64_t)std::min(ppt, p.max_seqlen_q) * p.g;
+    if (tiles * p.num_seqs > 0x7fffffffLL) return false;
+    // No more CTAs than steps (as far as the host knows) and than the workspace has room for.
+    const int64_t steps = tiles * p.num_seqs * p.hk * ((p.max_seqlen_k + bn - 1) / bn);
+    int64_t ctas = std::min<int64_t>((int64_t)ctas_per_sm(p.d) * num_sms, steps);
+    while (ctas > 1 && shares_bytes(ctas, rows, p.d) > workspace_bytes) ctas = ctas * 7 / 8;
+    plan->ctas = (int)ctas;
+    plan->shares.tiles = (int)tiles;
+    plan->shares.least = 1;
+    plan->shares.slot_rows = (int)rows;
+    // Partials in front, then (m, l), then the joins.
+    fp->part_o = static_cast<float*>(workspace);
+    fp->part_ml = fp->part_o + (size_t)ctas * 2 * rows * p.d;
+    plan->shares.joins = reinterpret_cast<TreeJoin*>((reinterpret_cast<uintptr_t>(fp->part_ml + (size_t)ctas * 4 * rows) + 15) &
+                                                     ~uintptr_t(15));
     return true;
 }
 
