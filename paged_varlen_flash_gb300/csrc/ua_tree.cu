@@ -23,20 +23,22 @@
 // two S tiles.  Barriers, tensor memory and the K/V ring live on from item to item: the
 // next item's copies and first Q K^T run under the epilogue of the one before.
 //
-// Roles (7 warps):
+// Roles (8 warps):
 //   warps 0-3  softmax and epilogue: thread r owns row r (tensor-memory lane r); two
 //              passes over the tile's columns (maximum, then P);
-//   warp 4     walks through the share and copies (TMA): Q, then the K and V tiles, one
-//              lane per paged block;
-//   warp 5     MMA issuer and owner of tensor memory;
-//   warp 6     looks through V tiles with keys that some row does not see.
+//   warp 4     walks through the share and copies (TMA) Q and the K tiles, one lane per
+//              paged block;
+//   warp 5     looks through V tiles with keys that some row does not see;
+//   warp 6     copies the V tiles;
+//   warp 7     MMA issuer and owner of tensor memory (beside warp 3, which has the last
+//              rows and the least to do).
 // The softmax loops are kept short (32 or 64 columns, masks and score terms in a loop of
 // their own): unrolled over a row's 128 columns with every term they missed the
 // instruction cache (48 small trees with a softcap at d = 64: 88 us, of which 50 us the
 // cap).
 //
 // Masked keys: their scores are replaced, whatever K holds.  Their V rows reach the
-// product with P = 0, and 0 times an infinity or NaN is NaN; so warp 6 clears values
+// product with P = 0, and 0 times an infinity or NaN is NaN; so warp 5 clears values
 // that are not finite in such tiles, and the epilogue adds them again to the rows that
 // see their key (a flag, no cost while all values are finite).
 #include <algorithm>
@@ -55,12 +57,13 @@ namespace {
 
 using namespace pf;
 
-constexpr int kThreadsT = 224;
+constexpr int kThreadsT = 256;
 constexpr int kWarpCopy = 4;
-constexpr int kWarpMmaT = 5;
-constexpr int kWarpFix = 6;
+constexpr int kWarpFix = 5;
+constexpr int kWarpCopyV = 6;
+constexpr int kWarpMmaT = 7;
 constexpr int kCols = 64;          // columns of S a softmax thread holds at a time
-constexpr int kUnitReaders = 130;  // MMA and fix warps (a lane each), softmax threads
+constexpr int kUnitReaders = 131;  // V copy, MMA and fix warps (a lane each), softmax threads
 
 // Score chains: the scale alone, a softcap, ALiBi with or without a softcap.
 enum { kPlain = 0, kCap = 1, kAlibi = 2 };
@@ -81,9 +84,9 @@ static_assert(sizeof(TreeUnit) == 64, "unit descriptor");
 
 template <int D>
 struct TCfg {
-    static constexpr int kBN = D == 256 ? 64 : 128;     // keys per tile
-    static constexpr int kStages = D == 128 ? 1 : 2;    // K and V tiles each
-    static constexpr int kBufs = D == 256 ? 2 : 1;      // S tiles
+    static constexpr int kBN = 64;                      // keys per tile
+    static constexpr int kStages = D == 64 ? 4 : 2;     // K and V tiles each
+    static constexpr int kBufs = 2;                     // S tiles
     static constexpr int kCtas = D == 256 ? 1 : 2;      // per SM
     static constexpr int kPanels = D / 64;
     static constexpr int kQPanel = kRows * 128;         // 128 rows x 64 dims
@@ -163,6 +166,46 @@ __device__ __forceinline__ int item_steps(const FwdParams& p, int s, int r, uint
     return (sk + BN - 1) / BN - beg / BN;
 }
 
+// A piece's K or V tiles through their ring, by a whole warp: lane i copies paged block i
+// of each tile; block ids are fetched one tile ahead.  kt counts the ring's tiles.  (K and
+// V have a warp each: behind V tiles, whose stage waits for the softmax, K tiles came a
+// tile's time later.)
+template <int D, bool V>
+__device__ __forceinline__ bool copy_tiles(const FwdParams& p, const CUtensorMap& tm, uint32_t ring, uint32_t full0,
+                                           uint32_t empty0, int& kt, int s, int hkv, int sk, int t_begin, int n,
+                                           volatile int* abort_flag) {
+    using C = TCfg<D>;
+    constexpr int kBN = C::kBN;
+    const int lane = threadIdx.x & 31;
+    const int b = p.b, b_log2 = 31 - __clz(b), per_tile = kBN >> b_log2, nblk = (sk + b - 1) >> b_log2;
+    const int32_t* bt = p.block_table + (int64_t)s * p.bt_stride;
+    auto tile_id = [&](int j) -> int32_t {
+        const int blk = ((t_begin + j) << (6 - b_log2)) + lane;
+        return lane < per_tile && blk < nblk ? __ldg(bt + blk) : -1;
+    };
+    static_assert(kBN == 64, "tile of whole blocks");
+    int32_t id_next = tile_id(0);
+    for (int j = 0; j < n; ++j, ++kt) {
+        const int stg = kt % C::kStages;
+        const int nb = min(per_tile, nblk - ((t_begin + j) << (6 - b_log2)));
+        const int32_t id = id_next;
+        if (j + 1 < n) id_next = tile_id(j + 1);
+        if (!V && lane < nb && (id < 0 || (int64_t)id >= p.num_blocks)) atomicOr(p.err, (int)UA_DEVERR_BLOCK_ID);
+        if (kt >= C::kStages &&
+            !__all_sync(0xffffffffu, wait_or_abort(empty0 + 8 * stg, ((kt / C::kStages) + 1) & 1, abort_flag, p.err)))
+            return false;
+        if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * stg, (uint32_t)nb * b * 128 * C::kPanels);
+        __syncwarp();
+        if (lane < nb) {
+#pragma unroll
+            for (int pn = 0; pn < C::kPanels; ++pn)
+                tma_load_4d(ring + stg * C::kTile + pn * C::kPanel + lane * b * 128, &tm, pn * 64, hkv, 0, id,
+                            full0 + 8 * stg);
+        }
+    }
+    return true;
+}
+
 template <int D, int MODE>
 __global__ void __launch_bounds__(kThreadsT, TCfg<D>::kCtas)
 tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -219,6 +262,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         tc::tmem_alloc(smem_u32(tmem_slot), C::kCols2);
         tc::tmem_relinquish();
     }
+    griddep_launch();      // the merge kernel's CTAs may wait on SMs that are done
     // This CTA's share: entries (row tile, sequence) in order, each thread a run of them.
     const int64_t entries = (int64_t)w.tiles * p.num_seqs;
     const int64_t per = (entries + kThreadsT - 1) / kThreadsT;
@@ -283,10 +327,9 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
         }
-        const int b = p.b;
         int64_t x = x0, e = idle ? 0 : start[0];
         int hkv = idle ? 0 : start[1], step = idle ? 0 : start[2];
-        int u = 0, qn = 0, kt = 0, k_extra = 0;     // units, Q loads, K/V tiles; a K tile without its V
+        int u = 0, qn = 0, kt = 0;     // units, Q loads, K tiles
         TreeJoin join{0, 0, 0, 0, 0};
         bool ok = true;
         for (;; ++u) {
@@ -375,54 +418,35 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
             ++qn;
             __syncwarp();
-            const int nblk_seq = (sk + b - 1) / b;
-            const int32_t* bt = p.block_table + (int64_t)s * p.bt_stride;
-            auto tile_id = [&](int j) -> int32_t {
-                const int blk0 = (t_begin + j) * kBN / b;
-                return lane < min(kBN / b, nblk_seq - blk0) ? __ldg(bt + blk0 + lane) : 0;
-            };
-            int32_t id_next = tile_id(0);
-            for (int j = 0; j < n; ++j, ++kt) {
-                const int stg = kt % C::kStages;
-                const int blk0 = (t_begin + j) * kBN / b;
-                const int nb = min(kBN / b, nblk_seq - blk0);
-                const uint32_t bytes = (uint32_t)nb * b * 128 * C::kPanels;
-                const int32_t id = id_next;
-                if (j + 1 < n) id_next = tile_id(j + 1);
-                if (lane < nb && (id < 0 || (int64_t)id >= p.num_blocks)) atomicOr(p.err, (int)UA_DEVERR_BLOCK_ID);
-                if (kt >= C::kStages && !(ok = wwait(k_empty0 + 8 * stg, ((kt / C::kStages) + 1) & 1))) break;
-                if (lane == 0) mbar_arrive_expect_tx(k_full0 + 8 * stg, bytes);
-                __syncwarp();
-                if (lane < nb) {
-#pragma unroll
-                    for (int pn = 0; pn < C::kPanels; ++pn)
-                        tma_load_4d(sK + stg * C::kTile + pn * C::kPanel + lane * b * 128, &tm_k, pn * 64, h_now, 0, id,
-                                    k_full0 + 8 * stg);
-                }
-                if (kt >= C::kStages && !(ok = wwait(v_empty0 + 8 * stg, ((kt / C::kStages) + 1) & 1))) {
-                    k_extra = 1;
-                    break;
-                }
-                if (lane == 0) mbar_arrive_expect_tx(v_full0 + 8 * stg, bytes);
-                __syncwarp();
-                if (lane < nb) {
-#pragma unroll
-                    for (int pn = 0; pn < C::kPanels; ++pn)
-                        tma_load_4d(sV + stg * C::kTile + pn * C::kPanel + lane * b * 128, &tm_v, pn * 64, h_now, 0, id,
-                                    v_full0 + 8 * stg);
-                }
-            }
+            ok = copy_tiles<D, false>(p, tm_k, sK, k_full0, k_empty0, kt, s, h_now, sk, t_begin, n, abort_flag);
             if (!ok) break;
         }
         if (lane == 0) w.joins[blockIdx.x] = join;
         if (*abort_flag && lane == 0) {
             // Let every copy this warp issued land before the CTA ends.
             if (qn > 0) mbar_wait_bounded(q_full, (qn - 1) & 1);
-            for (int j = max(0, kt + k_extra - C::kStages); j < kt + k_extra; ++j)
+            for (int j = max(0, kt - C::kStages); j < kt; ++j)
                 mbar_wait_bounded(k_full0 + 8 * (j % C::kStages), (j / C::kStages) & 1);
+        }
+        __syncwarp();
+    } else if (warp == kWarpCopyV) {
+        // -------------------------------- copies of V --------------------------------
+        int kt = 0;
+        bool ok = true;
+        for (int u = 0;; ++u) {
+            const int slot = u & 1;
+            if (!(ok = wwait(u_full0 + 8 * slot, (u >> 1) & 1))) break;
+            const TreeUnit& un = units[slot];
+            const int live = un.live, zero = un.zero, s = un.s, hkv = un.hkv, sk = un.sk, t_begin = un.t_begin, n = un.n;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(u_empty0 + 8 * slot);
+            if (!live) break;
+            if (zero) continue;
+            if (!(ok = copy_tiles<D, true>(p, tm_v, sV, v_full0, v_empty0, kt, s, hkv, sk, t_begin, n, abort_flag))) break;
+        }
+        if (*abort_flag && lane == 0)
             for (int j = max(0, kt - C::kStages); j < kt; ++j)
                 mbar_wait_bounded(v_full0 + 8 * (j % C::kStages), (j / C::kStages) & 1);
-        }
         __syncwarp();
     } else if (warp == kWarpMmaT) {
         // ------------------------- MMA issuer (one thread) -------------------------
@@ -431,9 +455,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         constexpr int kNV = D == 64 ? 64 : 128;       // dims per P V MMA
         constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kRows, kBN, false, false);
         constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kRows, kNV, false, true);
+        // Descriptors' lower words move with the address (in 16 bytes), the upper ones stay.
         const uint64_t qd = tc::smem_desc_sw128(sQ, 16, 1024);
         const uint64_t kd = tc::smem_desc_sw128(sK, 16, 1024);
         const uint64_t vd = tc::smem_desc_sw128(sV, C::kPanel, 1024);
+        const uint32_t q_lo = (uint32_t)qd, qk_hi = (uint32_t)(qd >> 32);
+        const uint32_t k_lo = (uint32_t)kd, v_lo = (uint32_t)vd, v_hi = (uint32_t)(vd >> 32);
         int gt = 0, qn = 0;                           // key tiles and units with work before this unit
         bool ok = true;
         for (int u = 0;; ++u) {
@@ -453,12 +480,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     return false;
                 if (!wwait(k_full0 + 8 * stg, (kt / C::kStages) & 1)) return false;
                 tc::fence_after_sync();
-                if (lane == 0) {
-                    const uint64_t kst = kd + (uint64_t)(stg * (C::kTile >> 4));
+                if (tc::elect_one()) {
+                    const uint32_t kst = k_lo + stg * (C::kTile >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k)
-                        tc::mma_bf16(tmem + buf * kBN, qd + (k >> 2) * (C::kQPanel >> 4) + (k & 3) * 2,
-                                     kst + (k >> 2) * (C::kPanel >> 4) + (k & 3) * 2, idesc_qk, k > 0 ? 1u : 0u);
+                        tc::mma_bf16_lo(tmem + buf * kBN, q_lo + (k >> 2) * (C::kQPanel >> 4) + (k & 3) * 2, qk_hi,
+                                        kst + (k >> 2) * (C::kPanel >> 4) + (k & 3) * 2, qk_hi, idesc_qk, k > 0 ? 1u : 0u);
                     tc::commit(s_full0 + 8 * buf);
                     tc::commit(k_empty0 + 8 * stg);
                     if (j + 1 == n) tc::commit(q_empty);      // the last read of Q
@@ -476,17 +503,17 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 // The first P V overwrites O: the epilogue in front must have read it.
                 if (j == 0 && qn > 0 && !(ok = wwait(o_free, (qn - 1) & 1))) break;
                 tc::fence_after_sync();
-                if (lane == 0) {
-                    const uint64_t vst = vd + (uint64_t)(stg * (C::kTile >> 4));
+                if (tc::elect_one()) {
+                    const uint32_t vst = v_lo + stg * (C::kTile >> 4);
 #pragma unroll
                     for (int k = 0; k < kBN / 16; ++k)
 #pragma unroll
                         for (int h = 0; h < D / kNV; ++h)
                             // A = P from tensor memory (16 keys = 8 columns), B = V
                             // MN-major, two 64-dim panels.
-                            tc::mma_bf16_ts(tmem + C::kTmemO + h * kNV, tmem + buf * kBN + k * 8,
-                                            vst + h * 2 * (C::kPanel >> 4) + k * 128, idesc_pv,
-                                            (j > 0 || k > 0) ? 1u : 0u);
+                            tc::mma_bf16_ts_lo(tmem + C::kTmemO + h * kNV, tmem + buf * kBN + k * 8,
+                                               vst + h * 2 * (C::kPanel >> 4) + k * 128, v_hi, idesc_pv,
+                                               (j > 0 || k > 0) ? 1u : 0u);
                     tc::commit(o_done0 + 8 * buf);
                     tc::commit(v_empty0 + 8 * stg);
                 }
@@ -499,7 +526,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
         if (*abort_flag) {
             // No MMA of this thread may still run when tensor memory is freed.
-            if (lane == 0) tc::commit(drain);
+            if (tc::elect_one()) tc::commit(drain);
             __syncwarp();
             mbar_wait_bounded(drain, 0);
         }
@@ -558,7 +585,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (lane == 0) mbar_arrive(u_empty0 + 8 * slot);
             if (!live) break;
         }
-    } else {
+    } else if (warp < 4) {
         // ------------------------------ softmax, epilogue ------------------------------
         const int r = threadIdx.x;
         const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
@@ -797,72 +824,78 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 }
 
 // Joins the pieces of the item that begins in share blockIdx.x and is cut by its end, one
-// warp per row; pieces are added in their order.
+// warp per row; pieces are added in their order.  Few pieces, as a batch leaves them,
+// are loaded together with their statistics: one round trip to memory.
 template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const FwdParams p, const TreeShares w) {
     constexpr int DPL = D / 32;
     constexpr int kAhead = D == 256 ? 4 : 8;
+    const int lane = threadIdx.x & 31;
+    const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
     griddep_wait();                          // the partials are complete
     const TreeJoin join = w.joins[blockIdx.x];
-    const int lane = threadIdx.x & 31;
-    if (join.pieces == 0) return;
+    if (join.pieces == 0 || r >= join.nodes * p.g) return;
     // Piece k > 0 is the first of share blockIdx.x + k.
     auto piece = [&](int k) -> int64_t {
-        return (int64_t)(k ? 2 * ((int)blockIdx.x + k) : join.slot) * w.slot_rows;
+        return (int64_t)(k ? 2 * ((int)blockIdx.x + k) : join.slot) * w.slot_rows + r;
+    };
+    float x[kAhead][DPL];
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+            if (k0 + q >= join.pieces) break;
+            const int64_t po = piece(k0 + q) * D + lane * DPL;
+#pragma unroll
+            for (int t = 0; t < DPL; ++t) x[q][t] = part_load(p, po + t);
+        }
     };
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < join.nodes * p.g; r += gridDim.y * 8) {
-        float M = -INFINITY;
-        for (int k = lane; k < join.pieces; k += 32) M = fmaxf(M, ml[piece(k) + r].x);
+    float2 mine = ml[piece(min(lane, join.pieces - 1))];
+    load(0);
+    float M = mine.x;
+    for (int k = lane + 32; k < join.pieces; k += 32) M = fmaxf(M, ml[piece(k)].x);
 #pragma unroll
-        for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-        float o[DPL];
+    for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+    float o[DPL];
 #pragma unroll
-        for (int t = 0; t < DPL; ++t) o[t] = 0.f;
-        float L = 0.f;
-        if (M != -INFINITY) {
-            float2 mine = make_float2(0.f, 0.f);
-            for (int k0 = 0; k0 < join.pieces; k0 += kAhead) {
-                if (k0 % 32 == 0) mine = ml[piece(min(k0 + lane, join.pieces - 1)) + r];
-                float x[kAhead][DPL];
+    for (int t = 0; t < DPL; ++t) o[t] = 0.f;
+    float L = 0.f;
+    if (M != -INFINITY) {
+        for (int k0 = 0;;) {
 #pragma unroll
-                for (int q = 0; q < kAhead; ++q) {
-                    if (k0 + q >= join.pieces) break;
-                    const int64_t po = (piece(k0 + q) + r) * D + lane * DPL;
+            for (int q = 0; q < kAhead; ++q) {
+                if (k0 + q >= join.pieces) break;
+                const float mk = __shfl_sync(0xffffffffu, mine.x, (k0 + q) & 31);
+                const float lk = __shfl_sync(0xffffffffu, mine.y, (k0 + q) & 31);
+                if (mk == -INFINITY) continue;   // a piece without keys: its o means nothing
+                const float a = fast_exp2(mk - M);
+                L = fmaf(a, lk, L);
 #pragma unroll
-                    for (int t = 0; t < DPL; ++t) x[q][t] = part_load(p, po + t);
-                }
-#pragma unroll
-                for (int q = 0; q < kAhead; ++q) {
-                    if (k0 + q >= join.pieces) break;
-                    const float mk = __shfl_sync(0xffffffffu, mine.x, (k0 + q) & 31);
-                    const float lk = __shfl_sync(0xffffffffu, mine.y, (k0 + q) & 31);
-                    if (mk == -INFINITY) continue;   // a piece without keys: its o means nothing
-                    const float a = fast_exp2(mk - M);
-                    L = fmaf(a, lk, L);
-#pragma unroll
-                    for (int t = 0; t < DPL; ++t) o[t] = fmaf(a, x[q][t], o[t]);
-                }
+                for (int t = 0; t < DPL; ++t) o[t] = fmaf(a, x[q][t], o[t]);
             }
+            k0 += kAhead;
+            if (k0 >= join.pieces) break;
+            if (k0 % 32 == 0) mine = ml[piece(min(k0 + lane, join.pieces - 1))];
+            load(k0);
         }
-        const int h = join.hkv * p.g + r % p.g;
-        float f = 1.f;
-        if (p.flags & UA_FLAG_SINKS) {
-            const float s2 = __ldg(p.sinks + h) * kLog2e;
-            if (s2 == INFINITY) {
-                L = 0.f;
-            } else if (s2 > M) {
-                f = M == -INFINITY ? 0.f : fast_exp2(M - s2);
-                L = L * f + 1.0f;
-            } else if (s2 != -INFINITY) {
-                L += fast_exp2(s2 - M);
-            }
-        }
-        f = L > 0.f ? f * __frcp_rn(L) : 0.f;
-        __nv_bfloat16* dst = p.out + ((join.row0 + r / p.g) * p.hq + h) * D + lane * DPL;
-#pragma unroll
-        for (int t = 0; t < DPL; ++t) dst[t] = __float2bfloat16_rn(o[t] * f);
     }
+    const int h = join.hkv * p.g + r % p.g;
+    float f = 1.f;
+    if (p.flags & UA_FLAG_SINKS) {
+        const float s2 = __ldg(p.sinks + h) * kLog2e;
+        if (s2 == INFINITY) {
+            L = 0.f;
+        } else if (s2 > M) {
+            f = M == -INFINITY ? 0.f : fast_exp2(M - s2);
+            L = L * f + 1.0f;
+        } else if (s2 != -INFINITY) {
+            L += fast_exp2(s2 - M);
+        }
+    }
+    f = L > 0.f ? f * __frcp_rn(L) : 0.f;
+    __nv_bfloat16* dst = p.out + ((join.row0 + r / p.g) * p.hq + h) * D + lane * DPL;
+#pragma unroll
+    for (int t = 0; t < DPL; ++t) dst[t] = __float2bfloat16_rn(o[t] * f);
 }
 
 template <int D>
@@ -876,10 +909,10 @@ cudaError_t launch_tree_d(const TreePlan& plan, const CUtensorMap& tq, const CUt
     kern<<<(unsigned)plan.ctas, kThreadsT, TCfg<D>::kSmem, stream>>>(tq, tm_k, tm_v, p, plan.shares);
     e = cudaGetLastError();
     if (e != cudaSuccess || plan.ctas == 1) return e;
-    return launch_early(tree_merge_kernel<D>, dim3((unsigned)plan.ctas, 4), 256, 0, stream, p, plan.shares);
+    return launch_early(tree_merge_kernel<D>, dim3((unsigned)plan.ctas, (unsigned)((plan.shares.slot_rows + 7) / 8)),
+                        256, 0, stream, p, plan.shares);
 }
 
-int tile_keys(int d) { return d == 256 ? 64 : 128; }
 int ctas_per_sm(int d) { return d == 256 ? 1 : 2; }
 
 // Bytes of the partials of `ctas` shares whose tiles have `rows` rows, and of the joins.
@@ -900,7 +933,7 @@ bool plan_tree(FwdParams* fp, int num_sms, void* workspace, size_t workspace_byt
     const FwdParams& p = *fp;
     *plan = TreePlan();
     if (p.g > kRows || p.max_seqlen_k > 1 << 30) return false;
-    const int ppt = kRows / p.g, bn = tile_keys(p.d);
+    const int ppt = kRows / p.g, bn = TCfg<64>::kBN;
     const int64_t tiles = (p.max_seqlen_q + ppt - 1) / ppt;
     const int64_t rows = (int64_t)std::min(ppt, p.max_seqlen_q) * p.g;
     if (tiles * p.num_seqs > 0x7fffffffLL) return false;
