@@ -56,6 +56,9 @@ namespace ua {
 namespace {
 
 using namespace pf;
+#ifndef TREE_TURN
+#define TREE_TURN 5
+#endif
 
 constexpr int kThreadsT = 256;
 constexpr int kWarpCopy = 4;
@@ -108,6 +111,13 @@ struct TCfg {
     static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory budget");
 };
 
+// 32 bytes at once: a whole sector of a row, where every thread writes a row of its own.
+__device__ __forceinline__ void store32b(void* dst, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
 // The position of the chunk's key c, within the range that a tree can have.
 __device__ __forceinline__ int node_position(const FwdParams& p, int64_t q0, int c, int ctx, int sk) {
     return min(max(__ldg(p.positions + q0 + c), ctx), sk - 1);
@@ -153,8 +163,8 @@ __device__ __noinline__ void add_unbounded(const FwdParams& p, int s, int hkv, i
     }
 }
 
-// Steps (key tiles) of the items of sequence s in row tile r: 0 where it has no such
-// tile, 1 for malformed lengths (rows of zeros).
+// Key tiles of the items of sequence s in row tile r: 0 where it has no such tile, 1 for
+// malformed lengths (rows of zeros).
 template <int BN>
 __device__ __forceinline__ int item_steps(const FwdParams& p, int s, int r, uint32_t& st) {
     int sq, sk;
@@ -271,7 +281,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     for (int64_t e = e_lo; e < e_hi; ++e) {
         const int r = (int)(e / p.num_seqs), s = (int)(e - (int64_t)r * p.num_seqs);
         uint32_t st;
-        mine += item_steps<kBN>(p, s, r, st);
+        const int steps = item_steps<kBN>(p, s, r, st);
+        mine += steps ? steps + w.turn : 0;
         if (st && r == 0 && blockIdx.x == 0) atomicOr(p.err, (int)st);
     }
     mine *= p.hk;
@@ -301,12 +312,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         for (int64_t e = e_lo; e < e_hi; ++e) {
             const int r = (int)(e / p.num_seqs), s = (int)(e - (int64_t)r * p.num_seqs);
             uint32_t st;
-            const int steps = item_steps<kBN>(p, s, r, st);
-            const int64_t all = (int64_t)steps * p.hk;
+            const int steps = item_steps<kBN>(p, s, r, st), item = steps ? steps + w.turn : 0;
+            const int64_t all = (int64_t)item * p.hk;
             if (x0 < at + all) {
                 start[0] = (int32_t)e;
-                start[1] = (int32_t)((x0 - at) / steps);
-                start[2] = (int32_t)((x0 - at) % steps);
+                start[1] = (int32_t)((x0 - at) / item);
+                start[2] = (int32_t)((x0 - at) % item);
                 break;
             }
             at += all;
@@ -332,7 +343,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         int u = 0, qn = 0, kt = 0;     // units, Q loads, K tiles
         TreeJoin join{0, 0, 0, 0, 0};
         bool ok = true;
-        for (;; ++u) {
+        for (;;) {
             const int slot = u & 1;
             if (u >= 2 && !(ok = wwait(u_empty0 + 8 * slot, ((u >> 1) + 1) & 1))) break;
             if (x >= x1) {
@@ -369,10 +380,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             int64_t q0;
             const uint32_t st = seq_status(p, s, sq, sk, q0);
             const int ctx = sk - sq, first = r * ppt;
-            const int n = (int)min((int64_t)(steps - step), x1 - x);
+            // The item's last w.turn steps stand for what an item costs besides its tiles.
+            const int n_all = (int)min((int64_t)(steps + w.turn - step), x1 - x), n = min(n_all, steps - step);
             const int t_begin = (st || !window ? 0 : max(0, ctx - p.window + 1) / kBN) + step;
             const bool whole = n == steps;
-            if (lane == 0) {
+            if (n > 0 && lane == 0) {
                 TreeUnit& un = units[slot];
                 un.live = 1;
                 un.zero = st != 0;
@@ -389,8 +401,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 un.odd = 0;
                 mbar_arrive(u_full0 + 8 * slot);
             }
-            if (!whole && step == 0) {
-                // The item begins here: its shares up to the one that holds its last step.
+            if (n > 0 && !whole && step == 0) {
+                // The item begins here: its shares up to the one that holds its last tile.
                 const int64_t end = x + steps;
                 join.pieces = (int)((end * shares - 1) / total - blockIdx.x) + 1;
                 join.slot = 2 * (int)blockIdx.x + (x > x0 ? 1 : 0);
@@ -398,16 +410,18 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 join.nodes = min(first + ppt, sq) - first;
                 join.hkv = hkv;
             }
-            x += n;
-            step += n;
+            x += n_all;
+            step += n_all;
             const int h_now = hkv;
-            if (step == steps) {
+            if (step == steps + w.turn) {
                 step = 0;
                 if (++hkv == p.hk) {
                     hkv = 0;
                     ++e;
                 }
             }
+            if (n <= 0) continue;
+            ++u;
             if (st) continue;
             if (qn >= 1 && !(ok = wwait(q_empty, (qn - 1) & 1))) break;
             if (lane == 0) {
@@ -593,6 +607,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         // The score chain is in log2 units from the products on (a factor of zero
         // would make NaN of masked scores).
         const float cap = p.softcap * kLog2e, fac = fmaxf(p.scale * (softcap ? 1.f / p.softcap : kLog2e), 0x1p-126f);
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
         int gt = 0;
         bool ok = true;
         for (int u = 0;; ++u) {
@@ -796,15 +811,24 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                     if (part >= 0) {
-                        part_store32(p, prow * D + c * 32, o);
-                    } else {
-                        uint4* dst = reinterpret_cast<uint4*>(p.out + row * (int64_t)D + c * 32);
+                        if (p.part_bf16) part_store32(p, prow * D + c * 32, o);
+                        else
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            dst[e / 8] = make_uint4(pack_bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])),
-                                                    pack_bf16x2(__uint_as_float(o[e + 2]), __uint_as_float(o[e + 3])),
-                                                    pack_bf16x2(__uint_as_float(o[e + 4]), __uint_as_float(o[e + 5])),
-                                                    pack_bf16x2(__uint_as_float(o[e + 6]), __uint_as_float(o[e + 7])));
+                            for (int e = 0; e < 32; e += 8) store32b(p.part_o + prow * D + c * 32 + e, o + e);
+                    } else {
+                        uint32_t h[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            h[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                        __nv_bfloat16* dst = p.out + row * (int64_t)D + c * 32;
+                        if (wide) {
+                            store32b(dst, h);
+                            store32b(dst + 16, h + 8);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<uint4*>(dst + 2 * e) = make_uint4(h[e], h[e + 1], h[e + 2], h[e + 3]);
+                        }
                     }
                 }
             }
@@ -944,6 +968,7 @@ bool plan_tree(FwdParams* fp, int num_sms, void* workspace, size_t workspace_byt
     plan->ctas = (int)ctas;
     plan->shares.tiles = (int)tiles;
     plan->shares.least = 1;
+    plan->shares.turn = TREE_TURN;
     plan->shares.slot_rows = (int)rows;
     // Partials in front, then (m, l), then the joins.
     fp->part_o = static_cast<float*>(workspace);

@@ -18,6 +18,7 @@ struct TreeShares {
     int32_t tiles;         // row tiles of the longest chunk
     int32_t slot_rows;     // rows of a partial; share i has slots 2 i and 2 i + 1
     int32_t least;         // steps of a share at least
+    int32_t turn;          // steps that an item costs besides its key tiles
 };
 
 struct TreePlan {
