@@ -410,11 +410,22 @@ def _check(t, name, kind, device):
         raise ValueError("%s must be %s, on the device of the other tensors" % (name, kind))
 
 
-def _vector(t, name, n, kind, device):
-    """Refuse all but a contiguous tensor of at least n elements of that type there."""
+def _refuse_vector(t, name, n, kind, device):
     if t.numel() < n or not t.is_contiguous():
         raise ValueError("%s must be contiguous, with at least %d elements" % (name, n))
-    _check(t, name, kind, device)
+    raise ValueError("%s must be %s, on the device of the other tensors" % (name, kind))
+
+
+_int_types = None
+
+
+def _ints():
+    """torch.int32 and torch.int64 (torch is not imported with this module)."""
+    global _int_types
+    if _int_types is None:
+        import torch
+        _int_types = torch.int32, torch.int64
+    return _int_types
 
 
 def _tree_rows(parents, num_seqs, device):
@@ -423,17 +434,18 @@ def _tree_rows(parents, num_seqs, device):
     if len(shape) != 2 or shape[0] < num_seqs or shape[1] < 1 or (shape[1] > 1 and stride[1] != 1) or (
             shape[0] > 1 and stride[0] < shape[1]):
         raise ValueError("parents must be [num_seqs, nodes] with unit inner stride")
-    _check(parents, "parents", "torch.int32", device)
+    if parents.dtype is not _ints()[0] or parents.get_device() != device:
+        raise ValueError("parents must be int32, on the device of the other tensors")
     return stride[0] if shape[0] > 1 else shape[1]
 
 
 def _mask_stride(mask, tokens, device):
     """Words between the rows of a tree mask [tokens, words]."""
-    shape, stride = mask.shape, mask.stride()
-    if len(shape) != 2 or shape[0] < tokens or shape[1] < 1 or (shape[1] > 1 and stride[1] != 1) or (
-            shape[0] > 1 and stride[0] != shape[1]):
+    shape = mask.shape
+    if len(shape) != 2 or shape[0] < tokens or shape[1] < 1 or not mask.is_contiguous():
         raise ValueError("tree_mask must be a contiguous [tokens, words]")
-    _check(mask, "tree_mask", "torch.uint32" if str(mask.dtype) == "torch.uint32" else "torch.int32", device)
+    if (mask.dtype is not _ints()[0] and str(mask.dtype) != "torch.uint32") or mask.get_device() != device:
+        raise ValueError("tree_mask must be int32 or uint32, on the device of the other tensors")
     return shape[1]
 
 
@@ -666,25 +678,32 @@ class Problem:
         ``blocks_held``, ``free_blocks`` (a stack of ``free_count`` ids); out:
         ``granted``, ``cu_seqlens_q``, ``seqused_k``, and per packed token ``positions``,
         ``slots`` (int64) and ``tree_mask`` (int32 or uint32 [max_tokens, words])."""
-        device = block_table.get_device()
-        shape, step = block_table.shape, block_table.stride()
-        if (len(shape) != 2 or shape[0] < num_seqs or shape[1] > self.max_blocks_per_seq or
-                (shape[1] < self.max_blocks_per_seq and num_seqs > 0) or (shape[1] > 1 and step[1] != 1) or
-                (num_seqs > 1 and step[0] != self.max_blocks_per_seq)):
-            raise ValueError("block_table must be [num_seqs, max_blocks_per_seq]")
-        _check(block_table, "block_table", "torch.int32", device)
-        for t, name, n in ((blocks_held, "blocks_held", num_seqs), (free_blocks, "free_blocks", self.num_blocks),
-                           (free_count, "free_count", 1), (ctx_lens, "ctx_lens", num_seqs),
-                           (new_lens, "new_lens", num_seqs), (granted, "granted", num_seqs),
-                           (cu_seqlens_q, "cu_seqlens_q", num_seqs + 1), (seqused_k, "seqused_k", num_seqs),
-                           (positions, "positions", max_tokens)):
-            _vector(t, name, n, "torch.int32", device)
-        _vector(slots, "slots", max_tokens, "torch.int64", device)
-        stride = _tree_rows(parents, num_seqs, device) if parents is not None else 0
-        words = _mask_stride(tree_mask, max_tokens, device) if tree_mask is not None else 0
-        st = ua_plan_step(self.handle, block_table, blocks_held, free_blocks, free_count, ctx_lens, new_lens, parents,
-                          stride, num_seqs, max_tokens, granted, cu_seqlens_q, seqused_k, positions, slots, tree_mask,
-                          words, stream)
+        # A step waits for the host: checks without a call more than they take.
+        i32, i64 = _ints()
+        device, width = block_table.get_device(), self.max_blocks_per_seq
+        if (block_table.dtype is not i32 or not block_table.is_contiguous() or block_table.dim() != 2 or
+                block_table.shape[1] != width or block_table.shape[0] < num_seqs):
+            raise ValueError("block_table must be a contiguous int32 [num_seqs, max_blocks_per_seq]")
+        for t, n, name in ((blocks_held, num_seqs, "blocks_held"), (free_blocks, self.num_blocks, "free_blocks"),
+                           (free_count, 1, "free_count"), (ctx_lens, num_seqs, "ctx_lens"),
+                           (new_lens, num_seqs, "new_lens"), (granted, num_seqs, "granted"),
+                           (cu_seqlens_q, num_seqs + 1, "cu_seqlens_q"), (seqused_k, num_seqs, "seqused_k"),
+                           (positions, max_tokens, "positions")):
+            if t.dtype is not i32 or t.numel() < n or not t.is_contiguous() or t.get_device() != device:
+                _refuse_vector(t, name, n, "int32", device)
+        if slots.dtype is not i64 or slots.numel() < max_tokens or not slots.is_contiguous() or slots.get_device() != device:
+            _refuse_vector(slots, "slots", max_tokens, "int64", device)
+        tree = mask = None
+        stride = words = 0
+        if parents is not None:
+            tree, stride = parents.data_ptr(), _tree_rows(parents, num_seqs, device)
+        if tree_mask is not None:
+            mask, words = tree_mask.data_ptr(), _mask_stride(tree_mask, max_tokens, device)
+        st = load_library().ua_plan_step(
+            self.handle, block_table.data_ptr(), blocks_held.data_ptr(), free_blocks.data_ptr(), free_count.data_ptr(),
+            ctx_lens.data_ptr(), new_lens.data_ptr(), tree, stride, num_seqs, max_tokens, granted.data_ptr(),
+            cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), positions.data_ptr(), slots.data_ptr(), mask, words,
+            _stream(stream))
         if st != UA_OK:
             raise UAError(st, "ua_plan_step")
 
@@ -700,6 +719,7 @@ class Problem:
         """Rotate q and k (bf16 [total_q, heads, d]; tokens may be strided) by
         ``positions`` and write k and v to ``slots`` (int64; negative: not stored).
         Returns the rotated q (``q_out``, which may be q)."""
+        i32, i64 = _ints()
         device = k_cache.get_device()
         q_stride = _token_stride(q, "q", total_q, self.num_q_heads, self.head_size)
         stride = _token_stride(k_new, "k_new", total_q, self.num_kv_heads, self.head_size)
@@ -709,10 +729,15 @@ class Problem:
             import torch
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         out_stride = _token_stride(q_out, "q_out", total_q, self.num_q_heads, self.head_size)
-        for t, name in ((q, "q"), (k_new, "k_new"), (v_new, "v_new"), (q_out, "q_out")):
-            _check(t, name, "torch.bfloat16", device)
-        _vector(positions, "positions", total_q, "torch.int32", device)
-        _vector(slots, "slots", total_q, "torch.int64", device)
+        _check(q, "q", "torch.bfloat16", device)
+        _check(k_new, "k_new", "torch.bfloat16", device)
+        _check(v_new, "v_new", "torch.bfloat16", device)
+        _check(q_out, "q_out", "torch.bfloat16", device)
+        if positions.dtype is not i32 or positions.numel() < total_q or not positions.is_contiguous() or (
+                positions.get_device() != device):
+            _refuse_vector(positions, "positions", total_q, "int32", device)
+        if slots.dtype is not i64 or slots.numel() < total_q or not slots.is_contiguous() or slots.get_device() != device:
+            _refuse_vector(slots, "slots", total_q, "int64", device)
         st = load_library().ua_rope_store(
             self.handle, q.data_ptr(), q_stride, k_new.data_ptr(), v_new.data_ptr(), stride, positions.data_ptr(),
             slots.data_ptr(), total_q, q_out.data_ptr(), out_stride, k_cache.data_ptr(), v_cache.data_ptr(),
@@ -729,14 +754,19 @@ class Problem:
         has.  ``positions`` (int32 [total_q]) are needed with a window or ALiBi."""
         device = q.get_device()
         words = _mask_stride(tree_mask, total_q, device)
+        places = None
         if positions is not None:
-            _vector(positions, "positions", total_q, "torch.int32", device)
+            if positions.dtype is not _ints()[0] or positions.numel() < total_q or not positions.is_contiguous() or (
+                    positions.get_device() != device):
+                _refuse_vector(positions, "positions", total_q, "int32", device)
+            places = positions.data_ptr()
         if out is None:
             import torch
             out = torch.empty_like(q)
-        st = ua_forward_tree(self.handle, q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, num_seqs, total_q,
-                             max_seqlen_q, max_seqlen_k, tree_mask, words, positions, flags, sinks, alibi_slopes, out,
-                             stream)
+        st = load_library().ua_forward_tree(
+            self.handle, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+            cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), num_seqs, total_q, max_seqlen_q, max_seqlen_k,
+            tree_mask.data_ptr(), words, places, flags, _ptr(sinks), _ptr(alibi_slopes), out.data_ptr(), _stream(stream))
         if st != UA_OK:
             raise UAError(st, "ua_forward_tree")
         return out
@@ -750,16 +780,18 @@ class Problem:
         stride = _tree_rows(parents, num_seqs, device)
         if parents.shape[1] < max_seqlen_q:
             raise ValueError("parents must have a column per node")
-        if path.dim() != 2 or path.shape[0] != num_seqs or path.shape[1] < 1 or not path.is_contiguous():
-            raise ValueError("path must be a contiguous [num_seqs, n]")
-        _check(path, "path", "torch.int32", device)
-        for t, name, n in ((cu_seqlens_q, "cu_seqlens_q", num_seqs + 1), (seqused_k, "seqused_k", num_seqs),
-                           (last, "last", num_seqs), (accepted, "accepted", num_seqs),
-                           (seqused_out, "seqused_out", num_seqs)):
-            _vector(t, name, n, "torch.int32", device)
-        st = ua_cache_accept(self.handle, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, parents, stride, last,
-                             num_seqs, total_q, max_seqlen_q, max_seqlen_k, path, path.shape[1], accepted, seqused_out,
-                             stream)
+        if path.dim() != 2 or path.shape[0] != num_seqs or path.shape[1] < 1:
+            raise ValueError("path must be [num_seqs, n]")
+        i32 = _ints()[0]
+        for t, n, name in ((path, 1, "path"), (cu_seqlens_q, num_seqs + 1, "cu_seqlens_q"),
+                           (seqused_k, num_seqs, "seqused_k"), (last, num_seqs, "last"),
+                           (accepted, num_seqs, "accepted"), (seqused_out, num_seqs, "seqused_out")):
+            if t.dtype is not i32 or t.numel() < n or not t.is_contiguous() or t.get_device() != device:
+                _refuse_vector(t, name, n, "int32", device)
+        st = load_library().ua_cache_accept(
+            self.handle, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_seqlens_q.data_ptr(),
+            seqused_k.data_ptr(), parents.data_ptr(), stride, last.data_ptr(), num_seqs, total_q, max_seqlen_q,
+            max_seqlen_k, path.data_ptr(), path.shape[1], accepted.data_ptr(), seqused_out.data_ptr(), _stream(stream))
         if st != UA_OK:
             raise UAError(st, "ua_cache_accept")
 

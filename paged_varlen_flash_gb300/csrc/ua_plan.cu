@@ -24,8 +24,8 @@
 namespace ua {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+constexpr int kThreads = 1024;     // at most
+constexpr int kFew = 256;          // threads of a CTA where they hold all sequences
 
 struct Sums {          // of the sequences in front of a thread's, or of all
     int64_t a, b, c;
@@ -45,11 +45,11 @@ __device__ __forceinline__ Sums prefix(Sums v, Sums* warp_sums, Sums* total) {
             x.c += c;
         }
     }
-    __syncthreads();                       // warp_sums may still be read from the call before
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
     Sums before{0, 0, 0}, all{0, 0, 0};
-    for (int w = 0; w < kWarps; ++w) {
+    const int warps = blockDim.x >> 5;
+    for (int w = 0; w < warps; ++w) {
         const Sums y = warp_sums[w];
         if (w < warp) {
             before.a += y.a;
@@ -95,29 +95,46 @@ __device__ __forceinline__ int owner_of(const int32_t* first, int n, int32_t x) 
     return lo;
 }
 
+// The slot of sequence s's key `place`; -1 and an error bit for a bad block id.
+template <typename Taken>
+__device__ __forceinline__ int64_t slot_of(const PlanParams& p, const int32_t* take, const Taken& taken, int s, int place,
+                                           uint32_t& err) {
+    const int blk = place >> p.b_log2, held = p.held[s];
+    const int32_t id = blk < held ? p.block_table[(int64_t)s * p.bt_stride + blk] : taken(take[s] + blk - held);
+    if (id < 0 || (int64_t)id >= p.num_blocks) {
+        err |= UA_DEVERR_BLOCK_ID;
+        return -1;
+    }
+    return ((int64_t)id << p.b_log2) + (place & ((1 << p.b_log2) - 1));
+}
+
 __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     extern __shared__ int32_t smem[];
-    __shared__ Sums warp_sums[kWarps];
+    __shared__ Sums warp_sums[2][kThreads / 32];
     __shared__ int last;
-    const int n = p.num_seqs, tid = threadIdx.x;
+    const int n = p.num_seqs, tid = threadIdx.x, threads = blockDim.x;
     int32_t* tok = smem;             // tokens in front of a sequence
     int32_t* take = tok + n + 1;     // blocks taken in front of it
     int32_t* give = take + n + 1;    // blocks returned in front of it
-    const int per = (n + kThreads - 1) / kThreads;
+    const int per = (n + threads - 1) / threads;
     const int s0 = min(n, tid * per), s1 = min(n, s0 + per);
+    int64_t count = *p.pool_count;
 
-    // 1. What is asked for, and which sequences get it.
+    // 1. What is asked for, and which sequences get it.  (A thread's first sequence stays in
+    // registers; only batches of more sequences than threads have others.)
+    Ask own{0, 0, 0, 0, 0, false};
+    if (s0 < s1) own = ask_of(p, s0);
+    auto ask = [&](int s) { return s == s0 ? own : ask_of(p, s); };
     Sums mine{0, 0, 0}, all;
     uint32_t err = 0;
     for (int s = s0; s < s1; ++s) {
-        const Ask a = ask_of(p, s);
+        const Ask a = ask(s);
         if (a.bad) err |= UA_DEVERR_BOUNDS;
         mine.a += a.more;
         mine.b += a.back;
         mine.c += a.fresh;
     }
-    const Sums before = prefix(mine, warp_sums, &all);
-    int64_t count = *p.pool_count;
+    const Sums before = prefix(mine, warp_sums[0], &all);
     // A pool of another size than the cache's, or more blocks given back than there are:
     // nothing is taken or nothing is given back.
     const bool sane = count >= 0 && count <= p.num_blocks;
@@ -127,36 +144,31 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     const int64_t R = returns ? all.b : 0;
     // 2. Prefix sums of what is given out.
     Sums got{0, 0, 0}, sum;
-    {
+    auto each = [&](auto&& f) {
         int64_t more = before.a, fresh = before.c;
         for (int s = s0; s < s1; ++s) {
-            const Ask a = ask_of(p, s);
+            const Ask a = ask(s);
             more += a.more;
             fresh += a.fresh;
-            const bool fits = fresh <= p.max_tokens;
+            const bool fits = fresh <= p.max_tokens, ok = fits && (a.more == 0 || more <= count + R);
             if (!fits && a.fresh) err |= UA_DEVERR_BOUNDS;
-            const bool ok = fits && (a.more == 0 || more <= count + R);
-            got.a += ok ? a.more : 0;
-            got.b += returns ? a.back : 0;
-            got.c += ok ? a.fresh : 0;
+            f(s, ok ? a.more : 0, returns ? a.back : 0, ok ? a.fresh : 0);
         }
-    }
-    Sums at = prefix(got, warp_sums, &sum);
-    {
-        int64_t more = before.a, fresh = before.c;
-        for (int s = s0; s < s1; ++s) {
-            const Ask a = ask_of(p, s);
-            more += a.more;
-            fresh += a.fresh;
-            const bool ok = fresh <= p.max_tokens && (a.more == 0 || more <= count + R);
-            take[s] = (int32_t)at.a;
-            give[s] = (int32_t)at.b;
-            tok[s] = (int32_t)at.c;
-            at.a += ok ? a.more : 0;
-            at.b += returns ? a.back : 0;
-            at.c += ok ? a.fresh : 0;
-        }
-    }
+    };
+    each([&](int, int more, int back, int fresh) {
+        got.a += more;
+        got.b += back;
+        got.c += fresh;
+    });
+    Sums at = prefix(got, warp_sums[1], &sum);
+    each([&](int s, int more, int back, int fresh) {
+        take[s] = (int32_t)at.a;
+        give[s] = (int32_t)at.b;
+        tok[s] = (int32_t)at.c;
+        at.a += more;
+        at.b += back;
+        at.c += fresh;
+    });
     if (tid == 0) {
         take[n] = (int32_t)sum.a;
         give[n] = (int32_t)sum.b;
@@ -164,8 +176,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     }
     __syncthreads();
     const int T = (int)sum.a, total = (int)sum.c;
-    const int b = 1 << p.b_log2;
-    const int64_t first = (int64_t)blockIdx.x * kThreads + tid, step = (int64_t)gridDim.x * kThreads;
+    const int64_t first = (int64_t)blockIdx.x * threads + tid, step = (int64_t)gridDim.x * threads;
 
     auto returned = [&](int r) -> int32_t {
         const int s = owner_of(give, n, r);
@@ -183,8 +194,48 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     }
     for (int64_t r = T + first; r < R; r += step) p.pool[count + R - 1 - r] = returned((int)r);
 
-    // 4. Tokens.
-    for (int64_t t = first; t < p.max_tokens; t += step) {
+    // 4. Tokens.  Chains without a mask four at a time, which nearly always are neighbours
+    // in one block.
+    const bool fours = !p.parents && !p.mask && p.aligned;
+    if (fours) {
+        for (int64_t t = 4 * first; t < p.max_tokens; t += 4 * step) {
+            int pos[4];
+            int64_t slot[4];
+            const int s = t < total ? owner_of(tok, n, (int)t) : 0;
+            const int place = t < total ? p.ctx_lens[s] + ((int)t - tok[s]) : 0;
+            if (t < total && t + 3 < tok[s + 1] && (place & ((1 << p.b_log2) - 1)) <= (1 << p.b_log2) - 4) {
+                const int64_t at_slot = slot_of(p, take, taken, s, place, err);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    pos[k] = place + k;
+                    slot[k] = at_slot < 0 ? -1 : at_slot + k;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    pos[k] = 0;
+                    slot[k] = -1;
+                    if (t + k >= total) continue;
+                    const int sk = owner_of(tok, n, (int)t + k);
+                    pos[k] = p.ctx_lens[sk] + ((int)t + k - tok[sk]);
+                    slot[k] = slot_of(p, take, taken, sk, pos[k], err);
+                }
+            }
+            if (t + 3 < p.max_tokens) {
+                *reinterpret_cast<int4*>(p.positions + t) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+                *reinterpret_cast<longlong2*>(p.slots + t) = make_longlong2(slot[0], slot[1]);
+                *reinterpret_cast<longlong2*>(p.slots + t + 2) = make_longlong2(slot[2], slot[3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    if (t + k < p.max_tokens) {
+                        p.positions[t + k] = pos[k];
+                        p.slots[t + k] = slot[k];
+                    }
+            }
+        }
+    }
+    for (int64_t t = first; !fours && t < p.max_tokens; t += step) {
         if (t >= total) {
             p.positions[t] = 0;
             p.slots[t] = -1;
@@ -192,12 +243,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
         }
         const int s = owner_of(tok, n, (int)t);
         const int i = (int)t - tok[s], ctx = p.ctx_lens[s];
-        const int place = ctx + i, blk = place >> p.b_log2, held = p.held[s];
-        const int32_t id =
-            blk < held ? p.block_table[(int64_t)s * p.bt_stride + blk] : taken(take[s] + blk - held);
-        const bool good = id >= 0 && (int64_t)id < p.num_blocks;
-        if (!good) err |= UA_DEVERR_BLOCK_ID;
-        p.slots[t] = good ? (int64_t)id * b + (place & (b - 1)) : -1;
+        p.slots[t] = slot_of(p, take, taken, s, ctx + i, err);
         int depth = i;
         if (p.parents) {
             // Up to the root; the bits of a word of the mask are complete when the
@@ -252,8 +298,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     } else {
         __syncthreads();
     }
-    for (int s = tid; s < n; s += kThreads) {
-        const Ask a = ask_of(p, s);
+    for (int s = tid; s < n; s += threads) {
+        const Ask a = s == s0 && per == 1 ? own : ask_of(p, s);
         const int fresh = tok[s + 1] - tok[s];
         p.granted[s] = fresh;
         p.cu[s] = tok[s];
@@ -270,10 +316,18 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
 
 cudaError_t launch_plan(const PlanParams& p, int num_sms, cudaStream_t stream) {
     const size_t smem = (size_t)3 * (p.num_seqs + 1) * sizeof(int32_t);
-    cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(num_sms, (p.max_tokens + kThreads - 1) / kThreads));
-    plan_kernel<<<(unsigned)ctas, kThreads, smem, stream>>>(p);
+    if (smem > 48 * 1024 - 2048) {
+        const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    // Few sequences: smaller CTAs, whose sums are quicker, and more of them.
+    const int threads = p.num_seqs <= kFew ? kFew : kThreads;
+    const int64_t each = (p.parents || p.mask ? 1 : 4) * (int64_t)threads;
+    const int64_t most = (int64_t)num_sms * (threads == kFew ? 4 : 1);
+    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(most, (p.max_tokens + each - 1) / each));
+    PlanParams q = p;
+    q.aligned = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15u) == 0;
+    plan_kernel<<<(unsigned)ctas, threads, smem, stream>>>(q);
     return cudaGetLastError();
 }
 

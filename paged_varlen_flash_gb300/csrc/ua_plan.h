@@ -30,6 +30,7 @@ struct PlanParams {
     int64_t max_tokens;
     int32_t mask_stride;
     int32_t num_seqs, bt_stride, b_log2;
+    int32_t aligned;               // positions and slots on 16-byte boundaries
 };
 
 cudaError_t launch_plan(const PlanParams& p, int num_sms, cudaStream_t stream);
