@@ -272,7 +272,6 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         tc::tmem_alloc(smem_u32(tmem_slot), C::kCols2);
         tc::tmem_relinquish();
     }
-    griddep_launch();      // the merge kernel's CTAs may wait on SMs that are done
     // This CTA's share: entries (row tile, sequence) in order, each thread a run of them.
     const int64_t entries = (int64_t)w.tiles * p.num_seqs;
     const int64_t per = (entries + kThreadsT - 1) / kThreadsT;
@@ -847,79 +846,78 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
 }
 
-// Joins the pieces of the item that begins in share blockIdx.x and is cut by its end, one
-// warp per row; pieces are added in their order.  Few pieces, as a batch leaves them,
-// are loaded together with their statistics: one round trip to memory.
+// Four values of a partial row.
+__device__ __forceinline__ float4 load_part4(const FwdParams& p, int64_t idx) {
+    if (p.part_bf16) {
+        const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(p.part_o) + idx);
+        return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
+    }
+    return *reinterpret_cast<const float4*>(p.part_o + idx);
+}
+
+// Joins the pieces of the item that begins in share blockIdx.x and is cut by its end, in
+// their order.  A thread has four dims of a row, and four pieces' loads in flight: one
+// round trip to memory for what a batch leaves.
 template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const FwdParams p, const TreeShares w) {
-    constexpr int DPL = D / 32;
-    constexpr int kAhead = D == 256 ? 4 : 8;
-    const int lane = threadIdx.x & 31;
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+    constexpr int kChunks = D / 4, kAhead = 4;
+    const int col = (threadIdx.x % kChunks) * 4, r = blockIdx.y * (256 / kChunks) + threadIdx.x / kChunks;
     griddep_wait();                          // the partials are complete
     const TreeJoin join = w.joins[blockIdx.x];
     if (join.pieces == 0 || r >= join.nodes * p.g) return;
-    // Piece k > 0 is the first of share blockIdx.x + k.
-    auto piece = [&](int k) -> int64_t {
-        return (int64_t)(k ? 2 * ((int)blockIdx.x + k) : join.slot) * w.slot_rows + r;
-    };
-    float x[kAhead][DPL];
-    auto load = [&](int k0) {
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+    float4 x[kAhead], o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float2 st[kAhead];
+    float top = -INFINITY, l = 0.f;
+    auto load = [&](int m0) {
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
-            if (k0 + q >= join.pieces) break;
-            const int64_t po = piece(k0 + q) * D + lane * DPL;
-#pragma unroll
-            for (int t = 0; t < DPL; ++t) x[q][t] = part_load(p, po + t);
+            // Piece m > 0 is the first of share blockIdx.x + m.
+            const int m = m0 + q;
+            if (m >= join.pieces) break;
+            const int64_t prow = (int64_t)(m ? 2 * ((int)blockIdx.x + m) : join.slot) * w.slot_rows + r;
+            st[q] = ml[prow];
+            x[q] = load_part4(p, prow * D + col);
         }
     };
-    const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    float2 mine = ml[piece(min(lane, join.pieces - 1))];
     load(0);
-    float M = mine.x;
-    for (int k = lane + 32; k < join.pieces; k += 32) M = fmaxf(M, ml[piece(k)].x);
+    for (int m0 = 0; m0 < join.pieces; m0 += kAhead) {
+        float4 y[kAhead];
+        float2 ty[kAhead];
 #pragma unroll
-    for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-    float o[DPL];
+        for (int q = 0; q < kAhead; ++q) {
+            y[q] = x[q];
+            ty[q] = st[q];
+        }
+        if (m0 + kAhead < join.pieces) load(m0 + kAhead);
 #pragma unroll
-    for (int t = 0; t < DPL; ++t) o[t] = 0.f;
-    float L = 0.f;
-    if (M != -INFINITY) {
-        for (int k0 = 0;;) {
-#pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-                if (k0 + q >= join.pieces) break;
-                const float mk = __shfl_sync(0xffffffffu, mine.x, (k0 + q) & 31);
-                const float lk = __shfl_sync(0xffffffffu, mine.y, (k0 + q) & 31);
-                if (mk == -INFINITY) continue;   // a piece without keys: its o means nothing
-                const float a = fast_exp2(mk - M);
-                L = fmaf(a, lk, L);
-#pragma unroll
-                for (int t = 0; t < DPL; ++t) o[t] = fmaf(a, x[q][t], o[t]);
-            }
-            k0 += kAhead;
-            if (k0 >= join.pieces) break;
-            if (k0 % 32 == 0) mine = ml[piece(min(k0 + lane, join.pieces - 1))];
-            load(k0);
+        for (int q = 0; q < kAhead; ++q) {
+            if (m0 + q >= join.pieces || ty[q].x == -INFINITY) continue;   // a piece without keys: its o means nothing
+            const float t = fmaxf(top, ty[q].x), a = fast_exp2(top - t), b = fast_exp2(ty[q].x - t);
+            top = t;
+            l = l * a + ty[q].y * b;
+            o.x = o.x * a + y[q].x * b;
+            o.y = o.y * a + y[q].y * b;
+            o.z = o.z * a + y[q].z * b;
+            o.w = o.w * a + y[q].w * b;
         }
     }
-    const int h = join.hkv * p.g + r % p.g;
+    const int i = r / p.g, h = join.hkv * p.g + r - i * p.g;
     float f = 1.f;
     if (p.flags & UA_FLAG_SINKS) {
         const float s2 = __ldg(p.sinks + h) * kLog2e;
         if (s2 == INFINITY) {
-            L = 0.f;
-        } else if (s2 > M) {
-            f = M == -INFINITY ? 0.f : fast_exp2(M - s2);
-            L = L * f + 1.0f;
+            l = 0.f;
+        } else if (s2 > top) {
+            f = top == -INFINITY ? 0.f : fast_exp2(top - s2);
+            l = l * f + 1.0f;
         } else if (s2 != -INFINITY) {
-            L += fast_exp2(s2 - M);
+            l += fast_exp2(s2 - top);
         }
     }
-    f = L > 0.f ? f * __frcp_rn(L) : 0.f;
-    __nv_bfloat16* dst = p.out + ((join.row0 + r / p.g) * p.hq + h) * D + lane * DPL;
-#pragma unroll
-    for (int t = 0; t < DPL; ++t) dst[t] = __float2bfloat16_rn(o[t] * f);
+    f = l > 0.f ? f * __frcp_rn(l) : 0.f;
+    *reinterpret_cast<uint2*>(p.out + ((join.row0 + i) * p.hq + h) * D + col) =
+        make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
 }
 
 template <int D>
@@ -933,7 +931,8 @@ cudaError_t launch_tree_d(const TreePlan& plan, const CUtensorMap& tq, const CUt
     kern<<<(unsigned)plan.ctas, kThreadsT, TCfg<D>::kSmem, stream>>>(tq, tm_k, tm_v, p, plan.shares);
     e = cudaGetLastError();
     if (e != cudaSuccess || plan.ctas == 1) return e;
-    return launch_early(tree_merge_kernel<D>, dim3((unsigned)plan.ctas, (unsigned)((plan.shares.slot_rows + 7) / 8)),
+    constexpr int step = 256 / (D / 4);      // rows of a CTA
+    return launch_early(tree_merge_kernel<D>, dim3((unsigned)plan.ctas, (unsigned)((plan.shares.slot_rows + step - 1) / step)),
                         256, 0, stream, p, plan.shares);
 }
 
