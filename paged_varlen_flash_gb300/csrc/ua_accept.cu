@@ -15,7 +15,9 @@
 
 #include "ua_accept.h"
 #include "ua_fp4.cuh"
+#include "ua_launch.h"
 #include "ua_plan.h"
+#include "ua_ptx.cuh"
 
 namespace ua {
 namespace {
@@ -30,6 +32,7 @@ __global__ void __launch_bounds__(1024) accept_kernel(const AcceptParams p) {
     __shared__ int len, start;
     const CacheParams& c = p.c;
     const int s = blockIdx.x, tid = threadIdx.x, b_log2 = 31 - __clz(c.b);
+    griddep_wait();
     const int32_t a = __ldg(p.cu_seqlens_q + s), z = __ldg(p.cu_seqlens_q + s + 1);
     const int32_t sk = c.seqused_k[s], last = __ldg(p.last + s);
     const int sq = z - a;
@@ -128,8 +131,7 @@ cudaError_t launch_accept(const AcceptParams& p, cudaStream_t stream) {
     const int64_t cols = 2LL * p.c.hk * (fp4 ? (p.c.d / 2 + p.c.d / 16) / 4
                                              : p.c.d * (p.c.kv_dtype == UA_DTYPE_BF16 ? 2 : 1) / 16);
     const int threads = (int)std::min<int64_t>(1024, std::max<int64_t>(64, (cols + 31) / 32 * 32));
-    (fp4 ? accept_kernel<true> : accept_kernel<false>)<<<(unsigned)p.c.num_seqs, threads, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_early(fp4 ? accept_kernel<true> : accept_kernel<false>, dim3((unsigned)p.c.num_seqs), threads, 0, stream, p);
 }
 
 }  // namespace ua

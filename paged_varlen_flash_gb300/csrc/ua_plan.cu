@@ -19,7 +19,9 @@
 #include <cstdint>
 
 #include "../../include/ua.h"
+#include "ua_launch.h"
 #include "ua_plan.h"
+#include "ua_ptx.cuh"
 
 namespace ua {
 namespace {
@@ -117,6 +119,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     int32_t* take = tok + n + 1;     // blocks taken in front of it
     int32_t* give = take + n + 1;    // blocks returned in front of it
     const int per = (n + threads - 1) / threads;
+    griddep_wait();
     const int s0 = min(n, tid * per), s1 = min(n, s0 + per);
     int64_t count = *p.pool_count;
 
@@ -327,8 +330,7 @@ cudaError_t launch_plan(const PlanParams& p, int num_sms, cudaStream_t stream) {
     const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>(most, (p.max_tokens + each - 1) / each));
     PlanParams q = p;
     q.aligned = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15u) == 0;
-    plan_kernel<<<(unsigned)ctas, threads, smem, stream>>>(q);
-    return cudaGetLastError();
+    return launch_early(plan_kernel, dim3((unsigned)ctas), threads, smem, stream, q);
 }
 
 }  // namespace ua

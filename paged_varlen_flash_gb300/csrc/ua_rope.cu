@@ -20,6 +20,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "ua_launch.h"
 #include "ua_ptx.cuh"
 #include "ua_quant.cuh"
 #include "ua_rope.h"
@@ -75,6 +76,7 @@ rope_store_kernel(const RopeParams p, const __grid_constant__ RopeTable table, f
     __shared__ float2 cs[kMaxFreq];
     const CacheParams& c = p.c;
     const int64_t token = blockIdx.x;
+    griddep_wait();
     const int n = table.n, units = c.d >> 4, unit_log2 = 31 - __clz(units);
     const int unit = threadIdx.x & (units - 1), row0 = threadIdx.x >> unit_log2, step = blockDim.x >> unit_log2;
     const int rows = p.hq + 2 * c.hk, turned = p.hq + c.hk;
@@ -167,6 +169,7 @@ rope_store_fp4_kernel(const RopeParams p, const __grid_constant__ RopeTable tabl
     __shared__ float2 cs[kMaxFreq];
     const CacheParams& c = p.c;
     const int64_t token = blockIdx.x;
+    griddep_wait();
     const int n = table.n, groups = c.d >> 4, group_log2 = 31 - __clz(groups);
     const int grp = threadIdx.x & (groups - 1), step = kThreads >> group_log2, rows = p.hq + 2 * c.hk;
     const int64_t slot = __ldg(p.slots + token);
@@ -241,8 +244,7 @@ cudaError_t launch_layout(const RopeParams& p, const RopeTable& t, cudaStream_t 
     // tokens of 48 rows 231, 229 and 309.
     const int64_t units = (int64_t)(p.hq + 2 * p.c.hk) * (p.c.d / 16);
     const int threads = p.c.kv_dtype != UA_DTYPE_FP4_E2M1 && units <= 64 * kRows ? 64 : kThreads;
-    kern<<<(unsigned)p.total_q, threads, 0, stream>>>(p, t, k_inv, v_inv);
-    return cudaGetLastError();
+    return launch_early(kern, dim3((unsigned)p.total_q), threads, 0, stream, p, t, k_inv, v_inv);
 }
 
 }  // namespace

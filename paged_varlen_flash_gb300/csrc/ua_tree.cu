@@ -272,6 +272,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         tc::tmem_alloc(smem_u32(tmem_slot), C::kCols2);
         tc::tmem_relinquish();
     }
+    griddep_wait();
     // This CTA's share: entries (row tile, sequence) in order, each thread a run of them.
     const int64_t entries = (int64_t)w.tiles * p.num_seqs;
     const int64_t per = (entries + kThreadsT - 1) / kThreadsT;
@@ -928,8 +929,7 @@ cudaError_t launch_tree_d(const TreePlan& plan, const CUtensorMap& tq, const CUt
                                               : tree_kernel<D, kPlain>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
-    kern<<<(unsigned)plan.ctas, kThreadsT, TCfg<D>::kSmem, stream>>>(tq, tm_k, tm_v, p, plan.shares);
-    e = cudaGetLastError();
+    e = launch_early(kern, dim3((unsigned)plan.ctas), kThreadsT, TCfg<D>::kSmem, stream, tq, tm_k, tm_v, p, plan.shares);
     if (e != cudaSuccess || plan.ctas == 1) return e;
     constexpr int step = 256 / (D / 4);      // rows of a CTA
     return launch_early(tree_merge_kernel<D>, dim3((unsigned)plan.ctas, (unsigned)((plan.shares.slot_rows + step - 1) / step)),
