@@ -23,7 +23,7 @@
 // two S tiles.  Barriers, tensor memory and the K/V ring live on from item to item: the
 // next item's copies and first Q K^T run under the epilogue of the one before.
 //
-// Roles (8 warps):
+// Roles (8 warps, 9 at d = 256):
 //   warps 0-3  softmax and epilogue: thread r owns row r (tensor-memory lane r); two
 //              passes over the tile's columns (maximum, then P);
 //   warp 4     walks through the share and copies (TMA) Q and the K tiles, one lane per
@@ -31,7 +31,7 @@
 //   warp 5     looks through V tiles with keys that some row does not see;
 //   warp 6     copies the V tiles;
 //   warp 7     MMA issuer and owner of tensor memory (beside warp 3, which has the last
-//              rows and the least to do).
+//              rows and the least to do); at d = 256 warp 8 issues the P V MMAs.
 // The softmax loops are kept short (32 or 64 columns, masks and score terms in a loop of
 // their own): unrolled over a row's 128 columns with every term they missed the
 // instruction cache (48 small trees with a softcap at d = 64: 88 us, of which 50 us the
@@ -60,13 +60,12 @@ using namespace pf;
 #define TREE_TURN 5
 #endif
 
-constexpr int kThreadsT = 256;
 constexpr int kWarpCopy = 4;
 constexpr int kWarpFix = 5;
 constexpr int kWarpCopyV = 6;
 constexpr int kWarpMmaT = 7;
+constexpr int kWarpPv = 8;         // d = 256
 constexpr int kCols = 64;          // columns of S a softmax thread holds at a time
-constexpr int kUnitReaders = 131;  // V copy, MMA and fix warps (a lane each), softmax threads
 
 // Score chains: the scale alone, a softcap, ALiBi with or without a softcap.
 enum { kPlain = 0, kCap = 1, kAlibi = 2 };
@@ -91,6 +90,9 @@ struct TCfg {
     static constexpr int kStages = D == 64 ? 4 : 2;     // K and V tiles each
     static constexpr int kBufs = 2;                     // S tiles
     static constexpr int kCtas = D == 256 ? 1 : 2;      // per SM
+    static constexpr bool kTwo = D == 256;              // an MMA issuer each for Q K^T and P V
+    static constexpr int kThreads = kTwo ? 288 : 256;
+    static constexpr int kUnitReaders = 131 + kTwo;     // V copy, MMA and fix warps (a lane each), softmax threads
     static constexpr int kPanels = D / 64;
     static constexpr int kQPanel = kRows * 128;         // 128 rows x 64 dims
     static constexpr int kPanel = kBN * 128;            // kBN keys x 64 dims
@@ -100,11 +102,11 @@ struct TCfg {
     static constexpr int kOffV = kOffK + kStages * kTile;
     static constexpr int kOffBar = kOffV + kStages * kTile;
     // q_full, q_empty, {k_full, k_empty, v_full, v_ready, v_empty}[kStages], s_full[2],
-    // p_full[2], o_done[2], o_free, u_full[2], u_empty[2], drain, never
-    static constexpr int kNumBars = 2 + 5 * kStages + 13;
+    // p_full[2], o_done[2], o_free, u_full[2], u_empty[2], drain[2], never
+    static constexpr int kNumBars = 2 + 5 * kStages + 14;
     static constexpr int kOffUnit = (kOffBar + kNumBars * 8 + 63) / 64 * 64;
     static constexpr int kOffMisc = kOffUnit + 2 * (int)sizeof(TreeUnit);
-    static constexpr int kSmem = kOffMisc + 128 + 1024;
+    static constexpr int kSmem = kOffMisc + 128 + 1024;   // (misc: addresses, 9 sums, the start)
     static constexpr int kTmemO = kBufs * kBN;
     static constexpr uint32_t kCols2 = D == 256 ? 512 : 256;    // tensor-memory columns
     static_assert(kTmemO + D <= (int)kCols2, "tensor memory budget");
@@ -217,7 +219,7 @@ __device__ __forceinline__ bool copy_tiles(const FwdParams& p, const CUtensorMap
 }
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreadsT, TCfg<D>::kCtas)
+__global__ void __launch_bounds__(TCfg<D>::kThreads, TCfg<D>::kCtas)
 tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_v, const FwdParams p, const TreeShares w) {
     using C = TCfg<D>;
@@ -238,12 +240,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const uint32_t v_full0 = k_empty0 + kS, v_ready0 = v_full0 + kS, v_empty0 = v_ready0 + kS;
     const uint32_t s_full0 = v_empty0 + kS, p_full0 = s_full0 + 16, o_done0 = s_full0 + 32;
     const uint32_t o_free = s_full0 + 48, u_full0 = s_full0 + 56, u_empty0 = s_full0 + 72;
-    const uint32_t drain = s_full0 + 88, never = s_full0 + 96;
+    const uint32_t drain0 = s_full0 + 88, never = s_full0 + 104;
     TreeUnit* units = reinterpret_cast<TreeUnit*>(smem + C::kOffUnit);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
-    int64_t* warp_sums = reinterpret_cast<int64_t*>(smem + C::kOffMisc + 16);   // [7]
-    int32_t* start = reinterpret_cast<int32_t*>(smem + C::kOffMisc + 80);       // entry, KV head, step
+    int64_t* warp_sums = reinterpret_cast<int64_t*>(smem + C::kOffMisc + 16);   // [9]
+    int32_t* start = reinterpret_cast<int32_t*>(smem + C::kOffMisc + 96);       // entry, KV head, step
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -260,10 +262,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             mbar_init(p_full0 + 8 * i, kRows);
             mbar_init(o_done0 + 8 * i, 1);
             mbar_init(u_full0 + 8 * i, 1);
-            mbar_init(u_empty0 + 8 * i, kUnitReaders);
+            mbar_init(u_empty0 + 8 * i, C::kUnitReaders);
         }
         mbar_init(o_free, kRows);
-        mbar_init(drain, 1);
+        mbar_init(drain0, 1);
+        mbar_init(drain0 + 8, 1);
         mbar_init(never, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -275,7 +278,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     griddep_wait();
     // This CTA's share: entries (row tile, sequence) in order, each thread a run of them.
     const int64_t entries = (int64_t)w.tiles * p.num_seqs;
-    const int64_t per = (entries + kThreadsT - 1) / kThreadsT;
+    const int64_t per = (entries + C::kThreads - 1) / C::kThreads;
     const int64_t e_lo = min(entries, threadIdx.x * per), e_hi = min(entries, e_lo + per);
     int64_t mine = 0;
     for (int64_t e = e_lo; e < e_hi; ++e) {
@@ -299,7 +302,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const uint32_t tmem = *tmem_slot;
     int64_t total = 0;
 #pragma unroll
-    for (int i = 0; i < kThreadsT / 32; ++i) {
+    for (int i = 0; i < C::kThreads / 32; ++i) {
         if (i < warp) upto += warp_sums[i];
         total += warp_sums[i];
     }
@@ -462,10 +465,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             for (int j = max(0, kt - C::kStages); j < kt; ++j)
                 mbar_wait_bounded(v_full0 + 8 * (j % C::kStages), (j / C::kStages) & 1);
         __syncwarp();
-    } else if (warp == kWarpMmaT) {
-        // ------------------------- MMA issuer (one thread) -------------------------
-        // MMAs of one thread run in issue order, so the Q K^T that goes over columns
-        // holding P cannot overtake the P V that reads them.
+    } else if (warp == kWarpMmaT || warp == kWarpPv) {
+        // ----------------------- MMA issuers (one thread each) -----------------------
+        // With one issuer MMAs run in its order, so the Q K^T that goes over columns holding
+        // P cannot overtake the P V that reads them.  At d = 256, where the MMAs bound the
+        // kernel, two issuers wait beside each other, and a Q K^T for the P V two tiles ago
+        // (2350 -> 1900 cycles a tile; their MMAs take 1300).
         constexpr int kNV = D == 64 ? 64 : 128;       // dims per P V MMA
         constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kRows, kBN, false, false);
         constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kRows, kNV, false, true);
@@ -475,6 +480,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint64_t vd = tc::smem_desc_sw128(sV, C::kPanel, 1024);
         const uint32_t q_lo = (uint32_t)qd, qk_hi = (uint32_t)(qd >> 32);
         const uint32_t k_lo = (uint32_t)kd, v_lo = (uint32_t)vd, v_hi = (uint32_t)(vd >> 32);
+        const bool does_qk = warp == kWarpMmaT, does_pv = !C::kTwo || warp == kWarpPv;
         int gt = 0, qn = 0;                           // key tiles and units with work before this unit
         bool ok = true;
         for (int u = 0;; ++u) {
@@ -492,6 +498,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (p.stall && kt == 0 &&
                     !__all_sync(0xffffffffu, wait_or_abort(never, 0, abort_flag, p.err, (uint64_t)p.stall_ns)))
                     return false;
+                if (C::kTwo && kt >= 2 && !wwait(o_done0 + 8 * buf, ((kt - 2) >> 1) & 1)) return false;
                 if (!wwait(k_full0 + 8 * stg, (kt / C::kStages) & 1)) return false;
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
@@ -507,15 +514,12 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 __syncwarp();
                 return true;
             };
-            if (!(ok = wwait(q_full, qn & 1) && issue_qk(0))) break;
-            for (int j = 0; ok && j < n; ++j) {
+            auto issue_pv = [&](int j) -> bool {
                 const int kt = gt + j, stg = kt % C::kStages, buf = kt % C::kBufs;
-                // With two S tiles the next one is filled while the softmax has this one.
-                if (C::kBufs == 2 && j + 1 < n && !(ok = issue_qk(j + 1))) break;
-                if (!(ok = wwait(v_ready0 + 8 * stg, (kt / C::kStages) & 1))) break;
-                if (!(ok = wwait(p_full0 + 8 * buf, (kt / C::kBufs) & 1))) break;
+                if (!wwait(v_ready0 + 8 * stg, (kt / C::kStages) & 1)) return false;
+                if (!wwait(p_full0 + 8 * buf, (kt / C::kBufs) & 1)) return false;
                 // The first P V overwrites O: the epilogue in front must have read it.
-                if (j == 0 && qn > 0 && !(ok = wwait(o_free, (qn - 1) & 1))) break;
+                if (j == 0 && qn > 0 && !wwait(o_free, (qn - 1) & 1)) return false;
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
                     const uint32_t vst = v_lo + stg * (C::kTile >> 4);
@@ -532,7 +536,13 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     tc::commit(v_empty0 + 8 * stg);
                 }
                 __syncwarp();
-                if (C::kBufs == 1 && j + 1 < n) ok = issue_qk(j + 1);
+                return true;
+            };
+            if (does_qk) ok = wwait(q_full, qn & 1) && issue_qk(0);
+            for (int j = 0; ok && j < n; ++j) {
+                // The next S tile is filled while the softmax has this one.
+                if (does_qk && j + 1 < n) ok = issue_qk(j + 1);
+                if (does_pv && ok) ok = issue_pv(j);
             }
             if (!ok) break;
             gt += n;
@@ -540,6 +550,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
         if (*abort_flag) {
             // No MMA of this thread may still run when tensor memory is freed.
+            const uint32_t drain = drain0 + (does_qk ? 0 : 8);
             if (tc::elect_one()) tc::commit(drain);
             __syncwarp();
             mbar_wait_bounded(drain, 0);
@@ -929,7 +940,7 @@ cudaError_t launch_tree_d(const TreePlan& plan, const CUtensorMap& tq, const CUt
                                               : tree_kernel<D, kPlain>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
-    e = launch_early(kern, dim3((unsigned)plan.ctas), kThreadsT, TCfg<D>::kSmem, stream, tq, tm_k, tm_v, p, plan.shares);
+    e = launch_early(kern, dim3((unsigned)plan.ctas), TCfg<D>::kThreads, TCfg<D>::kSmem, stream, tq, tm_k, tm_v, p, plan.shares);
     if (e != cudaSuccess || plan.ctas == 1) return e;
     constexpr int step = 256 / (D / 4);      // rows of a CTA
     return launch_early(tree_merge_kernel<D>, dim3((unsigned)plan.ctas, (unsigned)((plan.shares.slot_rows + step - 1) / step)),
