@@ -17,10 +17,7 @@
 //
 // S = Q K^T and O += P V are tcgen05.mma with M = 128 rows; P goes over its own S in
 // tensor memory.  At d = 64 and 128 a CTA keeps one S tile (256 columns of tensor memory
-// with O) and few K/V stages, so that two CTAs share an SM: while one waits for its copies
-// or for its softmax, the other one's copies are in flight.  At d = 256 Q and the tiles
-// (64 keys) fill an SM's shared memory, and one CTA overlaps its own softmax and MMAs over
-// two S tiles.  Barriers, tensor memory and the K/V ring live on from item to item: the
+// XX  Barriers, tensor memory and the K/V ring live on from item to item: the
 // next item's copies and first Q K^T run under the epilogue of the one before.
 //
 // Roles (8 warps, 9 at d = 256):
@@ -87,7 +84,7 @@ static_assert(sizeof(TreeUnit) == 64, "unit descriptor");
 template <int D>
 struct TCfg {
     static constexpr int kBN = 64;                      // keys per tile
-    static constexpr int kStages = D == 64 ? 4 : 2;     // K and V tiles each
+    static constexpr int kStages = D == 64 ? 4 : D == 128 ? 2 : 3;    // K and V tiles each
     static constexpr int kBufs = 2;                     // S tiles
     static constexpr int kCtas = D == 256 ? 1 : 2;      // per SM
     static constexpr bool kTwo = D == 256;              // an MMA issuer each for Q K^T and P V
@@ -98,7 +95,7 @@ struct TCfg {
     static constexpr int kPanel = kBN * 128;            // kBN keys x 64 dims
     static constexpr int kTile = kPanels * kPanel;
     static constexpr int kOffQ = 0;
-    static constexpr int kOffK = kPanels * kQPanel;
+    static constexpr int kOffK = kTwo ? 0 : kPanels * kQPanel;        // d = 256: Q in tensor memory
     static constexpr int kOffV = kOffK + kStages * kTile;
     static constexpr int kOffBar = kOffV + kStages * kTile;
     // q_full, q_empty, {k_full, k_empty, v_full, v_ready, v_empty}[kStages], s_full[2],
@@ -108,8 +105,9 @@ struct TCfg {
     static constexpr int kOffMisc = kOffUnit + 2 * (int)sizeof(TreeUnit);
     static constexpr int kSmem = kOffMisc + 128 + 1024;   // (misc: addresses, 9 sums, the start)
     static constexpr int kTmemO = kBufs * kBN;
+    static constexpr int kTmemQ = kTmemO + D;           // d = 256: two dims per column
     static constexpr uint32_t kCols2 = D == 256 ? 512 : 256;    // tensor-memory columns
-    static_assert(kTmemO + D <= (int)kCols2, "tensor memory budget");
+    static_assert(kTmemO + D + (kTwo ? D / 2 : 0) <= (int)kCols2, "tensor memory budget");
     static_assert(kCtas * (kSmem + 1024) <= 233472, "shared memory budget");
 };
 
@@ -248,7 +246,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     int32_t* start = reinterpret_cast<int32_t*>(smem + C::kOffMisc + 96);       // entry, KV head, step
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
+        mbar_init(q_full, C::kTwo ? kRows : 1);
         mbar_init(q_empty, 1);
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(k_full0 + 8 * i, 1);
@@ -426,15 +424,17 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (n <= 0) continue;
             ++u;
             if (st) continue;
-            if (qn >= 1 && !(ok = wwait(q_empty, (qn - 1) & 1))) break;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(q_full, (uint32_t)(g * ppt) * 128u * C::kPanels);
+            if (!C::kTwo) {
+                if (qn >= 1 && !(ok = wwait(q_empty, (qn - 1) & 1))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(q_full, (uint32_t)(g * ppt) * 128u * C::kPanels);
 #pragma unroll
-                for (int pn = 0; pn < C::kPanels; ++pn)
-                    tma_load_3d(sQ + pn * C::kQPanel, &tm_q, pn * 64, h_now * g, (int)q0 + first, q_full);
+                    for (int pn = 0; pn < C::kPanels; ++pn)
+                        tma_load_3d(sQ + pn * C::kQPanel, &tm_q, pn * 64, h_now * g, (int)q0 + first, q_full);
+                }
+                ++qn;
+                __syncwarp();
             }
-            ++qn;
-            __syncwarp();
             ok = copy_tiles<D, false>(p, tm_k, sK, k_full0, k_empty0, kt, s, h_now, sk, t_begin, n, abort_flag);
             if (!ok) break;
         }
@@ -504,12 +504,17 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (tc::elect_one()) {
                     const uint32_t kst = k_lo + stg * (C::kTile >> 4);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc::mma_bf16_lo(tmem + buf * kBN, q_lo + (k >> 2) * (C::kQPanel >> 4) + (k & 3) * 2, qk_hi,
-                                        kst + (k >> 2) * (C::kPanel >> 4) + (k & 3) * 2, qk_hi, idesc_qk, k > 0 ? 1u : 0u);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t k_at = kst + (k >> 2) * (C::kPanel >> 4) + (k & 3) * 2;
+                        if constexpr (C::kTwo)
+                            tc::mma_bf16_ts_lo(tmem + buf * kBN, tmem + C::kTmemQ + k * 8, k_at, qk_hi, idesc_qk, k > 0 ? 1u : 0u);
+                        else
+                            tc::mma_bf16_lo(tmem + buf * kBN, q_lo + (k >> 2) * (C::kQPanel >> 4) + (k & 3) * 2, qk_hi, k_at,
+                                            qk_hi, idesc_qk, k > 0 ? 1u : 0u);
+                    }
                     tc::commit(s_full0 + 8 * buf);
                     tc::commit(k_empty0 + 8 * stg);
-                    if (j + 1 == n) tc::commit(q_empty);      // the last read of Q
+                    if (!C::kTwo && j + 1 == n) tc::commit(q_empty);      // the last read of Q
                 }
                 __syncwarp();
                 return true;
@@ -538,7 +543,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 __syncwarp();
                 return true;
             };
-            if (does_qk) ok = wwait(q_full, qn & 1) && issue_qk(0);
+            if (does_qk) ok = wwait(q_full, qn & 1) && issue_qk(0);      // (fenced behind its second wait)
             for (int j = 0; ok && j < n; ++j) {
                 // The next S tile is filled while the softmax has this one.
                 if (does_qk && j + 1 < n) ok = issue_qk(j + 1);
@@ -652,6 +657,25 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 const int at = __ldg(p.positions + q0 + i);
                 if (at < ctx || at >= sk) atomicOr(p.err, (int)UA_DEVERR_TREE);
                 lo = max(0, node_position(p, q0, i, ctx, sk) - p.window + 1);
+            }
+            if constexpr (C::kTwo) {
+                // The row of Q into tensor memory.  (The last Q K^T of the unit before is
+                // complete: its scores have been read.)
+                if (live) {
+                    const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D);
+#pragma unroll 2
+                    for (int c = 0; c < D / 2; c += 16) {
+                        uint4 x[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = valid ? __ldg(src + c / 4 + e) : make_uint4(0, 0, 0, 0);
+                        const uint32_t y[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
+                                                x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
+                        tc::st16(trow + C::kTmemQ + c, y);
+                    }
+                    tc::wait_st();
+                }
+                tc::fence_before_sync();
+                mbar_arrive(q_full);
             }
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < n; ++j) {
