@@ -53,9 +53,6 @@ namespace ua {
 namespace {
 
 using namespace pf;
-#ifndef TREE_TURN
-#define TREE_TURN 5
-#endif
 
 constexpr int kWarpCopy = 4;
 constexpr int kWarpFix = 5;
@@ -118,6 +115,12 @@ __device__ __forceinline__ void store32b(void* dst, const uint32_t* v) {
                  : "memory");
 }
 
+__device__ __forceinline__ void load32b(uint32_t* v, const void* src) {
+    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "l"(src));
+}
+
 // The position of the chunk's key c, within the range that a tree can have.
 __device__ __forceinline__ int node_position(const FwdParams& p, int64_t q0, int c, int ctx, int sk) {
     return min(max(__ldg(p.positions + q0 + c), ctx), sk - 1);
@@ -161,6 +164,11 @@ __device__ __noinline__ void add_unbounded(const FwdParams& p, int s, int hkv, i
             if (!(fabsf(x) <= 3.4e38f)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
         }
     }
+}
+
+// 64-bit division where the operands need it.
+__device__ __forceinline__ int64_t div_of(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
 // Key tiles of the items of sequence s in row tile r: 0 where it has no such tile, 1 for
@@ -275,14 +283,16 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
     griddep_wait();
     // This CTA's share: entries (row tile, sequence) in order, each thread a run of them.
-    const int64_t entries = (int64_t)w.tiles * p.num_seqs;
-    const int64_t per = (entries + C::kThreads - 1) / C::kThreads;
-    const int64_t e_lo = min(entries, threadIdx.x * per), e_hi = min(entries, e_lo + per);
+    const uint32_t seqs = (uint32_t)p.num_seqs, entries = (uint32_t)w.tiles * seqs;      // (below 2^31)
+    const uint32_t per = (entries + C::kThreads - 1) / C::kThreads;
+    const uint32_t e_lo = min(entries, threadIdx.x * per), e_hi = min(entries, e_lo + per);
     int64_t mine = 0;
-    for (int64_t e = e_lo; e < e_hi; ++e) {
-        const int r = (int)(e / p.num_seqs), s = (int)(e - (int64_t)r * p.num_seqs);
+    int own_steps = 0;                           // of the run's first entry
+    for (uint32_t e = e_lo; e < e_hi; ++e) {
+        const int r = (int)(e / seqs), s = (int)(e - (uint32_t)r * seqs);
         uint32_t st;
         const int steps = item_steps<kBN>(p, s, r, st);
+        if (e == e_lo) own_steps = steps;
         mine += steps ? steps + w.turn : 0;
         if (st && r == 0 && blockIdx.x == 0) atomicOr(p.err, (int)st);
     }
@@ -304,21 +314,26 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         if (i < warp) upto += warp_sums[i];
         total += warp_sums[i];
     }
-    // A share has w.least steps at least.
-    const int64_t shares = min((int64_t)gridDim.x, (total + w.least - 1) / w.least);
+    // A share has w.least steps at least; share i begins at floor(total i / shares).
+    const int64_t shares = min((int64_t)gridDim.x, div_of(total + w.least - 1, w.least));
     const bool idle = blockIdx.x >= shares;
-    const int64_t x0 = idle ? 0 : total * blockIdx.x / shares, x1 = idle ? 0 : total * (blockIdx.x + 1) / shares;
+    const int64_t each = idle ? 0 : div_of(total, shares);
+    const uint32_t rest = idle ? 0 : (uint32_t)(total - each * shares);      // below 2^10, like the shares
+    auto share_begin = [&](uint32_t i) -> int64_t { return each * i + rest * i / (uint32_t)shares; };
+    const int64_t x0 = idle ? 0 : share_begin(blockIdx.x), x1 = idle ? 0 : share_begin(blockIdx.x + 1);
     if (!idle && x0 >= upto - mine && x0 < upto) {
         int64_t at = upto - mine;
-        for (int64_t e = e_lo; e < e_hi; ++e) {
-            const int r = (int)(e / p.num_seqs), s = (int)(e - (int64_t)r * p.num_seqs);
+        for (uint32_t e = e_lo; e < e_hi; ++e) {
+            const int r = (int)(e / seqs), s = (int)(e - (uint32_t)r * seqs);
             uint32_t st;
-            const int steps = item_steps<kBN>(p, s, r, st), item = steps ? steps + w.turn : 0;
+            const int steps = e == e_lo ? own_steps : item_steps<kBN>(p, s, r, st), item = steps ? steps + w.turn : 0;
             const int64_t all = (int64_t)item * p.hk;
             if (x0 < at + all) {
+                const int h = (int)div_of(x0 - at, item);
                 start[0] = (int32_t)e;
-                start[1] = (int32_t)((x0 - at) / item);
-                start[2] = (int32_t)((x0 - at) % item);
+                start[1] = h;
+                start[2] = (int32_t)(x0 - at - (int64_t)h * item);
+                start[3] = steps;
                 break;
             }
             at += all;
@@ -339,7 +354,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tma_prefetch_desc(&tm_k);
             tma_prefetch_desc(&tm_v);
         }
-        int64_t x = x0, e = idle ? 0 : start[0];
+        int64_t x = x0;
+        uint32_t e = idle ? 0 : (uint32_t)start[0];
         int hkv = idle ? 0 : start[1], step = idle ? 0 : start[2];
         int u = 0, qn = 0, kt = 0;     // units, Q loads, K tiles
         TreeJoin join{0, 0, 0, 0, 0};
@@ -354,29 +370,24 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
                 break;
             }
-            // The next entry with steps: 32 of them are looked at together.
-            int steps = 0;
-            for (;;) {
-                const int64_t le = e + lane;
+            // The next entry with steps (the first is known): 32 of them are looked at together.
+            int steps = x == x0 ? start[3] : 0;
+            while (steps == 0 && e < entries) {
+                const uint32_t le = e + lane;
                 uint32_t st_l = 0;
-                const int r_l = (int)(le / p.num_seqs), s_l = (int)(le - (int64_t)r_l * p.num_seqs);
+                const int r_l = (int)(le / seqs), s_l = (int)(le - (uint32_t)r_l * seqs);
                 const int n_l = le < entries ? item_steps<kBN>(p, s_l, r_l, st_l) : 0;
                 const unsigned some = __ballot_sync(0xffffffffu, n_l > 0);
-                if (some) {
-                    const int at = __ffs(some) - 1;
-                    steps = __shfl_sync(0xffffffffu, n_l, at);
-                    e += at;
-                    break;
-                }
-                e += 32;
-                if (e >= entries) break;             // not reached: x < x1 <= total
+                const int at = some ? __ffs(some) - 1 : 32;
+                if (some) steps = __shfl_sync(0xffffffffu, n_l, at);
+                e += at;
             }
-            if (steps == 0) {
+            if (steps == 0) {                        // not reached: x < x1 <= total
                 ok = false;
                 *abort_flag = 1;
                 break;
             }
-            const int r = (int)(e / p.num_seqs), s = (int)(e - (int64_t)r * p.num_seqs);
+            const int r = (int)(e / seqs), s = (int)(e - (uint32_t)r * seqs);
             int sq, sk;
             int64_t q0;
             const uint32_t st = seq_status(p, s, sq, sk, q0);
@@ -405,7 +416,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (n > 0 && !whole && step == 0) {
                 // The item begins here: its shares up to the one that holds its last tile.
                 const int64_t end = x + steps;
-                join.pieces = (int)((end * shares - 1) / total - blockIdx.x) + 1;
+                join.pieces = (int)(div_of(end * shares - 1, total) - blockIdx.x) + 1;
                 join.slot = 2 * (int)blockIdx.x + (x > x0 ? 1 : 0);
                 join.row0 = q0 + first;
                 join.nodes = min(first + ppt, sq) - first;
@@ -574,37 +585,44 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 const int stg = gt % C::kStages, key0 = (t_begin + j) * kBN;
                 if (!(ok = wwait(v_full0 + 8 * stg, (gt / C::kStages) & 1))) break;
                 if (key0 < full_lo || key0 + kBN > ctx) {
-                    uint8_t* v = smem + C::kOffV + stg * C::kTile;
-                    bool odd = false;
-                    auto clear = [&](int k_lo, int k_hi) {         // keys of the tile
-                        const int words = (k_hi - k_lo) * 8;       // 16 bytes each, per panel
+                    uint4* v = reinterpret_cast<uint4*>(smem + C::kOffV + stg * C::kTile);
+                    constexpr int kPanel16 = C::kPanel / 16;
+                    // Keys of the tile that some row does not see: [0, part) and [from, upto);
+                    // slots behind the end are nobody's and become zeros.
+                    const int part = min(max(full_lo - key0, 0), kBN), upto = min(sk - key0, kBN);
+                    const int from = max(part, min(max(ctx - key0, 0), kBN));
+                    for (int pn = 0; pn < C::kPanels; ++pn)
+                        for (int e = upto * 8 + lane; e < kBN * 8; e += 32) v[pn * kPanel16 + e] = make_uint4(0, 0, 0, 0);
+                    // The largest magnitude as 16-bit integers: 0x7f80 and more is not finite.
+                    uint32_t top = 0;
+                    auto look = [&](int k_lo, int k_hi) {
                         for (int pn = 0; pn < C::kPanels; ++pn)
-                            for (int e = lane; e < words; e += 32) {
-                                uint4* at = reinterpret_cast<uint4*>(v + pn * C::kPanel + k_lo * 128) + e;
-                                const uint4 x = *at;
-                                uint32_t y[4] = {x.x, x.y, x.z, x.w};
-                                bool hit = false;
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    if ((y[i] & 0x7f80u) == 0x7f80u) {
-                                        y[i] &= 0xffff0000u;
-                                        hit = true;
-                                    }
-                                    if ((y[i] & 0x7f800000u) == 0x7f800000u) {
-                                        y[i] &= 0xffffu;
-                                        hit = true;
-                                    }
-                                }
-                                if (hit) *at = make_uint4(y[0], y[1], y[2], y[3]);
-                                // (What lies in slots that no key has is nobody's.)
-                                const int key = key0 + k_lo + (e >> 3);
-                                odd |= hit && key >= vis_beg && key < sk;
+#pragma unroll 4
+                            for (int e = k_lo * 8 + lane; e < k_hi * 8; e += 32) {
+                                const uint4 x = v[pn * kPanel16 + e];
+                                top = __vmaxu2(top, x.x & 0x7fff7fffu);
+                                top = __vmaxu2(top, x.y & 0x7fff7fffu);
+                                top = __vmaxu2(top, x.z & 0x7fff7fffu);
+                                top = __vmaxu2(top, x.w & 0x7fff7fffu);
                             }
                     };
-                    const int part = min(max(full_lo - key0, 0), kBN);
-                    clear(0, part);
-                    clear(max(part, min(max(ctx - key0, 0), kBN)), kBN);
-                    if (odd) units[slot].odd = 1;
+                    look(0, part);
+                    look(from, upto);
+                    if (__any_sync(0xffffffffu, max(top & 0xffffu, top >> 16) >= 0x7f80u)) {
+#pragma unroll 1
+                        for (int i = lane; i < C::kPanels * kBN * 32; i += 32) {     // words of two values
+                            const int k = i / 32 % kBN;
+                            if (k >= part && (k < from || k >= upto)) continue;
+                            uint32_t* at = reinterpret_cast<uint32_t*>(v) + i;
+                            const uint32_t x = *at;
+                            uint32_t y = x;
+                            if ((x & 0x7f80u) == 0x7f80u) y &= 0xffff0000u;
+                            if ((x & 0x7f800000u) == 0x7f800000u) y &= 0xffffu;
+                            if (y == x) continue;
+                            *at = y;
+                            if (key0 + k >= vis_beg) units[slot].odd = 1;
+                        }
+                    }
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -623,7 +641,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         // The score chain is in log2 units from the products on (a factor of zero
         // would make NaN of masked scores).
         const float cap = p.softcap * kLog2e, fac = fmaxf(p.scale * (softcap ? 1.f / p.softcap : kLog2e), 0x1p-126f);
-        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+        const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0, wide_q = (reinterpret_cast<uintptr_t>(p.q) & 31u) == 0;
         int gt = 0;
         bool ok = true;
         for (int u = 0;; ++u) {
@@ -662,15 +680,24 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 // The row of Q into tensor memory.  (The last Q K^T of the unit before is
                 // complete: its scores have been read.)
                 if (live) {
-                    const uint4* src = reinterpret_cast<const uint4*>(p.q + row * D);
-#pragma unroll 2
-                    for (int c = 0; c < D / 2; c += 16) {
-                        uint4 x[4];
+                    // (Rows that are not there take the last one's values.)
+                    const uint4* src = reinterpret_cast<const uint4*>(p.q + (valid ? row : (q0 + last) * p.hq + hkv * g) * D);
+#pragma unroll 1
+                    for (int c = 0; c < D / 2; c += 64) {
+                        // 256 bytes in flight: the loads wait together.
+                        uint32_t y[64];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) x[e] = valid ? __ldg(src + c / 4 + e) : make_uint4(0, 0, 0, 0);
-                        const uint32_t y[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
-                                                x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
-                        tc::st16(trow + C::kTmemQ + c, y);
+                        for (int e = 0; e < 64; e += 8) {
+                            if (wide_q) {
+                                load32b(y + e, src + (c + e) / 4);
+                            } else {
+                                const uint4 u = __ldg(src + (c + e) / 4), v = __ldg(src + (c + e) / 4 + 1);
+                                y[e] = u.x; y[e + 1] = u.y; y[e + 2] = u.z; y[e + 3] = u.w;
+                                y[e + 4] = v.x; y[e + 5] = v.y; y[e + 6] = v.z; y[e + 7] = v.w;
+                            }
+                        }
+                        tc::st32(trow + C::kTmemQ + c, *reinterpret_cast<uint32_t(*)[32]>(y));
+                        tc::st32(trow + C::kTmemQ + c + 32, *reinterpret_cast<uint32_t(*)[32]>(y + 32));
                     }
                     tc::wait_st();
                 }
@@ -843,18 +870,24 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                         add_unbounded(p, seq, hkv, q0, mask, beg, min(end, full_lo), ctx, sq, sk, lo, c * 32, o);
                         add_unbounded(p, seq, hkv, q0, mask, max(beg, max(full_lo, ctx)), end, ctx, sq, sk, lo, c * 32, o);
                     }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
                     if (part >= 0) {
-                        if (p.part_bf16) part_store32(p, prow * D + c * 32, o);
-                        else
+                        // Column by column: a warp's 32 rows are neighbours there (row by row
+                        // these stores took 15,600 cycles at d = 256, this way XX).
+                        const int64_t at = ((int64_t)part * D + c * 32) * w.slot_rows + r;
+                        if (p.part_bf16) {
+                            __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.part_o) + at;
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8) store32b(p.part_o + prow * D + c * 32 + e, o + e);
+                            for (int e = 0; e < 32; ++e, dst += w.slot_rows) *dst = __float2bfloat16_rn(__uint_as_float(o[e]));
+                        } else {
+                            float* dst = p.part_o + at;
+#pragma unroll
+                            for (int e = 0; e < 32; ++e, dst += w.slot_rows) *dst = __uint_as_float(o[e]);
+                        }
                     } else {
                         uint32_t h[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            h[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                            h[e] = pack_bf16x2(__uint_as_float(o[2 * e]) * f, __uint_as_float(o[2 * e + 1]) * f);
                         __nv_bfloat16* dst = p.out + row * (int64_t)D + c * 32;
                         if (wide) {
                             store32b(dst, h);
@@ -882,60 +915,46 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
 }
 
-// Four values of a partial row.
-__device__ __forceinline__ float4 load_part4(const FwdParams& p, int64_t idx) {
-    if (p.part_bf16) {
-        const uint2 u = *reinterpret_cast<const uint2*>(reinterpret_cast<const __nv_bfloat16*>(p.part_o) + idx);
-        return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-    }
-    return *reinterpret_cast<const float4*>(p.part_o + idx);
-}
+constexpr int kMergeCols = 8;
 
 // Joins the pieces of the item that begins in share blockIdx.x and is cut by its end, in
-// their order.  A thread has four dims of a row, and four pieces' loads in flight: one
-// round trip to memory for what a batch leaves.
+// their order.  A thread has eight dims of a row, its warp 32 neighbouring rows, as the
+// partials lie; four pieces' loads wait together.
 template <int D>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const FwdParams p, const TreeShares w) {
-    constexpr int kChunks = D / 4, kAhead = 4;
-    const int col = (threadIdx.x % kChunks) * 4, r = blockIdx.y * (256 / kChunks) + threadIdx.x / kChunks;
+    constexpr int N = kMergeCols, kAhead = 4;
+    const int task = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int col = task % (D / N) * N, r = task / (D / N) * 32 + (threadIdx.x & 31);
     griddep_wait();                          // the partials are complete
     const TreeJoin join = w.joins[blockIdx.x];
     if (join.pieces == 0 || r >= join.nodes * p.g) return;
     const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-    float4 x[kAhead], o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float2 st[kAhead];
-    float top = -INFINITY, l = 0.f;
-    auto load = [&](int m0) {
+    float o[N], top = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-            // Piece m > 0 is the first of share blockIdx.x + m.
-            const int m = m0 + q;
-            if (m >= join.pieces) break;
-            const int64_t prow = (int64_t)(m ? 2 * ((int)blockIdx.x + m) : join.slot) * w.slot_rows + r;
-            st[q] = ml[prow];
-            x[q] = load_part4(p, prow * D + col);
-        }
-    };
-    load(0);
+    for (int t = 0; t < N; ++t) o[t] = 0.f;
+#pragma unroll 1
     for (int m0 = 0; m0 < join.pieces; m0 += kAhead) {
-        float4 y[kAhead];
-        float2 ty[kAhead];
+        float x[kAhead][N];
+        float2 st[kAhead];
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
-            y[q] = x[q];
-            ty[q] = st[q];
+            st[q] = make_float2(-INFINITY, 0.f);
+            if (m0 + q >= join.pieces) continue;
+            // Piece m > 0 is the first of share blockIdx.x + m.
+            const int64_t slot = m0 + q ? 2 * ((int)blockIdx.x + m0 + q) : join.slot;
+            st[q] = ml[slot * w.slot_rows + r];
+            const int64_t at = (slot * D + col) * w.slot_rows + r;
+#pragma unroll
+            for (int t = 0; t < N; ++t) x[q][t] = part_load(p, at + (int64_t)t * w.slot_rows);
         }
-        if (m0 + kAhead < join.pieces) load(m0 + kAhead);
 #pragma unroll
         for (int q = 0; q < kAhead; ++q) {
-            if (m0 + q >= join.pieces || ty[q].x == -INFINITY) continue;   // a piece without keys: its o means nothing
-            const float t = fmaxf(top, ty[q].x), a = fast_exp2(top - t), b = fast_exp2(ty[q].x - t);
+            if (st[q].x == -INFINITY) continue;      // a piece without keys: its o means nothing
+            const float t = fmaxf(top, st[q].x), a = fast_exp2(top - t), b = fast_exp2(st[q].x - t);
             top = t;
-            l = l * a + ty[q].y * b;
-            o.x = o.x * a + y[q].x * b;
-            o.y = o.y * a + y[q].y * b;
-            o.z = o.z * a + y[q].z * b;
-            o.w = o.w * a + y[q].w * b;
+            l = l * a + st[q].y * b;
+#pragma unroll
+            for (int k = 0; k < N; ++k) o[k] = o[k] * a + x[q][k] * b;
         }
     }
     const int i = r / p.g, h = join.hkv * p.g + r - i * p.g;
@@ -952,8 +971,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const FwdParams p, cons
         }
     }
     f = l > 0.f ? f * __frcp_rn(l) : 0.f;
-    *reinterpret_cast<uint2*>(p.out + ((join.row0 + i) * p.hq + h) * D + col) =
-        make_uint2(pack_bf16x2(o.x * f, o.y * f), pack_bf16x2(o.z * f, o.w * f));
+    *reinterpret_cast<uint4*>(p.out + ((join.row0 + i) * p.hq + h) * D + col) =
+        make_uint4(pack_bf16x2(o[0] * f, o[1] * f), pack_bf16x2(o[2] * f, o[3] * f), pack_bf16x2(o[4] * f, o[5] * f),
+                   pack_bf16x2(o[6] * f, o[7] * f));
 }
 
 template <int D>
@@ -966,9 +986,8 @@ cudaError_t launch_tree_d(const TreePlan& plan, const CUtensorMap& tq, const CUt
     if (e != cudaSuccess) return e;
     e = launch_early(kern, dim3((unsigned)plan.ctas), TCfg<D>::kThreads, TCfg<D>::kSmem, stream, tq, tm_k, tm_v, p, plan.shares);
     if (e != cudaSuccess || plan.ctas == 1) return e;
-    constexpr int step = 256 / (D / 4);      // rows of a CTA
-    return launch_early(tree_merge_kernel<D>, dim3((unsigned)plan.ctas, (unsigned)((plan.shares.slot_rows + step - 1) / step)),
-                        256, 0, stream, p, plan.shares);
+    const unsigned tasks = (unsigned)((plan.shares.slot_rows + 31) / 32 * (D / kMergeCols));
+    return launch_early(tree_merge_kernel<D>, dim3((unsigned)plan.ctas, (tasks + 7) / 8), 256, 0, stream, p, plan.shares);
 }
 
 int ctas_per_sm(int d) { return d == 256 ? 1 : 2; }
@@ -1002,7 +1021,10 @@ bool plan_tree(FwdParams* fp, int num_sms, void* workspace, size_t workspace_byt
     plan->ctas = (int)ctas;
     plan->shares.tiles = (int)tiles;
     plan->shares.least = 1;
-    plan->shares.turn = TREE_TURN;
+    // An item's turn (Q, the first tile's way through the pipeline, the epilogue) in key tiles:
+    // 64 requests of 16 to 32 nodes at d = 128 225, 218, 213 and 212 us with 0, 2, 4 and 7 of
+    // them, 48 small trees at d = 64 30 us with 3 and 33 with 8; at d = 256 159 and 157 us.
+    plan->shares.turn = p.d == 256 ? 8 : 4;
     plan->shares.slot_rows = (int)rows;
     // Partials in front, then (m, l), then the joins.
     fp->part_o = static_cast<float*>(workspace);
