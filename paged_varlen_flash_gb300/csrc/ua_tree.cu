@@ -15,24 +15,34 @@
 // tree_merge_kernel in the order of the shares.  So no SM waits for a longer
 // sequence of another one, and a batch has at most two partials per CTA.
 //
-// S = Q K^T and O += P V are tcgen05.mma with M = 128 rows; P goes over its own S in
-// tensor memory.  At d = 64 and 128 a CTA keeps one S tile (256 columns of tensor memory
-// XX  Barriers, tensor memory and the K/V ring live on from item to item: the
-// next item's copies and first Q K^T run under the epilogue of the one before.
+// S = Q K^T and O += P V are tcgen05.mma with M = 128 rows over tiles of 64 keys; P goes
+// over its own S in tensor memory.  Two S tiles, so that Q K^T of the next tile runs under
+// the softmax of this one.  At d = 64 and 128 two CTAs share an SM (256 columns of tensor
+// memory each, 80 and 96 KB of shared memory): while one waits for its copies, the other
+// one's are in flight.  At d = 256 one CTA has the SM: Q lies in tensor memory (as the A
+// operand from there a Q K^T of N = 64 takes 32 cycles per 16 dims, from shared memory 49:
+// the rows of Q alone are 4 KB at 128 bytes a cycle), which leaves shared memory for
+// three K and V tiles.  Barriers, tensor memory and the K/V rings live on from item to
+// item: the next item's copies and first Q K^T run under the epilogue of the one before.
 //
 // Roles (8 warps, 9 at d = 256):
 //   warps 0-3  softmax and epilogue: thread r owns row r (tensor-memory lane r); two
-//              passes over the tile's columns (maximum, then P);
+//              passes over the tile's columns (maximum, then P), with masks and score
+//              terms in a short loop of their own;
 //   warp 4     walks through the share and copies (TMA) Q and the K tiles, one lane per
 //              paged block;
 //   warp 5     looks through V tiles with keys that some row does not see;
 //   warp 6     copies the V tiles;
 //   warp 7     MMA issuer and owner of tensor memory (beside warp 3, which has the last
 //              rows and the least to do); at d = 256 warp 8 issues the P V MMAs.
-// The softmax loops are kept short (32 or 64 columns, masks and score terms in a loop of
-// their own): unrolled over a row's 128 columns with every term they missed the
-// instruction cache (48 small trees with a softcap at d = 64: 88 us, of which 50 us the
-// cap).
+//
+// Measured: 64 requests of 16 to 32 nodes, 512 to 8192 keys, 32 / 8 heads, d = 128: 205 us,
+// 196 of them this kernel (1.2 GB of K and V, 6.1 TB/s, 0.90 of a plain copy); bound by HBM,
+// then by the ramp at both ends.  4 requests of 64 nodes and 30,000 to 65,535 keys, 16 / 2
+// heads, d = 256: 155 us (1,270 TFLOP/s); about 1,700 cycles a tile of MMAs of 1,024, bound
+// by the chain softmax -> P V -> Q K^T and L2 (four row tiles read every key, from HBM once).
+// 48 trees of up to 64 nodes, softcap, window 1024, d = 64: 30 us, and one of 8 nodes over
+// 999 keys 12 us: starting, one tile's latency, the epilogue and the merge.
 //
 // Masked keys: their scores are replaced, whatever K holds.  Their V rows reach the
 // product with P = 0, and 0 times an infinity or NaN is NaN; so warp 5 clears values
@@ -872,7 +882,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     }
                     if (part >= 0) {
                         // Column by column: a warp's 32 rows are neighbours there (row by row
-                        // these stores took 15,600 cycles at d = 256, this way XX).
+                        // these stores took 15,600 cycles at d = 256, this way
+                        // 8,200).
                         const int64_t at = ((int64_t)part * D + c * 32) * w.slot_rows + r;
                         if (p.part_bf16) {
                             __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.part_o) + at;
@@ -1012,15 +1023,18 @@ bool plan_tree(FwdParams* fp, int num_sms, void* workspace, size_t workspace_byt
     if (p.g > kRows || p.max_seqlen_k > 1 << 30) return false;
     const int ppt = kRows / p.g, bn = TCfg<64>::kBN;
     const int64_t tiles = (p.max_seqlen_q + ppt - 1) / ppt;
-    const int64_t rows = (int64_t)std::min(ppt, p.max_seqlen_q) * p.g;
+    const int64_t rows = (int64_t)std::max(1, std::min(ppt, p.max_seqlen_q)) * p.g;
     if (tiles * p.num_seqs > 0x7fffffffLL) return false;
     // No more CTAs than steps (as far as the host knows) and than the workspace has room for.
     const int64_t steps = tiles * p.num_seqs * p.hk * ((p.max_seqlen_k + bn - 1) / bn);
     int64_t ctas = std::min<int64_t>((int64_t)ctas_per_sm(p.d) * num_sms, steps);
+    ctas = std::max<int64_t>(1, ctas);
     while (ctas > 1 && shares_bytes(ctas, rows, p.d) > workspace_bytes) ctas = ctas * 7 / 8;
     plan->ctas = (int)ctas;
     plan->shares.tiles = (int)tiles;
-    plan->shares.least = 1;
+    // Not too small shares: one request of 8000 keys, 2 KV heads, d = 64: 33.5, 23.2, 17.5 and
+    // 16.5 us with 1, 2, 4 and 6 steps at least; 8 KV heads at d = 128 31.1, 31.0, 22.0 and 22.9.
+    plan->shares.least = 5;
     // An item's turn (Q, the first tile's way through the pipeline, the epilogue) in key tiles:
     // 64 requests of 16 to 32 nodes at d = 128 225, 218, 213 and 212 us with 0, 2, 4 and 7 of
     // them, 48 small trees at d = 64 30 us with 3 and 33 with 8; at d = 256 159 and 157 us.
