@@ -428,6 +428,14 @@ def _ints():
     return _int_types
 
 
+def _check_table(table, num_seqs, width, device):
+    """Refuse a block table that is not a contiguous int32 [num_seqs, width]."""
+    shape = table.shape
+    if (table.dtype is not _ints()[0] or not table.is_contiguous() or len(shape) != 2 or shape[1] != width or
+            shape[0] < num_seqs or table.get_device() != device):
+        raise ValueError("block_table must be a contiguous int32 [num_seqs, max_blocks_per_seq]")
+
+
 def _tree_rows(parents, num_seqs, device):
     """Elements between the rows of the trees' parents [num_seqs, n]."""
     shape, stride = parents.shape, parents.stride()
@@ -681,9 +689,7 @@ class Problem:
         # A step waits for the host: checks without a call more than they take.
         i32, i64 = _ints()
         device, width = block_table.get_device(), self.max_blocks_per_seq
-        if (block_table.dtype is not i32 or not block_table.is_contiguous() or block_table.dim() != 2 or
-                block_table.shape[1] != width or block_table.shape[0] < num_seqs):
-            raise ValueError("block_table must be a contiguous int32 [num_seqs, max_blocks_per_seq]")
+        _check_table(block_table, num_seqs, width, device)
         for t, n, name in ((blocks_held, num_seqs, "blocks_held"), (free_blocks, self.num_blocks, "free_blocks"),
                            (free_count, 1, "free_count"), (ctx_lens, num_seqs, "ctx_lens"),
                            (new_lens, num_seqs, "new_lens"), (granted, num_seqs, "granted"),
@@ -751,18 +757,31 @@ class Problem:
                      stream=None):
         """``forward`` for trees of drafted tokens: of its chunk's own keys a row sees
         those whose bits its row of ``tree_mask`` (int32 or uint32 [total_q, words])
-        has.  ``positions`` (int32 [total_q]) are needed with a window or ALiBi."""
-        device = q.get_device()
+        has.  ``positions`` (int32 [total_q]) are needed with a window or ALiBi.  q and
+        ``out`` are contiguous."""
+        device, row = q.get_device(), self.num_q_heads * self.head_size
         words = _mask_stride(tree_mask, total_q, device)
         places = None
+        _check_table(block_table, num_seqs, self.max_blocks_per_seq, device)
+        if not q.is_contiguous() or q.numel() < total_q * row:
+            raise ValueError("q must be a contiguous [total_q, H_q, d]")
+        _check(q, "q", "torch.bfloat16", device)
+        i32 = _ints()[0]
+        for t, n, name in ((cu_seqlens_q, num_seqs + 1, "cu_seqlens_q"), (seqused_k, num_seqs, "seqused_k")):
+            if t.dtype is not i32 or t.numel() < n or not t.is_contiguous() or t.get_device() != device:
+                _refuse_vector(t, name, n, "int32", device)
         if positions is not None:
-            if positions.dtype is not _ints()[0] or positions.numel() < total_q or not positions.is_contiguous() or (
+            if positions.dtype is not i32 or positions.numel() < total_q or not positions.is_contiguous() or (
                     positions.get_device() != device):
                 _refuse_vector(positions, "positions", total_q, "int32", device)
             places = positions.data_ptr()
         if out is None:
             import torch
             out = torch.empty_like(q)
+        else:
+            if not out.is_contiguous() or out.numel() < total_q * row:
+                raise ValueError("out must be a contiguous [total_q, H_q, d]")
+            _check(out, "out", "torch.bfloat16", device)
         st = load_library().ua_forward_tree(
             self.handle, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
             cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), num_seqs, total_q, max_seqlen_q, max_seqlen_k,
@@ -780,6 +799,7 @@ class Problem:
         stride = _tree_rows(parents, num_seqs, device)
         if parents.shape[1] < max_seqlen_q:
             raise ValueError("parents must have a column per node")
+        _check_table(block_table, num_seqs, self.max_blocks_per_seq, device)
         if path.dim() != 2 or path.shape[0] != num_seqs or path.shape[1] < 1:
             raise ValueError("path must be [num_seqs, n]")
         i32 = _ints()[0]

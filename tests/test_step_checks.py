@@ -219,6 +219,30 @@ def test_cache_accept_arguments(p):
                      path=[i32(N + 1, 5), i32(N), i32(N, 6)[:, :5], i32(N, 0), torch.zeros(N, 5), elsewhere(i32(N, 5))]))
 
 
+def test_rows_and_tables_of_tree_calls(p):
+    """q is packed (a view of a fused projection has other strides), tables have the
+    problem's width."""
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)  # noqa: E731
+    cache = bf(BLOCKS, B, HK, D)
+    good = dict(q=bf(T, HQ, D), table=i32(N, WIDTH), cu=i32(N + 1), used=i32(N), out=bf(T, HQ, D))
+
+    def tree(**over):
+        x = {**good, **over}
+        p.forward_tree(x["q"], cache, cache, x["table"], x["cu"], x["used"], N, T, 5, 50, ua.UA_FLAG_CAUSAL, i32(T, 1),
+                       out=x["out"], stream=0)
+
+    rows = [bf(T, HQ + 2, D)[:, :HQ], bf(T - 1, HQ, D), torch.zeros(T, HQ, D), elsewhere(bf(T, HQ, D))]
+    tables = [i32(N, WIDTH + 1), i32(N - 1, WIDTH), i32(N, 2 * WIDTH)[:, ::2], torch.zeros(N, WIDTH, dtype=torch.int64)]
+    check_calls(tree, {"cu": (N + 1, torch.int32), "used": (N, torch.int32)}, dict(q=rows, out=rows, table=tables))
+    reaches_the_library(tree, out=None)
+
+    def accept(table=i32(N, WIDTH)):
+        p.cache_accept(cache, cache, table, i32(N + 1), i32(N), i32(N, 5), i32(N), N, T, 5, 50, i32(N, 5), i32(N), i32(N),
+                       stream=0)
+
+    check_calls(accept, {}, dict(table=tables))
+
+
 # ---------------------------------------------------------------- frequencies
 def test_rope_frequencies():
     plain, one = ua.rope_frequencies(64)
