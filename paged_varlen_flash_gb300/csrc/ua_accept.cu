@@ -35,8 +35,8 @@ __global__ void __launch_bounds__(1024) accept_kernel(const AcceptParams p) {
     const CacheParams& c = p.c;
     const int s = blockIdx.x, tid = threadIdx.x, b_log2 = 31 - __clz(c.b);
     griddep_wait();
-    const int32_t a = __ldg(p.cu_seqlens_q + s), z = __ldg(p.cu_seqlens_q + s + 1);
-    const int32_t sk = c.seqused_k[s], last = __ldg(p.last + s);
+    const int32_t a = p.cu_seqlens_q[s], z = p.cu_seqlens_q[s + 1];
+    const int32_t sk = c.seqused_k[s], last = p.last[s];
     const int sq = z - a;
     uint32_t st = 0;
     if (a < 0 || z < a || (int64_t)z > p.total_q) {
@@ -49,7 +49,7 @@ __global__ void __launch_bounds__(1024) accept_kernel(const AcceptParams p) {
     // Without query rows nothing was drafted, and `last` says nothing.
     const bool tree = last >= -1 && last < sq;
     const int up = st || sq == 0 || !tree ? -1 : last;
-    for (int i = tid; i <= up; i += blockDim.x) node[i] = __ldg(p.parents + (int64_t)s * p.parents_stride + i);
+    for (int i = tid; i <= up; i += blockDim.x) node[i] = p.parents[(int64_t)s * p.parents_stride + i];
     __syncthreads();
     if (tid == 0) {
         // The branch from its end on, packed at the upper end of the nodes passed: the
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(1024) accept_kernel(const AcceptParams p) {
         const int r = node[base + t];
         from[t] = -1;
         if (r == t) continue;
-        const int32_t x = __ldg(table + ((ctx + r) >> b_log2)), y = __ldg(table + ((ctx + t) >> b_log2));
+        const int32_t x = table[((ctx + r) >> b_log2)], y = table[((ctx + t) >> b_log2)];
         if (x < 0 || y < 0 || (int64_t)x >= c.num_blocks || (int64_t)y >= c.num_blocks) {
             atomicOr(c.err, (int)UA_DEVERR_BLOCK_ID);
             continue;

@@ -76,11 +76,14 @@ struct FwdParams {
 
 // Per-sequence metadata check.  Returns UA_DEVERR_* bits (0 = well formed) and
 // the sequence's S_q, S_k and first packed row.
+// EARLY: of a call's first kernel that starts under the end of the one in front, which may
+// write the lengths (so no read-only loads).
+template <bool EARLY = false>
 __device__ __forceinline__ uint32_t seq_status(const FwdParams& p, int s, int& sq, int& sk,
                                                int64_t& q0) {
-    const int32_t a = __ldg(p.cu_seqlens_q + s);
-    const int32_t e = __ldg(p.cu_seqlens_q + s + 1);
-    sk = __ldg(p.seqused_k + s);
+    const int32_t a = EARLY ? p.cu_seqlens_q[s] : __ldg(p.cu_seqlens_q + s);
+    const int32_t e = EARLY ? p.cu_seqlens_q[s + 1] : __ldg(p.cu_seqlens_q + s + 1);
+    sk = EARLY ? p.seqused_k[s] : __ldg(p.seqused_k + s);
     q0 = a;
     sq = e - a;
     uint32_t st = 0;

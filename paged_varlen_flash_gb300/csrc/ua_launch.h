@@ -11,8 +11,9 @@ namespace ua {
 // when they start.  Each calls griddep_wait() in every thread, at the latest before it
 // ends, and before it touches what the kernel in front of it writes (by plain loads: a
 // read-only load may be moved in front of the wait).  A first kernel that is launched
-// like this calls it before its first access to global memory: only its launch and
-// what it sets up on chip run under the end of whatever came before.
+// like this calls it before its first access to global memory, and has no read-only
+// loads at all (any input may be what the kernel in front writes): only its launch
+// and what it sets up on chip run under the end of whatever came before.
 template <typename... P, typename... A>
 cudaError_t launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
     cudaLaunchAttribute attr{};

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
                     bits |= 1u << (node & 31);
                 }
                 ++depth;
-                const int q = __ldg(up + node);
+                const int q = up[node];
                 if (q < -1 || q >= node) {
                     err |= UA_DEVERR_TREE;
                     break;

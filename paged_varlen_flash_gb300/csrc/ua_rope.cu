@@ -80,8 +80,8 @@ rope_store_kernel(const RopeParams p, const __grid_constant__ RopeTable table, f
     const int n = table.n, units = c.d >> 4, unit_log2 = 31 - __clz(units);
     const int unit = threadIdx.x & (units - 1), row0 = threadIdx.x >> unit_log2, step = blockDim.x >> unit_log2;
     const int rows = p.hq + 2 * c.hk, turned = p.hq + c.hk;
-    const int64_t slot = __ldg(p.slots + token);
-    const int32_t pos = __ldg(p.positions + token);
+    const int64_t slot = p.slots[token];
+    const int32_t pos = p.positions[token];
     // The thread's runs: both of rotated dims, or (with neighbours paired: each for itself) not.
     const bool half = !PAIRS && unit < n / 8;
     const int a = PAIRS || half ? 8 * unit : 2 * n + 16 * (unit - n / 8);
@@ -172,8 +172,8 @@ rope_store_fp4_kernel(const RopeParams p, const __grid_constant__ RopeTable tabl
     griddep_wait();
     const int n = table.n, groups = c.d >> 4, group_log2 = 31 - __clz(groups);
     const int grp = threadIdx.x & (groups - 1), step = kThreads >> group_log2, rows = p.hq + 2 * c.hk;
-    const int64_t slot = __ldg(p.slots + token);
-    token_turns(table, __ldg(p.positions + token), cs, 8);
+    const int64_t slot = p.slots[token];
+    token_turns(table, p.positions[token], cs, 8);
     __syncthreads();
     const int64_t block = slot >> (31 - __clz(c.b));
     const bool store = slot >= 0 && block < c.num_blocks;

@@ -126,14 +126,14 @@ __device__ __forceinline__ void store32b(void* dst, const uint32_t* v) {
 }
 
 __device__ __forceinline__ void load32b(uint32_t* v, const void* src) {
-    asm("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
                  : "l"(src));
 }
 
 // The position of the chunk's key c, within the range that a tree can have.
 __device__ __forceinline__ int node_position(const FwdParams& p, int64_t q0, int c, int ctx, int sk) {
-    return min(max(__ldg(p.positions + q0 + c), ctx), sk - 1);
+    return min(max(p.positions[q0 + c], ctx), sk - 1);
 }
 
 // Which of the 32 keys from kb on a row sees (bit e: key kb + e).  lo: the first
@@ -145,8 +145,8 @@ __device__ __forceinline__ uint32_t seen_keys(const FwdParams& p, const uint32_t
     uint32_t bits = 0xffffffffu;
     if (c0 > -32) {
         const int w = c0 >> 5;             // -1: the words in front of the chunk are all ones
-        const uint32_t a = w < 0 ? 0xffffffffu : __ldg(row + w);
-        const uint32_t b = w + 1 < p.mask_stride ? __ldg(row + w + 1) : 0u;
+        const uint32_t a = w < 0 ? 0xffffffffu : row[w];
+        const uint32_t b = w + 1 < p.mask_stride ? row[w + 1] : 0u;
         bits = __funnelshift_r(a, b, c0 & 31);
         if (sq - c0 < 32) bits &= (1u << (sq - c0)) - 1u;
     }
@@ -165,7 +165,7 @@ __device__ __noinline__ void add_unbounded(const FwdParams& p, int s, int hkv, i
     const int b_log2 = 31 - __clz(p.b);
     for (int key = beg; key < end; ++key) {
         if (!(seen_keys(p, row, q0, key, ctx, sq, sk, lo) & 1u)) continue;
-        const int32_t id = __ldg(p.block_table + (int64_t)s * p.bt_stride + (key >> b_log2));
+        const int32_t id = p.block_table[(int64_t)s * p.bt_stride + (key >> b_log2)];
         if (id < 0 || (int64_t)id >= p.num_blocks) continue;        // read as zeros
         const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_cache) +
                                  (((int64_t)id * p.b + (key & (p.b - 1))) * p.hk + hkv) * p.d + c;
@@ -187,7 +187,7 @@ template <int BN>
 __device__ __forceinline__ int item_steps(const FwdParams& p, int s, int r, uint32_t& st) {
     int sq, sk;
     int64_t q0;
-    st = seq_status(p, s, sq, sk, q0);
+    st = seq_status<true>(p, s, sq, sk, q0);
     if ((st & UA_DEVERR_CU_SEQLENS) || r * (kRows / p.g) >= sq) return 0;
     if (st) return 1;
     const int beg = (p.flags & UA_FLAG_WINDOW) ? max(0, sk - sq - p.window + 1) : 0;
@@ -209,7 +209,7 @@ __device__ __forceinline__ bool copy_tiles(const FwdParams& p, const CUtensorMap
     const int32_t* bt = p.block_table + (int64_t)s * p.bt_stride;
     auto tile_id = [&](int j) -> int32_t {
         const int blk = ((t_begin + j) << (6 - b_log2)) + lane;
-        return lane < per_tile && blk < nblk ? __ldg(bt + blk) : -1;
+        return lane < per_tile && blk < nblk ? bt[blk] : -1;
     };
     static_assert(kBN == 64, "tile of whole blocks");
     int32_t id_next = tile_id(0);
@@ -400,7 +400,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const int r = (int)(e / seqs), s = (int)(e - (uint32_t)r * seqs);
             int sq, sk;
             int64_t q0;
-            const uint32_t st = seq_status(p, s, sq, sk, q0);
+            const uint32_t st = seq_status<true>(p, s, sq, sk, q0);
             const int ctx = sk - sq, first = r * ppt;
             // The item's last w.turn steps stand for what an item costs besides its tiles.
             const int n_all = (int)min((int64_t)(steps + w.turn - step), x1 - x), n = min(n_all, steps - step);
@@ -678,11 +678,11 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
             const bool live = __any_sync(0xffffffffu, valid);   // else the warp only keeps the barriers going
             const int full_lo = window ? max(0, sk - p.window) : 0;
-            const float slope = MODE == kAlibi && valid ? __ldg(p.alibi + head) * kLog2e : 0.f;
+            const float slope = MODE == kAlibi && valid ? p.alibi[head] * kLog2e : 0.f;
             const uint32_t* mask = p.tree_mask + (q0 + min(i, last)) * p.mask_stride;
             int lo = 0;
             if (window && valid) {
-                const int at = __ldg(p.positions + q0 + i);
+                const int at = p.positions[q0 + i];
                 if (at < ctx || at >= sk) atomicOr(p.err, (int)UA_DEVERR_TREE);
                 lo = max(0, node_position(p, q0, i, ctx, sk) - p.window + 1);
             }
@@ -701,7 +701,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                             if (wide_q) {
                                 load32b(y + e, src + (c + e) / 4);
                             } else {
-                                const uint4 u = __ldg(src + (c + e) / 4), v = __ldg(src + (c + e) / 4 + 1);
+                                const uint4 u = src[(c + e) / 4], v = src[(c + e) / 4 + 1];
                                 y[e] = u.x; y[e + 1] = u.y; y[e + 2] = u.z; y[e + 3] = u.w;
                                 y[e + 4] = v.x; y[e + 5] = v.y; y[e + 6] = v.z; y[e + 7] = v.w;
                             }
@@ -857,7 +857,7 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 } else {
                     float L = l;
                     if (p.flags & UA_FLAG_SINKS) {
-                        const float s2 = __ldg(p.sinks + head) * kLog2e;
+                        const float s2 = p.sinks[head] * kLog2e;
                         if (s2 == INFINITY) {
                             L = 0.f;
                         } else if (s2 > m) {
@@ -971,7 +971,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const FwdParams p, cons
     const int i = r / p.g, h = join.hkv * p.g + r - i * p.g;
     float f = 1.f;
     if (p.flags & UA_FLAG_SINKS) {
-        const float s2 = __ldg(p.sinks + h) * kLog2e;
+        const float s2 = p.sinks[h] * kLog2e;
         if (s2 == INFINITY) {
             l = 0.f;
         } else if (s2 > top) {
@@ -1023,7 +1023,8 @@ bool plan_tree(FwdParams* fp, int num_sms, void* workspace, size_t workspace_byt
     if (p.g > kRows || p.max_seqlen_k > 1 << 30) return false;
     const int ppt = kRows / p.g, bn = TCfg<64>::kBN;
     const int64_t tiles = (p.max_seqlen_q + ppt - 1) / ppt;
-    const int64_t rows = (int64_t)std::max(1, std::min(ppt, p.max_seqlen_q)) * p.g;
+    // Nodes of a tile: no sequence has more than all tokens, whatever bound the call names.
+    const int64_t rows = std::max<int64_t>(1, std::min<int64_t>({ppt, p.max_seqlen_q, p.total_q})) * p.g;
     if (tiles * p.num_seqs > 0x7fffffffLL) return false;
     // No more CTAs than steps (as far as the host knows) and than the workspace has room for.
     const int64_t steps = tiles * p.num_seqs * p.hk * ((p.max_seqlen_k + bn - 1) / bn);

@@ -258,6 +258,50 @@ def test_a_problem_for_key_weights_has_fewer_shares():
     bt.check(got)
 
 
+@pytest.mark.parametrize("weights", [0, ua.UA_FLAG_KEY_WEIGHTS])
+@pytest.mark.parametrize("hq,hk,d,sq,sk", [(1, 1, 64, 1, 3000), (2, 1, 256, 3, 777), (4, 4, 128, 2, 1500)])
+def test_bounds_far_above_the_call(hq, hk, d, sq, sk, weights):
+    """max_seqlen_q of 64 nodes where the problem has room for a few tokens: partials are
+    as long as the tokens are many."""
+    bt = Trees(832, hq, hk, d, 16, (sq,), (sk,), words=2).device()
+    width = bt.d_table.shape[1]
+    p = ua.Problem(hq, hk, d, 16, bt.d_k.shape[0], 1, width, sq, ua.UA_FLAG_CAUSAL | weights, bt.scale)
+    got = p.forward_tree(bt.d_q, bt.d_k, bt.d_v, bt.d_table, bt.d_cu, bt.d_sk, 1, sq, 64, width * 16, ua.UA_FLAG_CAUSAL,
+                         torch.from_numpy(bt.mask.view(np.int32)).cuda())
+    assert p.check_device_error() == 0
+    bt.check(got)
+
+
+def test_each_call_sees_what_the_one_in_front_wrote():
+    """Kernels start under the end of the one in front, which has had the same lines
+    of the tables, lengths and masks in its hands."""
+    loop = Loop(833, n=24, width=16, blocks=400, nodes=16)
+    busy = torch.randn(1 << 22, device="cuda")
+    for _ in range(6):
+        loop.draw()
+        before = [x.clone() for x in (loop.table, loop.held, loop.pool, loop.left, loop.ctx, loop.k, loop.v)]
+        loop.calls()
+        fast = [x.clone() for x in (loop.table, loop.pos, loop.slots, loop.mask, loop.out, loop.path, loop.ctx, loop.k, loop.v)]
+        for x, y in zip((loop.table, loop.held, loop.pool, loop.left, loop.ctx, loop.k, loop.v), before):
+            x.copy_(y)
+        # The same calls, each behind a complete stop.
+        real = {name: getattr(loop.p, name) for name in ("plan_step", "rope_store", "forward_tree", "cache_accept")}
+        for name, call in real.items():
+            def slow(*a, call=call, **kw):
+                busy.sin_()
+                torch.cuda.synchronize()
+                out = call(*a, **kw)
+                torch.cuda.synchronize()
+                return out
+            setattr(loop.p, name, slow)
+        loop.calls()
+        for name in real:
+            delattr(loop.p, name)
+        for x, y in zip((loop.table, loop.pos, loop.slots, loop.mask, loop.out, loop.path, loop.ctx, loop.k, loop.v), fast):
+            torch.testing.assert_close(x, y, rtol=0, atol=0, equal_nan=True)
+    assert loop.p.check_device_error() == 0
+
+
 def test_calls_without_anything_to_do():
     bt = Trees(831, 8, 2, 128, 16, (2, 3), (40, 20)).device()
     p = bt.problem()
