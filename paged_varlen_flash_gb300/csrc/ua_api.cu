@@ -1028,8 +1028,8 @@ ua_status ua_forward_tree(ua_problem* p, const void* q, const void* k_cache, con
     if (!(flags & UA_FLAG_CAUSAL) || mask_stride < 1 || 32LL * mask_stride < max_seqlen_q || !on_device(p))
         return UA_ERR_INVALID_ARG;
     const ua_problem_desc& d = p->desc;
-    if ((flags & UA_FLAG_QQ_BIAS) || d.kv_dtype != UA_DTYPE_BF16 || d.path != UA_PATH_AUTO ||
-        max_seqlen_q > ua::kMaxTree)
+    if ((flags & UA_FLAG_QQ_BIAS) || d.kv_dtype == UA_DTYPE_FP8_E4M3 || d.path != UA_PATH_AUTO ||
+        max_seqlen_q > ua::kMaxTree || d.num_q_heads / d.num_kv_heads > 128)
         return UA_ERR_UNSUPPORTED;
     if (skip) return UA_OK;
     const bool places = (flags & (UA_FLAG_WINDOW | UA_FLAG_ALIBI)) != 0;
@@ -1037,6 +1037,7 @@ ua_status ua_forward_tree(ua_problem* p, const void* q, const void* k_cache, con
     fp.tree_mask = tree_mask;
     fp.mask_stride = mask_stride;
     fp.positions = positions;
+    if (d.kv_dtype == UA_DTYPE_FP4_E2M1) return run_fp4(p, &fp, reinterpret_cast<cudaStream_t>(stream));
     ua::TreePlan plan;
     if (!ua::plan_tree(&fp, p->num_sms, p->d_ws, p->tree_bytes, &plan)) return UA_ERR_UNSUPPORTED;
     rs = encode_maps(p, k_cache, v_cache, true);

@@ -29,6 +29,10 @@
 // rows each, 49 us; 8 of 1000 to 12000 keys in four segments 67 us, of which a
 // third is a tail of CTAs with longer sequences than the others'.  Codes held in registers by the
 // converters instead of the staged ring: 106 to 128 us for the latter.
+// Draft trees (TREE) differ in what a row sees: chunk keys by its row of the mask, the
+// window and ALiBi by the nodes' positions; every tile that reaches past the context is
+// looked at key by key.  64 requests of 16 to 32 nodes, 512 to 8192 keys, 32 / 8 heads,
+// d = 128: 316 us (causal chunks 314); one of 8 nodes, 999 keys, 8 / 2 heads, d = 64: 16.
 // Tensor memory: S(0), S(1) in columns [0, 256), O in [256, 256 + d).
 #include <algorithm>
 #include <cstdint>
@@ -40,6 +44,7 @@
 #include "ua_prefill_common.cuh"
 #include "ua_ptx.cuh"
 #include "ua_tc.cuh"
+#include "ua_tree_mask.cuh"
 
 namespace ua {
 namespace {
@@ -80,12 +85,15 @@ struct RCfg {
     static_assert(kRaw % 16 == 0, "bulk copy alignment");
 };
 
-// The dims (one bit per 16) that are NaN in V at keys [lo, hi) of sequence s.
-__device__ __noinline__ uint32_t nan_groups(const FwdParams& p, int s, int hkv, int lo, int hi) {
+// The dims (one bit per 16) that are NaN in V at those of the keys [lo, hi) of sequence s
+// that `sees` takes.
+template <typename Sees>
+__device__ __noinline__ uint32_t nan_groups(const FwdParams& p, int s, int hkv, int lo, int hi, Sees sees) {
     const int scale_row = p.d / 16, b_log2 = 31 - __clz(p.b);
     const int64_t page_bytes = fp4_page_bytes(p.b, p.d);
     uint32_t found = 0;
     for (int key = lo; key < hi; ++key) {
+        if (!sees(key)) continue;
         const int32_t id = __ldg(p.block_table + (int64_t)s * p.bt_stride + (key >> b_log2));
         if (id < 0 || (int64_t)id >= p.num_blocks) continue;       // reads as zeros
         const uint8_t* sc = static_cast<const uint8_t*>(p.v_cache) + ((int64_t)id * p.hk + hkv) * page_bytes +
@@ -96,7 +104,7 @@ __device__ __noinline__ uint32_t nan_groups(const FwdParams& p, int s, int hkv, 
     return found;
 }
 
-template <int D, bool GEN>
+template <int D, bool GEN, bool TREE>
 __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams p) {
     using C = RCfg<D>;
     constexpr int kBN = C::kBN;
@@ -127,8 +135,8 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
     const bool causal = (p.flags & UA_FLAG_CAUSAL) != 0;
     const bool window = (p.flags & UA_FLAG_WINDOW) != 0;
     // Keys any row of the tile sees, and this segment's.
-    const int vis_beg = window ? max(0, first + ctx - p.window + 1) : 0;
-    const int vis_end = causal ? min(sk, last + ctx + 1) : sk;
+    const int vis_beg = window ? max(0, (TREE ? 0 : first) + ctx - p.window + 1) : 0;
+    const int vis_end = causal && !TREE ? min(sk, last + ctx + 1) : sk;
     int k_beg = vis_beg, k_end = vis_end;
     if (split) {
         k_beg = max(k_beg, seg * p.chunk);
@@ -154,8 +162,8 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
     const int t_begin = k_beg / kBN;
     const int n = (k_end + kBN - 1) / kBN - t_begin;
     // Keys every row of the tile sees.
-    const int full_lo = window ? max(0, last + ctx - p.window + 1) : 0;
-    const int full_hi = causal ? min(first + ctx, sk - 1) : sk - 1;
+    const int full_lo = window ? max(0, (TREE ? sq - 1 : last) + ctx - p.window + 1) : 0;
+    const int full_hi = TREE ? ctx - 1 : causal ? min(first + ctx, sk - 1) : sk - 1;
 
     uint64_t* bar_mem = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
     const uint32_t q_full = smem_u32(bar_mem);
@@ -385,7 +393,13 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
         const bool live = __any_sync(0xffffffffu, valid);   // else the warp only keeps the barriers going
         const uint32_t trow = tmem + ((uint32_t)(warp * 32) << 16);
         const int hi = causal ? min(pos + ctx, sk - 1) : sk - 1;
-        const int lo = window ? max(0, pos + ctx - p.window + 1) : 0;
+        int lo = window ? max(0, pos + ctx - p.window + 1) : 0;
+        const uint32_t* mask = TREE ? p.tree_mask + (q0 + min(pos, last)) * p.mask_stride : nullptr;
+        if (TREE && window && valid) {
+            const int at = p.positions[q0 + pos];
+            if (at < ctx || at >= sk) atomicOr(p.err, (int)UA_DEVERR_TREE);
+            lo = max(0, node_position(p, q0, pos, ctx, sk) - p.window + 1);
+        }
         const bool softcap = GEN && (p.flags & UA_FLAG_SOFTCAP) != 0;
         const bool alibi = GEN && (p.flags & UA_FLAG_ALIBI) != 0;
         const bool qq = GEN && (p.flags & UA_FLAG_QQ_BIAS) != 0;
@@ -420,12 +434,16 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
 #pragma unroll
                     for (int h = 0; h < kCols / 32; ++h) {
                         const int key = key0 + c + h * 32;
+                        uint32_t see = 0xffffffffu;
+                        if (TREE && edge) see = seen_keys(p, mask, q0, key, ctx, sq, sk, lo);
                         if constexpr (GEN) {
+                            int at = key + lane;              // position of the lane's key
+                            if (TREE && alibi && at >= ctx && at < sk) at = node_position(p, q0, at - ctx, ctx, sk);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
                                 float v = __uint_as_float(x[h][e]) * fac;
                                 if (softcap) v = cap * tanh_from_exp2(v);
-                                if (alibi) v += slope * (float)(key + e - ctx);
+                                if (alibi) v += slope * (float)((TREE ? __shfl_sync(0xffffffffu, at, e) : key + e) - ctx);
                                 if (qq && valid && key + e >= ctx && key + e <= hi)
                                     v += __ldg(p.qq_bias + (int64_t)pos * p.qq_stride + (key + e - ctx)) * kLog2e;
                                 x[h][e] = __float_as_uint(v);
@@ -434,7 +452,8 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                         if (edge) {
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
-                                if (key + e < lo || key + e > hi) x[h][e] = __float_as_uint(-INFINITY);
+                                if (TREE ? !(see >> e & 1u) : key + e < lo || key + e > hi)
+                                    x[h][e] = __float_as_uint(-INFINITY);
                         }
                         if (GEN || edge) tc::st32(s_col + c + h * 32, x[h]);
                         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -507,8 +526,10 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
             // Dims that are NaN at keys this row sees and others of the tile do not.
             uint32_t nans = 0;
             if (valid && *nan_flag) {
-                const int beg = max(lo, t_begin * kBN), end = min(hi + 1, (t_begin + n) * kBN);
-                nans = nan_groups(p, s, hkv, beg, min(end, full_lo)) | nan_groups(p, s, hkv, max(beg, full_hi + 1), end);
+                const int beg = max(TREE ? vis_beg : lo, t_begin * kBN), end = min(TREE ? sk : hi + 1, (t_begin + n) * kBN);
+                auto sees = [&](int key) { return !TREE || (seen_keys(p, mask, q0, key, ctx, sq, sk, lo) & 1u) != 0; };
+                nans = nan_groups(p, s, hkv, beg, min(end, full_lo), sees) |
+                       nan_groups(p, s, hkv, max(beg, max(full_lo, full_hi + 1)), end, sees);
             }
             // tcgen05.ld is warp-collective: every lane of a live warp loads.
             tc::fence_after_sync();
@@ -569,7 +590,8 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
 template <int D>
 cudaError_t launch_rows_d(const Fp4RowsPlan& plan, const FwdParams& p, cudaStream_t stream) {
     const bool gen = (p.flags & (UA_FLAG_SOFTCAP | UA_FLAG_ALIBI | UA_FLAG_QQ_BIAS)) != 0;
-    auto kern = gen ? fp4_rows_kernel<D, true> : fp4_rows_kernel<D, false>;
+    auto kern = p.tree_mask ? (gen ? fp4_rows_kernel<D, true, true> : fp4_rows_kernel<D, false, true>)
+                            : (gen ? fp4_rows_kernel<D, true, false> : fp4_rows_kernel<D, false, false>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RCfg<D>::kSmem);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)(plan.tiles * plan.splits), (unsigned)p.hk, (unsigned)p.num_seqs);
@@ -581,7 +603,8 @@ cudaError_t launch_rows_d(const Fp4RowsPlan& plan, const FwdParams& p, cudaStrea
 
 bool plan_fp4_rows(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4RowsPlan* plan) {
     *plan = Fp4RowsPlan();
-    if (p.g > kRows || p.max_seqlen_k > 1 << 30 || (int64_t)p.g * p.max_seqlen_q < kFp4RowsMin) return false;
+    if (p.g > kRows || p.max_seqlen_k > 1 << 30 || (!p.tree_mask && (int64_t)p.g * p.max_seqlen_q < kFp4RowsMin))
+        return false;
     const int ppt = kRows / p.g;
     const int64_t tiles = (p.max_seqlen_q + ppt - 1) / ppt;
     // Segments.  A CTA (one per SM) costs its key tiles plus about ten tiles' time

@@ -5,7 +5,8 @@ Tolerances.  Attention: with dx the score error bound of ``score_error`` (natura
 a softmax weight w is off by at most w (2 dx + 2^-18), and a row's output by
     2^-8 |o|                        the final rounding to bf16
   + (2 dx + 2^-10 + 2^-8) sum w|v|  weights, and P rounded to bf16 for the MMA.
-bf16 partials round each of a row's pieces once more (2^-8 of at most sum w|v|).
+bf16 partials round each of a row's pieces once more (2^-8 of at most sum w|v|).  Over a
+4-bit cache P is f16 (2^-11, within the 2^-10 above), and the last 2^-8 falls away.
 
 Rotation: cos and sin are off by at most e = 2^-20: the fraction of a turn has 32 bits and
 becomes an fp32 number (half a step of a number up to 1 half turns: 2^-25 pi), sincospi
@@ -401,8 +402,8 @@ def test_rope_frequencies_are_taken_by_value():
 class Trees(Batch):
     """A batch whose chunks are trees."""
 
-    def __init__(self, seed, hq, hk, d, b, sq, sk, words=None, **kw):
-        super().__init__(seed, "bf16", hq, hk, d, b, sq, sk, **kw)
+    def __init__(self, seed, hq, hk, d, b, sq, sk, words=None, kind="bf16", **kw):
+        super().__init__(seed, kind, hq, hk, d, b, sq, sk, **kw)
         self.trees = [S.grow(self.rng, n) for n in sq]
         self.words = words or max(1, -(-max(sq) // 32))
         self.mask = np.concatenate([S.mask_of(t, self.words) for t in self.trees])
@@ -434,7 +435,7 @@ class Trees(Batch):
                 continue
             o, total, mag = self.want(s, softcap=softcap, **kw)
             dx = R.score_error(mag, self.d, softcap, extra)
-            per = 2 * dx + 2.0 ** -10 + 2.0 ** -8 + (2.0 ** -8 if bf16_parts else 0.0)
+            per = 2 * dx + 2.0 ** -10 + (2.0 ** -8 if self.kind == "bf16" else 0.0) + (2.0 ** -8 if bf16_parts else 0.0)
             ok = np.isfinite(o)
             np.testing.assert_array_equal(ok, np.isfinite(got[a:z]))
             bound = 2.0 ** -8 * np.abs(o[ok]) + per * total[ok] + 1e-30
