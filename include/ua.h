@@ -596,11 +596,10 @@ ua_status ua_rope_store(ua_problem *p, const void *q, int64_t q_stride, const vo
  *                  position is j, a chunk key's that of its row: the window keeps keys
  *                  from position(row) - W + 1 on, ALiBi adds slope * (position - ctx)
  * The mask takes the place of the causal rule: flags must have UA_FLAG_CAUSAL (else
- * UA_ERR_INVALID_ARG); UA_FLAG_QQ_BIAS is not served (UA_ERR_UNSUPPORTED).  Needs a bf16
- * or 4-bit cache, path AUTO, g <= 128, max_seqlen_q <= 1024, max_seqlen_k <= 2^30 and H_k <=
- * 65535 (else UA_ERR_UNSUPPORTED; ua_cache_expand makes bf16 pages of an fp8 cache).  A
- * value that is not finite reaches the rows that see its key and no others.  Equal calls
- * give equal bits.
+ * UA_ERR_INVALID_ARG); UA_FLAG_QQ_BIAS is not served (UA_ERR_UNSUPPORTED).  Needs path
+ * AUTO, g <= 128, max_seqlen_q <= 1024, max_seqlen_k <= 2^30 and H_k <= 65535 (else
+ * UA_ERR_UNSUPPORTED).  A value that is not finite reaches the rows that see its key and
+ * no others.  Equal calls give equal bits.
  */
 ua_status ua_forward_tree(ua_problem *p, const void *q, const void *k_cache, const void *v_cache,
                           const int32_t *block_table, const int32_t *cu_seqlens_q,

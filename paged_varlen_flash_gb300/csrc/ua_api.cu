@@ -439,7 +439,7 @@ ua_status run_combine(const ua::FwdParams& fp, cudaStream_t st) {
     return UA_ERR_CUDA;
 }
 
-// Attention over a 4-bit cache.  With fp->scores the rows' final (m, l) go to
+// Attention over a 4-bit cache, or of draft trees over an fp8 one.  With fp->scores the rows' final (m, l) go to
 // the front of the workspace, laid out like the partials of one segment.
 ua_status run_fp4(ua_problem* p, ua::FwdParams* fp, cudaStream_t st) {
     const size_t rows = (size_t)fp->total_q * p->desc.num_q_heads;
@@ -447,15 +447,17 @@ ua_status run_fp4(ua_problem* p, ua::FwdParams* fp, cudaStream_t st) {
     if (ua::plan_fp4_rows(*fp, p->num_sms, p->ws_bytes, &tiles)) {
         set_partials(p, fp, tiles.splits, tiles.chunk);
         prof_mark(p, true, st);
-        const cudaError_t e = ua::launch_fp4_rows(tiles, *fp, st);
+        const cudaError_t e = fp->kv_fp8 ? ua::launch_fp8_tree(tiles, p->map_kp, p->map_vp, *fp, st)
+                                         : ua::launch_fp4_rows(tiles, *fp, st);
         prof_mark(p, false, st);
         if (e != cudaSuccess) {
-            note_cuda(e, "fp4 rows kernel launch");
+            note_cuda(e, "quantised rows kernel launch");
             return UA_ERR_CUDA;
         }
         const bool combine = tiles.splits > 1 || fp->scores;
         p->last_launches = combine ? 2 : 1;
-        p->last_path = combine ? "fp4_rows+combine" : "fp4_rows";
+        p->last_path = fp->kv_fp8 ? (combine ? "fp8_tree+combine" : "fp8_tree")
+                                  : (combine ? "fp4_rows+combine" : "fp4_rows");
         return combine ? run_combine(*fp, st) : UA_OK;
     }
     const size_t stats = fp->scores ? rows * 2 : 0;
@@ -1028,7 +1030,7 @@ ua_status ua_forward_tree(ua_problem* p, const void* q, const void* k_cache, con
     if (!(flags & UA_FLAG_CAUSAL) || mask_stride < 1 || 32LL * mask_stride < max_seqlen_q || !on_device(p))
         return UA_ERR_INVALID_ARG;
     const ua_problem_desc& d = p->desc;
-    if ((flags & UA_FLAG_QQ_BIAS) || d.kv_dtype == UA_DTYPE_FP8_E4M3 || d.path != UA_PATH_AUTO ||
+    if ((flags & UA_FLAG_QQ_BIAS) || d.path != UA_PATH_AUTO ||
         max_seqlen_q > ua::kMaxTree || d.num_q_heads / d.num_kv_heads > 128)
         return UA_ERR_UNSUPPORTED;
     if (skip) return UA_OK;
@@ -1038,10 +1040,11 @@ ua_status ua_forward_tree(ua_problem* p, const void* q, const void* k_cache, con
     fp.mask_stride = mask_stride;
     fp.positions = positions;
     if (d.kv_dtype == UA_DTYPE_FP4_E2M1) return run_fp4(p, &fp, reinterpret_cast<cudaStream_t>(stream));
-    ua::TreePlan plan;
-    if (!ua::plan_tree(&fp, p->num_sms, p->d_ws, p->tree_bytes, &plan)) return UA_ERR_UNSUPPORTED;
     rs = encode_maps(p, k_cache, v_cache, true);
     if (rs != UA_OK) return rs;
+    if (fp.kv_fp8) return run_fp4(p, &fp, reinterpret_cast<cudaStream_t>(stream));
+    ua::TreePlan plan;
+    if (!ua::plan_tree(&fp, p->num_sms, p->d_ws, p->tree_bytes, &plan)) return UA_ERR_UNSUPPORTED;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     prof_mark(p, true, st);
     const cudaError_t e = ua::launch_tree(plan, p->map_kp, p->map_vp, fp, st);

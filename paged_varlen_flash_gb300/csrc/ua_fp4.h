@@ -1,6 +1,8 @@
 // ua_fp4.h -- launchers of the attention kernels over 4-bit (e2m1) caches (internal).
 #pragma once
 
+#include <cuda.h>
+
 #include "ua_common.cuh"
 
 namespace ua {
@@ -47,5 +49,9 @@ bool plan_fp4_rows(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4R
 // Enqueue it (p.splits / p.chunk / partial pointers set from the plan).  With
 // p.scores set partials are written even for one segment (scores are not).
 cudaError_t launch_fp4_rows(const Fp4RowsPlan& plan, const FwdParams& p, cudaStream_t stream);
+
+// The same kernel for draft trees over an fp8 cache (d = 128), through maps of b-slot boxes.
+cudaError_t launch_fp8_tree(const Fp4RowsPlan& plan, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const FwdParams& p,
+                            cudaStream_t stream);
 
 }  // namespace ua

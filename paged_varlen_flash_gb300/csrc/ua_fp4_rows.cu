@@ -1,5 +1,6 @@
 // ua_fp4_rows.cu -- attention over a 4-bit cache for calls with many packed rows
-// per KV head (prompt chunks, observation windows), on tcgen05.
+// per KV head (prompt chunks, observation windows), and of draft trees over 4-bit and
+// fp8 caches, on tcgen05.
 //
 // With a tile of 128 rows every cached value is used 128 times, so the values
 // are worth a trip through shared memory: converter threads read codes and
@@ -32,7 +33,11 @@
 // Draft trees (TREE) differ in what a row sees: chunk keys by its row of the mask, the
 // window and ALiBi by the nodes' positions; every tile that reaches past the context is
 // looked at key by key.  64 requests of 16 to 32 nodes, 512 to 8192 keys, 32 / 8 heads,
-// d = 128: 316 us (causal chunks 314); one of 8 nodes, 999 keys, 8 / 2 heads, d = 64: 16.
+// d = 128: 285 us (causal chunks 288); one of 8 nodes, 999 keys, 8 / 2 heads, d = 64: 14.
+//
+// An fp8 cache (F8, trees at d = 128) comes through the tensor maps of its pages, rows of
+// 128 bytes swizzled; its codes are exact in f16 too, and NaN stands in single values. The
+// same 64 requests 274 us; expanding the cache to bf16 pages first would move 1.8 GB more.
 // Tensor memory: S(0), S(1) in columns [0, 256), O in [256, 256 + d).
 #include <algorithm>
 #include <cstdint>
@@ -56,16 +61,17 @@ constexpr int kWarpQk = 12;        // also owns tensor memory
 constexpr int kWarpCopy = 13;
 constexpr int kCols = 64;          // columns of S a softmax thread holds at a time
 
-template <int D>
+// F8: an e4m3 cache, whose tiles are twice the bytes.
+template <int D, bool F8>
 struct RCfg {
     static constexpr int kBN = D == 256 ? 64 : 128;     // keys per tile
     static constexpr int kStages = D == 256 ? 1 : 2;    // f16 K and V tiles
-    static constexpr int kRing = D == 64 ? 4 : 3;       // 4-bit K and V tiles
+    static constexpr int kRing = F8 ? 2 : D == 64 ? 4 : 3;    // K and V tiles as they are cached
     static constexpr int kPanels = D / 64;
     static constexpr int kQPanel = kRows * 128;         // 128 rows x 64 dims, f16
     static constexpr int kPanel = kBN * 128;            // kBN keys x 64 dims, f16
     static constexpr int kTile = kPanels * kPanel;
-    static constexpr int kRaw = kBN * (D / 2 + D / 16); // codes, then scales
+    static constexpr int kRaw = F8 ? kBN * D : kBN * (D / 2 + D / 16);    // (4 bits: codes, then scales)
     static constexpr int kOffQ = 0;
     static constexpr int kOffK = kPanels * kQPanel;
     static constexpr int kOffV = kOffK + kStages * kTile;
@@ -79,21 +85,31 @@ struct RCfg {
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kSmem = kOffMisc + 16 + 1024;
     static constexpr int kTmemO = 256;
-    static constexpr int kChunks = D / 32;              // 16-byte runs of codes per key
+    static constexpr int kChunks = D / (F8 ? 16 : 32);  // 16-byte runs of codes per key
     static constexpr int kEach = kBN * kChunks / 128;   // of them per converter thread and tile
     static_assert(kSmem <= 232448, "shared memory budget");
     static_assert(kRaw % 16 == 0, "bulk copy alignment");
+    static_assert(!F8 || (D == 128 && kOffRawK % 1024 == 0), "swizzled rows of 128 bytes");
+};
+
+// A row's mask and what seen_keys wants beside it; mask = null: a row that sees all keys asked for.
+struct TreeRow {
+    const uint32_t* mask;
+    int64_t q0;
+    int ctx, sq, sk, lo;
+    __device__ __forceinline__ bool sees(const FwdParams& p, int key) const {
+        return !mask || (seen_keys(p, mask, q0, key, ctx, sq, sk, lo) & 1u) != 0;
+    }
 };
 
 // The dims (one bit per 16) that are NaN in V at those of the keys [lo, hi) of sequence s
-// that `sees` takes.
-template <typename Sees>
-__device__ __noinline__ uint32_t nan_groups(const FwdParams& p, int s, int hkv, int lo, int hi, Sees sees) {
+// that the row sees.
+__device__ __noinline__ uint32_t nan_groups(const FwdParams& p, int s, int hkv, int lo, int hi, TreeRow row) {
     const int scale_row = p.d / 16, b_log2 = 31 - __clz(p.b);
     const int64_t page_bytes = fp4_page_bytes(p.b, p.d);
     uint32_t found = 0;
     for (int key = lo; key < hi; ++key) {
-        if (!sees(key)) continue;
+        if (!row.sees(p, key)) continue;
         const int32_t id = __ldg(p.block_table + (int64_t)s * p.bt_stride + (key >> b_log2));
         if (id < 0 || (int64_t)id >= p.num_blocks) continue;       // reads as zeros
         const uint8_t* sc = static_cast<const uint8_t*>(p.v_cache) + ((int64_t)id * p.hk + hkv) * page_bytes +
@@ -104,9 +120,25 @@ __device__ __noinline__ uint32_t nan_groups(const FwdParams& p, int s, int hkv, 
     return found;
 }
 
-template <int D, bool GEN, bool TREE>
-__global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams p) {
-    using C = RCfg<D>;
+// The dims 32 c .. 32 c + 31 that are NaN in an e4m3 cache's V at those keys.
+__device__ __noinline__ uint32_t nan_dims(const FwdParams& p, int s, int hkv, int lo, int hi, int c, TreeRow row) {
+    const int b_log2 = 31 - __clz(p.b);
+    uint32_t found = 0;
+    for (int key = lo; key < hi; ++key) {
+        if (!row.sees(p, key)) continue;
+        const int32_t id = __ldg(p.block_table + (int64_t)s * p.bt_stride + (key >> b_log2));
+        if (id < 0 || (int64_t)id >= p.num_blocks) continue;       // reads as zeros
+        const uint8_t* v = static_cast<const uint8_t*>(p.v_cache) +
+                           (((int64_t)id * p.b + (key & (p.b - 1))) * p.hk + hkv) * p.d + 32 * c;
+        for (int e = 0; e < 32; ++e)
+            if ((v[e] & 0x7f) == 0x7f) found |= 1u << e;
+    }
+    return found;
+}
+
+template <int D, bool GEN, bool TREE, bool F8>
+__device__ __forceinline__ void rows_body(const FwdParams& p, const CUtensorMap* tm_k, const CUtensorMap* tm_v) {
+    using C = RCfg<D, F8>;
     constexpr int kBN = C::kBN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -301,7 +333,9 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
             uint8_t* ring = smem + (op ? C::kOffRawV : C::kOffRawK);
             auto id_of = [&](int j) -> int32_t {       // -2: no such page
                 const int blk = ((t_begin + j) * kBN >> b_log2) + page;
-                return j < n && page < pages && blk < nblk ? __ldg(bt + blk) : -2;
+                if (j >= n || page >= pages || blk >= nblk) return -2;
+                const int32_t id = __ldg(bt + blk);
+                return F8 && id == -2 ? -1 : id;
             };
             int32_t id_next = id_of(0);
             int issued = 0;
@@ -310,6 +344,21 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                 const int32_t id = id_next;
                 id_next = id_of(j + 1);
                 if (j >= C::kRing && !wwait(empty0 + 8 * slot, ((j / C::kRing) + 1) & 1)) break;
+                if constexpr (F8) {
+                    // Boxes of a block's slots, 128 bytes each; a bad block's are filled with zeros.
+                    const bool there = id != -2;
+                    const unsigned boxes = __ballot_sync(0xffffffffu, there);
+                    if (there && (id < 0 || (int64_t)id >= p.num_blocks)) atomicOr(p.err, (int)UA_DEVERR_BLOCK_ID);
+                    if (lane < 2)
+                        mbar_arrive_expect_tx(full0 + 8 * slot,
+                                              (uint32_t)__popc(boxes & (op ? 0xaaaaaaaau : 0x55555555u)) * p.b * 128);
+                    __syncwarp();
+                    if (there)
+                        tma_load_4d(smem_u32(ring + slot * C::kRaw + page * p.b * 128), op ? tm_v : tm_k, 0, hkv, 0, id,
+                                    full0 + 8 * slot);
+                    issued = j + 1;
+                    continue;
+                }
                 const bool good = id >= 0 && (int64_t)id < p.num_blocks;
                 const unsigned mask = __ballot_sync(0xffffffffu, good);
                 uint8_t* codes = ring + slot * C::kRaw + page * code_bytes;
@@ -364,8 +413,41 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
             // that only some rows see; the epilogue gives those rows the NaN.
             const int key0 = (t_begin + j) * kBN;
             const bool edge = is_v && (key0 < full_lo || key0 + kBN - 1 > full_hi);
+            if constexpr (F8) {
 #pragma unroll 2
-            for (int i = 0; i < C::kEach; ++i) {
+                for (int i = 0; i < C::kEach; ++i) {
+                    const int k = k0 + i * (128 / C::kChunks), key = key0 + k;
+                    const uint4 c = *reinterpret_cast<const uint4*>(raw + k * 128 + ((chunk ^ (k & 7)) << 4));
+                    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                    uint32_t h[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        h[2 * e] = e4m3x2_to_f16(w[e] & 0xffffu);
+                        h[2 * e + 1] = e4m3x2_to_f16(w[e] >> 16);
+                    }
+                    if (edge && (key < full_lo || key > full_hi)) {
+                        if (key < vis_beg || key >= vis_end) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) h[e] = 0;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t x = h[e];
+                                if ((x & 0x7c00u) == 0x7c00u) h[e] &= 0xffff0000u;
+                                if ((x & 0x7c000000u) == 0x7c000000u) h[e] &= 0xffffu;
+                                if (h[e] != x) *nan_flag = 1;
+                            }
+                        }
+                    }
+                    uint8_t* row = tiles_mem + stg * C::kTile + (chunk >> 2) * C::kPanel + k * 128;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<uint4*>(row + ((((chunk & 3) * 2 + e) ^ (k & 7)) << 4)) =
+                            make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+                }
+            }
+#pragma unroll 2
+            for (int i = 0; i < (F8 ? 0 : C::kEach); ++i) {
                 const int k = k0 + i * (128 / C::kChunks);
                 const uint4 c = *reinterpret_cast<const uint4*>(raw + k * (D / 2) + chunk * 16);
                 uint32_t s8 = *reinterpret_cast<const uint16_t*>(raw + kBN * (D / 2) + k * (D / 16) + chunk * 2);
@@ -525,9 +607,10 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
         if (ok && live) {
             // Dims that are NaN at keys this row sees and others of the tile do not.
             uint32_t nans = 0;
-            if (valid && *nan_flag) {
-                const int beg = max(TREE ? vis_beg : lo, t_begin * kBN), end = min(TREE ? sk : hi + 1, (t_begin + n) * kBN);
-                auto sees = [&](int key) { return !TREE || (seen_keys(p, mask, q0, key, ctx, sq, sk, lo) & 1u) != 0; };
+            const bool look = valid && *nan_flag;
+            const int beg = max(TREE ? vis_beg : lo, t_begin * kBN), end = min(TREE ? sk : hi + 1, (t_begin + n) * kBN);
+            const TreeRow sees{mask, q0, ctx, sq, sk, lo};
+            if (!F8 && look) {
                 nans = nan_groups(p, s, hkv, beg, min(end, full_lo), sees) |
                        nan_groups(p, s, hkv, max(beg, max(full_lo, full_hi + 1)), end, sees);
             }
@@ -561,9 +644,12 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
                 tc::ld32(trow + C::kTmemO + c * 32, o);
                 tc::wait_ld();
                 if (!valid) continue;
+                if (F8 && look)
+                    nans = nan_dims(p, s, hkv, beg, min(end, full_lo), c, sees) |
+                           nan_dims(p, s, hkv, max(beg, max(full_lo, full_hi + 1)), end, c, sees);
 #pragma unroll
                 for (int e = 0; e < 32; ++e)
-                    o[e] = nans >> (2 * c + e / 16) & 1 ? 0x7fffffffu : __float_as_uint(__uint_as_float(o[e]) * f);
+                    o[e] = nans >> (F8 ? e : 2 * c + e / 16) & 1 ? 0x7fffffffu : __float_as_uint(__uint_as_float(o[e]) * f);
                 if (split) {
                     part_store32(p, (row * p.splits + seg) * D + c * 32, o);
                 } else {
@@ -587,15 +673,26 @@ __global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams 
     }
 }
 
+template <int D, bool GEN, bool TREE>
+__global__ void __launch_bounds__(kThreadsR, 1) fp4_rows_kernel(const FwdParams p) {
+    rows_body<D, GEN, TREE, false>(p, nullptr, nullptr);
+}
+
+template <bool GEN>
+__global__ void __launch_bounds__(kThreadsR, 1)
+fp8_tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
+    rows_body<128, GEN, true, true>(p, &tm_k, &tm_v);
+}
+
 template <int D>
 cudaError_t launch_rows_d(const Fp4RowsPlan& plan, const FwdParams& p, cudaStream_t stream) {
     const bool gen = (p.flags & (UA_FLAG_SOFTCAP | UA_FLAG_ALIBI | UA_FLAG_QQ_BIAS)) != 0;
     auto kern = p.tree_mask ? (gen ? fp4_rows_kernel<D, true, true> : fp4_rows_kernel<D, false, true>)
                             : (gen ? fp4_rows_kernel<D, true, false> : fp4_rows_kernel<D, false, false>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RCfg<D>::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, RCfg<D, false>::kSmem);
     if (e != cudaSuccess) return e;
     dim3 grid((unsigned)(plan.tiles * plan.splits), (unsigned)p.hk, (unsigned)p.num_seqs);
-    kern<<<grid, kThreadsR, RCfg<D>::kSmem, stream>>>(p);
+    kern<<<grid, kThreadsR, RCfg<D, false>::kSmem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -650,6 +747,19 @@ cudaError_t launch_fp4_rows(const Fp4RowsPlan& plan, const FwdParams& p, cudaStr
         case 256: return launch_rows_d<256>(plan, p, stream);
         default: return cudaErrorInvalidValue;
     }
+}
+
+cudaError_t launch_fp8_tree(const Fp4RowsPlan& plan, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const FwdParams& p,
+                            cudaStream_t stream) {
+    if (p.d != 128) return cudaErrorInvalidValue;
+    const bool gen = (p.flags & (UA_FLAG_SOFTCAP | UA_FLAG_ALIBI)) != 0;
+    auto kern = gen ? fp8_tree_kernel<true> : fp8_tree_kernel<false>;
+    constexpr int smem = RCfg<128, true>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    dim3 grid((unsigned)(plan.tiles * plan.splits), (unsigned)p.hk, (unsigned)p.num_seqs);
+    kern<<<grid, kThreadsR, smem, stream>>>(tm_k, tm_v, p);
+    return cudaGetLastError();
 }
 
 }  // namespace ua
