@@ -173,7 +173,8 @@ typedef struct ua_problem ua_problem;
  * Validate *desc and create a problem bound to the current CUDA device.  The
  * problem owns a device workspace (split-KV partials of fp32 (m, l, o), the
  * device error word) that is allocated here, once; ua_forward allocates
- * nothing.  Returns UA_ERR_INVALID_ARG for malformed fields (e.g. H_q % H_k !=
+ * nothing.  (Of a bf16 cache it has room for the partials of ua_forward_tree: two
+ * tiles of up to 128 rows per share of the work, about 41 MB at most.)  Returns UA_ERR_INVALID_ARG for malformed fields (e.g. H_q % H_k !=
  * 0, WINDOW without CAUSAL), UA_ERR_UNSUPPORTED for d or b outside the sets
  * above or a non-bf16 dtype, UA_ERR_OUT_OF_MEMORY if the workspace cannot be
  * allocated.  *out is set only on UA_OK; free it with ua_destroy.
