@@ -460,6 +460,8 @@ ua_status run_fp4(ua_problem* p, ua::FwdParams* fp, cudaStream_t st) {
                                   : (combine ? "fp4_rows+combine" : "fp4_rows");
         return combine ? run_combine(*fp, st) : UA_OK;
     }
+    // The kernel below knows no tree masks and reads 4-bit pages alone.
+    if (fp->tree_mask || fp->kv_fp8) return UA_ERR_UNSUPPORTED;
     const size_t stats = fp->scores ? rows * 2 : 0;
     ua::Fp4Plan plan;
     if (!ua::plan_fp4(*fp, p->num_sms, p->ws_bytes - stats * sizeof(float) - 16, &plan)) return UA_ERR_UNSUPPORTED;
@@ -1031,7 +1033,8 @@ ua_status ua_forward_tree(ua_problem* p, const void* q, const void* k_cache, con
         return UA_ERR_INVALID_ARG;
     const ua_problem_desc& d = p->desc;
     if ((flags & UA_FLAG_QQ_BIAS) || d.path != UA_PATH_AUTO ||
-        max_seqlen_q > ua::kMaxTree || d.num_q_heads / d.num_kv_heads > 128)
+        max_seqlen_q > ua::kMaxTree || max_seqlen_k > 1 << 30 || d.num_kv_heads > 65535 ||
+        d.num_q_heads / d.num_kv_heads > 128)
         return UA_ERR_UNSUPPORTED;
     if (skip) return UA_OK;
     const bool places = (flags & (UA_FLAG_WINDOW | UA_FLAG_ALIBI)) != 0;
