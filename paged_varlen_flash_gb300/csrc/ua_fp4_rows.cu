@@ -703,7 +703,8 @@ bool plan_fp4_rows(const FwdParams& p, int num_sms, size_t workspace_bytes, Fp4R
     if (p.g > kRows || p.max_seqlen_k > 1 << 30 || (!p.tree_mask && (int64_t)p.g * p.max_seqlen_q < kFp4RowsMin))
         return false;
     const int ppt = kRows / p.g;
-    const int64_t tiles = (p.max_seqlen_q + ppt - 1) / ppt;
+    // (One tile at least: it reports sequences of more rows than a call allows, also one of none.)
+    const int64_t tiles = std::max(1, (p.max_seqlen_q + ppt - 1) / ppt);
     // Segments.  A CTA (one per SM) costs its key tiles plus about ten tiles' time
     // to start and finish, a segment about one more in the join.  The host knows
     // the longest sequence only, so the number taken is the one whose time is

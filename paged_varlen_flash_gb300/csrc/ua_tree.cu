@@ -996,7 +996,8 @@ bool plan_tree(FwdParams* fp, int num_sms, void* workspace, size_t workspace_byt
     *plan = TreePlan();
     if (p.g > kRows || p.max_seqlen_k > 1 << 30) return false;
     const int ppt = kRows / p.g, bn = TCfg<64>::kBN;
-    const int64_t tiles = (p.max_seqlen_q + ppt - 1) / ppt;
+    // (One tile at least: it reports sequences of more rows than a call allows, also one of none.)
+    const int64_t tiles = std::max(1, (p.max_seqlen_q + ppt - 1) / ppt);
     // Nodes of a tile: no sequence has more than all tokens, whatever bound the call names.
     const int64_t rows = std::max<int64_t>(1, std::min<int64_t>({ppt, p.max_seqlen_q, p.total_q})) * p.g;
     if (tiles * p.num_seqs > 0x7fffffffLL) return false;
