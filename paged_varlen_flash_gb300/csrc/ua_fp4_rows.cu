@@ -477,10 +477,10 @@ __device__ __forceinline__ void rows_body(const FwdParams& p, const CUtensorMap*
         const int hi = causal ? min(pos + ctx, sk - 1) : sk - 1;
         int lo = window ? max(0, pos + ctx - p.window + 1) : 0;
         const uint32_t* mask = TREE ? p.tree_mask + (q0 + min(pos, last)) * p.mask_stride : nullptr;
-        if (TREE && window && valid) {
+        if (TREE && (p.flags & (UA_FLAG_WINDOW | UA_FLAG_ALIBI)) && valid) {
             const int at = p.positions[q0 + pos];
             if (at < ctx || at >= sk) atomicOr(p.err, (int)UA_DEVERR_TREE);
-            lo = max(0, node_position(p, q0, pos, ctx, sk) - p.window + 1);
+            if (window) lo = max(0, node_position(p, q0, pos, ctx, sk) - p.window + 1);
         }
         const bool softcap = GEN && (p.flags & UA_FLAG_SOFTCAP) != 0;
         const bool alibi = GEN && (p.flags & UA_FLAG_ALIBI) != 0;

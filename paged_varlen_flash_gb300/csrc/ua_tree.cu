@@ -655,10 +655,10 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const float slope = MODE == kAlibi && valid ? p.alibi[head] * kLog2e : 0.f;
             const uint32_t* mask = p.tree_mask + (q0 + min(i, last)) * p.mask_stride;
             int lo = 0;
-            if (window && valid) {
+            if ((window || MODE == kAlibi) && valid) {
                 const int at = p.positions[q0 + i];
                 if (at < ctx || at >= sk) atomicOr(p.err, (int)UA_DEVERR_TREE);
-                lo = max(0, node_position(p, q0, i, ctx, sk) - p.window + 1);
+                if (window) lo = max(0, node_position(p, q0, i, ctx, sk) - p.window + 1);
             }
             if constexpr (C::kTwo) {
                 // The row of Q into tensor memory.  (The last Q K^T of the unit before is

@@ -1,15 +1,11 @@
-"""Step calls at the edges of what their documentation allows: batches without rows,
-positions out of range, results that a call allocates, budgets that are met, far angles,
-tables of 16384 sequences, random rotary stores.  Tolerances: tests/test_step_ops_gpu.py
-where nothing else is said."""
+"""Tree calls at the edges of what their documentation allows: batches without rows and
+positions out of range.  Tolerances: tests/test_step_ops_gpu.py."""
 import numpy as np
 import pytest
 import torch
 
 import paged_varlen_flash_gb300 as ua
-from tests import cache_ref as R
-from tests import step_ref as S
-from tests.test_step_ops_gpu import Planned, Trees, _built, check_rotated, i32, same  # noqa: F401
+from tests.test_step_ops_gpu import Trees, _built, i32  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -32,3 +28,26 @@ def test_trees_of_a_batch_without_rows(kind, d):
         assert p.check_device_error() == 0 and bool((out == 7).all())
     call(bt.d_cu, bt.d_sk, 40)
     assert p.check_device_error() == ua.UA_DEVERR_BOUNDS and bool((out == 0).all())
+
+
+# ---------------------------------------------------------------- positions out of range
+@pytest.mark.parametrize("kind,d", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("fp8", 128), ("fp4", 64), ("fp4", 128),
+                                    ("fp4", 256)])
+@pytest.mark.parametrize("at,moved", [(2000, 39), (-1, 35), (34, 35), (40, 39)])
+def test_alibi_positions_outside_the_chunk_are_reported(kind, d, at, moved):
+    """With ALiBi alone, as with a window: moved into the chunk and reported.  Good ones are not."""
+    bt = Trees(2001, 4, 2, d, 16, (5, 3), (40, 20), kind=kind).device()
+    alibi = np.array([0.5, 0.25, 0.125, 1.0], np.float32)
+    flags = ua.UA_FLAG_CAUSAL | ua.UA_FLAG_ALIBI
+    p = bt.problem(flags)
+    bt.check(bt.run(p, flags, alibi=alibi), alibi=alibi)
+    assert p.check_device_error() == 0
+    bt.pos[0][2] = at
+    got = bt.run(p, flags, alibi=alibi)
+    assert p.check_device_error() == ua.UA_DEVERR_TREE
+    bt.pos[0][2] = moved
+    bt.check(got, alibi=alibi)
+    # Without a window or ALiBi positions are not read.
+    bt.pos[0][2] = at
+    bt.check(bt.run(p, ua.UA_FLAG_CAUSAL))
+    assert p.check_device_error() == 0
