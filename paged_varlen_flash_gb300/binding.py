@@ -182,6 +182,23 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _empty_like(t, stream):
+    """Memory like t's for a call on ``stream``.  The allocator hands out what its current
+    stream has given back, which kernels of that stream may still use: another stream gets
+    memory of its own, kept until what the current one has queued by then is done."""
+    import torch
+    if stream is None or not t.is_cuda:
+        return torch.empty_like(t)
+    raw, current = _stream(stream), torch.cuda.current_stream(t.device)
+    if raw == current.cuda_stream:
+        return torch.empty_like(t)
+    own = torch.cuda.ExternalStream(raw, device=t.device) if raw else torch.cuda.default_stream(t.device)
+    with torch.cuda.stream(own):
+        out = torch.empty_like(t)
+    out.record_stream(current)
+    return out
+
+
 def flags_of(causal=True, softcap=0.0, alibi=False, window=0, sinks=False, qq_bias=False):
     f = 0
     if causal:
@@ -558,8 +575,7 @@ class Problem:
                 total_q, max_seqlen_q, max_seqlen_k, flags, sinks=None, alibi_slopes=None,
                 out=None, stream=None):
         if out is None:
-            import torch
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         st = ua_forward(self.handle, q, k_cache, v_cache, block_table, cu_seqlens_q,
                         seqused_k, num_seqs, total_q, max_seqlen_q, max_seqlen_k, flags,
                         sinks, alibi_slopes, out, stream)
@@ -571,8 +587,7 @@ class Problem:
                      num_seqs, total_q, max_seqlen_q, max_seqlen_k, topk_idx, topk_len, flags,
                      sinks=None, alibi_slopes=None, out=None, stream=None):
         if out is None:
-            import torch
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         if topk_idx.dim() != 2 or topk_idx.stride(1) != 1:
             raise ValueError("topk_idx must be [total_q, K] with unit inner stride")
         st = ua_forward_topk(self.handle, q, k_cache, v_cache, block_table, cu_seqlens_q,
@@ -594,8 +609,7 @@ class Problem:
         if weights_in is not None and _weight_rows(weights_in, "weights_in", *rows) != stride:
             raise ValueError("weights_in and weights_out must share a row stride")
         if out is None:
-            import torch
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         st = ua_forward_weights(self.handle, q, k_cache, v_cache, block_table, cu_seqlens_q,
                                 seqused_k, num_seqs, total_q, max_seqlen_q, max_seqlen_k, flags,
                                 sinks, alibi_slopes, weights_in, weights_out, stride, decay, out,
@@ -732,8 +746,7 @@ class Problem:
         if _token_stride(v_new, "v_new", total_q, self.num_kv_heads, self.head_size) != stride:
             raise ValueError("k_new and v_new must share a token stride")
         if q_out is None:
-            import torch
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _empty_like(q, stream)
         out_stride = _token_stride(q_out, "q_out", total_q, self.num_q_heads, self.head_size)
         _check(q, "q", "torch.bfloat16", device)
         _check(k_new, "k_new", "torch.bfloat16", device)
@@ -776,8 +789,7 @@ class Problem:
                 _refuse_vector(positions, "positions", total_q, "int32", device)
             places = positions.data_ptr()
         if out is None:
-            import torch
-            out = torch.empty_like(q)
+            out = _empty_like(q, stream)
         else:
             if not out.is_contiguous() or out.numel() < total_q * row:
                 raise ValueError("out must be a contiguous [total_q, H_q, d]")
