@@ -516,7 +516,9 @@ ua_status ua_cache_evict(ua_problem *p, void *k_cache, void *v_cache, const int3
  * the stack with the first of them on top (first sequence, lowest position); then
  * sequences in their order take what they lack from the top.  A sequence that needs
  * more blocks than are left, counting what those in front of it asked for, gets no
- * tokens and keeps what it has; sequences that need no further block always get theirs.
+ * tokens and keeps what it has; sequences that need no further block are served always.
+ * Of the served ones those get tokens whose last one is within max_tokens, counting the
+ * tokens of all served ones in front.
  * (A finished request passes ctx = new = 0, rejected drafts simply a smaller ctx in
  * the next step.  A step that is followed by one with new = 0 leaves the pool as it
  * was.)
@@ -534,8 +536,9 @@ ua_status ua_cache_evict(ua_problem *p, void *k_cache, void *v_cache, const int3
  *   max_tokens     host-side bound on the tokens, <= max_total_q; places behind the last
  *                  token get position 0 and slot -1
  * Malformed lengths (negative, past max_blocks_per_seq * b, past parents_stride or 32 *
- * mask_stride, or tokens past max_tokens) get nothing (UA_DEVERR_BOUNDS), a bad block id
- * the slot -1 (UA_DEVERR_BLOCK_ID), a bad parent ends its branch (UA_DEVERR_TREE).
+ * mask_stride) get nothing and seqused_k = 0; these and tokens past max_tokens are
+ * reported (UA_DEVERR_BOUNDS).  A bad block id gives the slot -1 (UA_DEVERR_BLOCK_ID), a
+ * bad parent ends its branch (UA_DEVERR_TREE).
  * Needs num_seqs <= 16384 (else UA_ERR_UNSUPPORTED).  Arrays may not overlap otherwise.
  */
 ua_status ua_plan_step(ua_problem *p, int32_t *block_table, int32_t *blocks_held,

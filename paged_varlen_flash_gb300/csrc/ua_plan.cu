@@ -150,16 +150,31 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
     if (!sane) count = 0;
     if (!returns) err |= UA_DEVERR_POOL;
     const int64_t R = returns ? all.b : 0;
-    // 2. Prefix sums of what is given out.
-    Sums got{0, 0, 0}, sum;
-    auto each = [&](auto&& f) {
-        int64_t more = before.a, fresh = before.c;
+    // 2. Prefix sums of what is given out.  Places are asked for by the sequences that the
+    // pool serves.  (Where it serves all of them, or there are places for all tokens, the sums
+    // above will do: the same for the whole CTA.)
+    const bool dry = all.a > count + R && all.c > p.max_tokens;
+    int64_t fresh_before = before.c;
+    if (dry) {
+        Sums served{0, 0, 0}, unused;
+        int64_t more = before.a;
         for (int s = s0; s < s1; ++s) {
             const Ask a = ask(s);
             more += a.more;
-            fresh += a.fresh;
-            const bool fits = fresh <= p.max_tokens, ok = fits && (a.more == 0 || more <= count + R);
-            if (!fits && a.fresh) err |= UA_DEVERR_BOUNDS;
+            if (a.more == 0 || more <= count + R) served.c += a.fresh;
+        }
+        fresh_before = prefix(served, warp_sums[1], &unused).c;
+    }
+    Sums got{0, 0, 0}, sum;
+    auto each = [&](auto&& f) {
+        int64_t more = before.a, fresh = fresh_before;
+        for (int s = s0; s < s1; ++s) {
+            const Ask a = ask(s);
+            more += a.more;
+            const bool served = a.more == 0 || more <= count + R;
+            if (served) fresh += a.fresh;
+            const bool fits = fresh <= p.max_tokens, ok = fits && served;
+            if (served && !fits && a.fresh) err |= UA_DEVERR_BOUNDS;
             f(s, ok ? a.more : 0, returns ? a.back : 0, ok ? a.fresh : 0);
         }
     };
@@ -168,7 +183,8 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
         got.b += back;
         got.c += fresh;
     });
-    Sums at = prefix(got, warp_sums[1], &sum);
+    // (Every thread is past the first sums when the second ones have been joined.)
+    Sums at = prefix(got, warp_sums[dry ? 0 : 1], &sum);
     each([&](int s, int more, int back, int fresh) {
         take[s] = (int32_t)at.a;
         give[s] = (int32_t)at.b;
