@@ -537,8 +537,9 @@ ua_status ua_cache_evict(ua_problem *p, void *k_cache, void *v_cache, const int3
  *                  token get position 0 and slot -1
  * Malformed lengths (negative, past max_blocks_per_seq * b, past parents_stride or 32 *
  * mask_stride) get nothing and seqused_k = 0; these and tokens past max_tokens are
- * reported (UA_DEVERR_BOUNDS).  A bad block id gives the slot -1 (UA_DEVERR_BLOCK_ID), a
- * bad parent ends its branch (UA_DEVERR_TREE).
+ * reported (UA_DEVERR_BOUNDS).  A bad block id gives the slot -1 and is reported, also
+ * where it is given back (UA_DEVERR_BLOCK_ID; it goes to the pool all the same), a bad
+ * parent ends its branch (UA_DEVERR_TREE).
  * Needs num_seqs <= 16384 (else UA_ERR_UNSUPPORTED).  Arrays may not overlap otherwise.
  */
 ua_status ua_plan_step(ua_problem *p, int32_t *block_table, int32_t *blocks_held,

@@ -216,7 +216,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanParams p) {
         if (id < 0 || (int64_t)id >= p.num_blocks) err |= UA_DEVERR_BLOCK_ID;
         p.block_table[(int64_t)s * p.bt_stride + p.held[s] + ((int)k - take[s])] = id;
     }
-    for (int64_t r = T + first; r < R; r += step) p.pool[count + R - 1 - r] = returned((int)r);
+    for (int64_t r = T + first; r < R; r += step) {
+        const int32_t id = returned((int)r);
+        if (id < 0 || (int64_t)id >= p.num_blocks) err |= UA_DEVERR_BLOCK_ID;
+        p.pool[count + R - 1 - r] = id;
+    }
 
     // 4. Tokens.  Chains without a mask four at a time, which nearly always are neighbours
     // in one block.

@@ -70,3 +70,26 @@ def test_plans_whose_sums_need_more_shared_memory(n):
         new = [int(x) for x in g.integers(0, 5, n)]
         st.step(new, sum(new) + 3, [S.grow(g, k) for k in new] if tree else None, 1 if tree else 0)
         st.step([0] * n, 1)
+
+
+@pytest.mark.parametrize("bad", [-1, 200, 2 ** 31 - 1, -2 ** 31])
+@pytest.mark.parametrize("taken", [False, True])
+def test_bad_ids_that_are_given_back_are_reported(bad, taken):
+    """When they go to the pool, not only when somebody takes them from there again."""
+    st = Planned(2600, 4, 16, pool=5, ctx=[40, 16, 33, 0], spare=0)
+    st.ref.table[2][1] = bad
+    st.upload()
+    want = [st.ref.table[2][0], bad, st.ref.table[2][2]]
+    new = [0, 0, 0, 16 * 2 if taken else 0]
+    out = st.outputs(40)
+    st.problem.plan_step(st.table, st.held, st.pool, st.left, i32([40, 16, 0, 0]), i32(new), 4, 40, **out)
+    assert st.problem.check_device_error() == S.BLOCK_ID
+    same(st.held, [3, 1, 0, 2 if taken else 0])
+    same(st.left, [6 if taken else 8])
+    # The first returned block lies on top; the last one below the others.
+    if taken:
+        same(st.table[3, :2], want[:2])
+        same(out["slots"][:32], [want[0] * 16 + i for i in range(16)] + [-1] * 16)
+        same(st.pool[:6], st.ref.pool + want[2:])
+    else:
+        same(st.pool[:8], st.ref.pool + want[::-1])
