@@ -570,9 +570,10 @@ ua_status ua_set_rope(ua_problem *p, const double *inv_freq, int32_t n, uint32_t
  * ua_rope_store -- rotate q and k by the tokens' positions and write k and v into the
  * caches.  A pair (x, y) with angle phi = position * inv_freq[i] becomes
  *     magnitude * (x cos phi - y sin phi, x sin phi + y cos phi)
- * in fp32, rounded once to bf16; other dims stay.  The angle keeps its fraction of a
- * turn to 2^-32 at any position.  Keys are then stored like ua_cache_store does, from
- * the rounded values.
+ * in fp32, rounded once to bf16; other dims stay.  The angle's fraction of a turn is off
+ * by 2^-25 at most, at any position (the frequency is taken to 2^-65 of a turn per
+ * position, the fraction becomes an fp32 number).  Keys are then stored like
+ * ua_cache_store does, from the rounded values.
  *   q              bf16 [total_q, H_q, d], tokens q_stride elements apart
  *   k_new, v_new   bf16 [total_q, H_k, d], tokens kv_stride elements apart
  *   q_out          bf16 [total_q, H_q, d], tokens out_stride elements apart; q itself

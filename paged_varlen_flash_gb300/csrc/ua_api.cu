@@ -495,6 +495,19 @@ bool on_device(const ua_problem* p) {
     return dev == p->device;
 }
 
+// f / 2 pi (0 <= f <= 6: below one turn) times 2^64, to the nearest integer: the double's 53 bits
+// times 1 / 2 pi to 128 bits.  (A product of doubles is off by up to 2^11, which at position
+// 2^31 are 2^-22 of a turn.)
+uint64_t turn_of(double f) {
+    using U128 = unsigned __int128;
+    constexpr uint64_t hi = 0x28be60db9391054au, lo = 0x7f09d5f47d4d3770u;    // 2^128 / 2 pi
+    int e = 0;
+    const uint64_t m = (uint64_t)std::ldexp(std::frexp(f, &e), 53);
+    const U128 x = (U128)m * hi + (uint64_t)((U128)m * lo >> 64);              // m 2^64 / 2 pi, below 2^115
+    const int shift = 53 - e;                                                  // f = m 2^-shift; 50 at least, or m = 0
+    return shift < 50 || shift > 127 ? 0 : (uint64_t)((x + ((U128)1 << (shift - 1))) >> shift);
+}
+
 bool aligned16(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 
 ua::CacheParams cache_params(const ua_problem* p, const void* k_cache, const void* v_cache,
@@ -969,8 +982,7 @@ ua_status ua_set_rope(ua_problem* p, const double* inv_freq, int32_t n, uint32_t
     ua::RopeTable t{};
     for (int i = 0; i < n; ++i) {
         if (!(inv_freq[i] >= 0. && inv_freq[i] <= 6.)) return UA_ERR_INVALID_ARG;
-        // Below one turn, so that the product is below 2^64.
-        t.turn[i] = (uint64_t)(inv_freq[i] * (0x1p63 / 3.14159265358979323846));
+        t.turn[i] = turn_of(inv_freq[i]);
     }
     t.n = n;
     t.pairs = layout == UA_ROPE_PAIRS;

@@ -5,8 +5,9 @@
 //     m (a cos(phi) - b sin(phi)),  m (a sin(phi) + b cos(phi)),   phi = pos * f_i.
 // The angle is kept as a fraction of a turn in 64 bits: pos * round(2^64 f_i / 2 pi)
 // modulo 2^64 drops the whole turns exactly, so that the fraction is off by at most
-// |pos| 2^-65 turns wherever the position lies, where an fp32 product would be off by
-// |pos f| 2^-24.  Its upper 32 bits go to sincospi.
+// |pos| 2^-65 turns (2^-34 at the last position), where an fp32 product would be off by
+// |pos f| 2^-24.  Its upper 32 bits go to sincospi as an fp32 number: 2^-32 of a turn cut
+// off, and 2^-26 rounded away at most, at any position.
 //
 // One CTA per token, bound by HBM for prompts.  A thread owns two runs of 8 dims of every
 // 16th (8th, 32nd) row: (j ..) and (j + n ..) where halves are paired, so that a pair is
