@@ -351,8 +351,10 @@ def rope_frequencies(rotated, base=10000.0, scaling=None, factor=1.0, trained=0,
                     divides the lowest frequency by ``factor`` and keeps the highest;
     * ``"bands"``   divided by ``factor`` where fewer than ``low`` turns fit the
                     ``trained`` context, kept from ``high`` turns on, linear between;
-    * ``"yarn"``    the same between the dims of ``high`` and ``low`` turns, linear in
-                    the dim, and cos and sin times 0.1 ln(factor) + 1.
+    * ``"yarn"``    the same, linear in the pair's number between the (whole) ones that
+                    make ``high`` and ``low`` turns (cut at 0 and ``rotated`` - 1, which
+                    may lie behind the last pair), and cos and sin times
+                    0.1 ln(factor) + 1.
     """
     n = rotated // 2
     if rotated < 2 or rotated % 2 or base <= 0 or factor <= 0:
@@ -374,9 +376,9 @@ def rope_frequencies(rotated, base=10000.0, scaling=None, factor=1.0, trained=0,
     if scaling == "bands":
         keep = [(t - low) / (high - low) for t in turns]
     else:
-        # The (fractional) dim at which `turns` turns fit the trained context.
+        # The (fractional) number of a pair that makes `turns` turns in the trained context.
         dim = lambda t: n * math.log(trained / (2 * math.pi * t)) / math.log(base)  # noqa: E731
-        first, end = max(math.floor(dim(high)), 0), min(math.ceil(dim(low)), n - 1)
+        first, end = max(math.floor(dim(high)), 0), min(math.ceil(dim(low)), rotated - 1)
         keep = [1 - (i - first) / max(end - first, 1e-3) for i in range(n)]
     keep = [min(1.0, max(0.0, k)) for k in keep]
     return ([f * (k + (1 - k) / factor) for f, k in zip(freq, keep)],

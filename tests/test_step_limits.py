@@ -1,5 +1,10 @@
-"""Refusals of the step calls that a launch must not be needed for: the library's, in a
-process without a GPU, and the binding's.  CPU only."""
+"""Refusals of the step calls that a launch must not be needed for, in a process without a
+GPU, and frequencies of long trained contexts.  CPU only."""
+import math
+
+import pytest
+
+import paged_varlen_flash_gb300 as ua
 from tests.test_problem_create import run  # noqa: F401
 
 TREE = """
@@ -29,3 +34,19 @@ for kind in (ua.UA_DTYPE_BF16, ua.UA_DTYPE_FP8_E4M3, ua.UA_DTYPE_FP4_E2M1):
     assert tree(p, max_k=(1 << 30) + 1) == 2 and tree(p, max_k=1 << 30) == 3, kind
     ua.ua_destroy(p)
 """)
+
+
+@pytest.mark.parametrize("rotated,base,trained,factor", [(128, 10000.0, 131072, 4.0), (128, 10000.0, 131072, 8.0),
+                                                         (64, 500000.0, 1 << 25, 2.0), (16, 100.0, 4096, 8.0)])
+def test_yarn_ramps_that_end_behind_the_last_pair(rotated, base, trained, factor):
+    """Where even the last pair makes more than ``low`` turns, it keeps a part of its frequency."""
+    n, low, high = rotated // 2, 1.0, 32.0
+    plain = ua.rope_frequencies(rotated, base)[0]
+    yarn, _ = ua.rope_frequencies(rotated, base, "yarn", factor, trained, low, high)
+    number = lambda turns: n * math.log(trained / (2 * math.pi * turns), base)  # noqa: E731
+    first, end = math.floor(number(high)), min(math.ceil(number(low)), rotated - 1)
+    assert trained * plain[-1] / (2 * math.pi) > low and end >= n
+    for i, (f, y) in enumerate(zip(plain, yarn)):
+        keep = min(1.0, 1 - (i - first) / (end - first))
+        assert math.isclose(y, f * (keep + (1 - keep) / factor), rel_tol=1e-9), i
+    assert yarn[-1] > plain[-1] / factor * 1.001
