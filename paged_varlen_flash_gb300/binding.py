@@ -399,11 +399,12 @@ def _token_stride(t, name, total_q=0, num_kv_heads=None, head_size=None):
     stride = t.stride()
     if len(stride) != 3:
         raise ValueError("%s must be [total_q, H_k, d]" % name)
+    step, head, unit = stride
     n, heads, dims = t.shape
-    if (stride[2] != 1 or (heads > 1 and stride[1] != dims) or n < total_q or
+    if (unit != 1 or (heads > 1 and head != dims) or n < total_q or
             (num_kv_heads is not None and (heads != num_kv_heads or dims != head_size))):
         raise ValueError("%s must be [total_q, H_k, d] with contiguous heads" % name)
-    return stride[0] if n > 1 else max(stride[0], heads * dims)
+    return step if n > 1 else max(step, heads * dims)
 
 
 def _weight_stride(t, name):
@@ -435,16 +436,32 @@ def _refuse_vector(t, name, n, kind, device):
     raise ValueError("%s must be %s, on the device of the other tensors" % (name, kind))
 
 
-_int_types = None
+_element_types = None
+
+
+def _types():
+    """int32, int64, bf16, fp32, and those of the caches by kv_dtype (torch is not imported
+    with this module)."""
+    global _element_types
+    if _element_types is None:
+        import torch
+        codes = torch.uint8, torch.float8_e4m3fn
+        _element_types = (torch.int32, torch.int64, torch.bfloat16, torch.float32,
+                          {UA_DTYPE_BF16: (torch.bfloat16,), UA_DTYPE_FP8_E4M3: codes, UA_DTYPE_FP4_E2M1: codes[:1]})
+    return _element_types
 
 
 def _ints():
-    """torch.int32 and torch.int64 (torch is not imported with this module)."""
-    global _int_types
-    if _int_types is None:
-        import torch
-        _int_types = torch.int32, torch.int64
-    return _int_types
+    """torch.int32 and torch.int64."""
+    return _types()[:2]
+
+
+def _head_terms(t, name, num_q_heads, device):
+    """The address of sinks or slopes, a contiguous fp32 [H_q]."""
+    if (t.dtype is not _types()[3] or t.numel() < num_q_heads or not t.is_contiguous() or
+            t.get_device() != device):
+        _refuse_vector(t, name, num_q_heads, "float32", device)
+    return t.data_ptr()
 
 
 def _check_table(table, num_seqs, width, device):
@@ -555,12 +572,30 @@ class Problem:
                                         max_total_q, flags, scale, softcap, window, path,
                                         kv_dtype, k_scale, v_scale, split_partials)
         self.flags = flags
+        self.kv_dtype = kv_dtype
+        self._cache_shape = cache_shape(num_blocks, num_kv_heads, head_size, block_size, kv_dtype)
         self.head_size = head_size
         self.block_size = block_size
         self.num_blocks = num_blocks
         self.max_blocks_per_seq = max_blocks_per_seq
         self.num_q_heads = num_q_heads
         self.num_kv_heads = num_kv_heads
+
+    kv_dtype, _cache_shape = UA_DTYPE_BF16, None
+
+    def _check_caches(self, k_cache, v_cache, device):
+        """Refuse caches that are not the problem's: kernels would read or write past them."""
+        shape, types = self._cache_shape, _types()[4][self.kv_dtype]
+        kind = types[0]
+        if (k_cache.shape == shape and v_cache.shape == shape and k_cache.dtype is kind and v_cache.dtype is kind and
+                k_cache.is_contiguous() and v_cache.is_contiguous() and k_cache.get_device() == v_cache.get_device() == device):
+            return                       # (the usual case, in as few calls as it takes)
+        shape = cache_shape(self.num_blocks, self.num_kv_heads, self.head_size, self.block_size, self.kv_dtype)
+        for t in (k_cache, v_cache):
+            if (t.dtype not in types or t.shape[1:] != shape[1:] or t.shape[0] < shape[0] or not t.is_contiguous() or
+                    t.get_device() != device):
+                raise ValueError("k_cache and v_cache must be contiguous %s of %s, on the device of the other tensors" % (
+                    list(shape), " or ".join(map(str, types))))
 
     @classmethod
     def for_workload(cls, w, max_total_q=None, max_num_seqs=None, extra_flags=0,
@@ -741,19 +776,19 @@ class Problem:
         """Rotate q and k (bf16 [total_q, heads, d]; tokens may be strided) by
         ``positions`` and write k and v to ``slots`` (int64; negative: not stored).
         Returns the rotated q (``q_out``, which may be q)."""
-        i32, i64 = _ints()
-        device = k_cache.get_device()
-        q_stride = _token_stride(q, "q", total_q, self.num_q_heads, self.head_size)
-        stride = _token_stride(k_new, "k_new", total_q, self.num_kv_heads, self.head_size)
-        if _token_stride(v_new, "v_new", total_q, self.num_kv_heads, self.head_size) != stride:
-            raise ValueError("k_new and v_new must share a token stride")
+        i32, i64, bf16 = _types()[:3]
+        device, heads, kv_heads, d = k_cache.get_device(), self.num_q_heads, self.num_kv_heads, self.head_size
+        self._check_caches(k_cache, v_cache, device)
         if q_out is None:
             q_out = _empty_like(q, stream)
-        out_stride = _token_stride(q_out, "q_out", total_q, self.num_q_heads, self.head_size)
-        _check(q, "q", "torch.bfloat16", device)
-        _check(k_new, "k_new", "torch.bfloat16", device)
-        _check(v_new, "v_new", "torch.bfloat16", device)
-        _check(q_out, "q_out", "torch.bfloat16", device)
+        q_stride = _token_stride(q, "q", total_q, heads, d)
+        stride = _token_stride(k_new, "k_new", total_q, kv_heads, d)
+        out_stride = _token_stride(q_out, "q_out", total_q, heads, d)
+        if _token_stride(v_new, "v_new", total_q, kv_heads, d) != stride:
+            raise ValueError("k_new and v_new must share a token stride")
+        if not (q.dtype is bf16 and k_new.dtype is bf16 and v_new.dtype is bf16 and q_out.dtype is bf16 and
+                q.get_device() == k_new.get_device() == v_new.get_device() == q_out.get_device() == device):
+            raise ValueError("q, k_new, v_new and q_out must be torch.bfloat16, on the device of the caches")
         if positions.dtype is not i32 or positions.numel() < total_q or not positions.is_contiguous() or (
                 positions.get_device() != device):
             _refuse_vector(positions, "positions", total_q, "int32", device)
@@ -781,6 +816,12 @@ class Problem:
         if not q.is_contiguous() or q.numel() < total_q * row:
             raise ValueError("q must be a contiguous [total_q, H_q, d]")
         _check(q, "q", "torch.bfloat16", device)
+        self._check_caches(k_cache, v_cache, device)
+        sink = slope = None
+        if sinks is not None:
+            sink = _head_terms(sinks, "sinks", self.num_q_heads, device)
+        if alibi_slopes is not None:
+            slope = _head_terms(alibi_slopes, "alibi_slopes", self.num_q_heads, device)
         i32 = _ints()[0]
         for t, n, name in ((cu_seqlens_q, num_seqs + 1, "cu_seqlens_q"), (seqused_k, num_seqs, "seqused_k")):
             if t.dtype is not i32 or t.numel() < n or not t.is_contiguous() or t.get_device() != device:
@@ -799,7 +840,7 @@ class Problem:
         st = load_library().ua_forward_tree(
             self.handle, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
             cu_seqlens_q.data_ptr(), seqused_k.data_ptr(), num_seqs, total_q, max_seqlen_q, max_seqlen_k,
-            tree_mask.data_ptr(), words, places, flags, _ptr(sinks), _ptr(alibi_slopes), out.data_ptr(), _stream(stream))
+            tree_mask.data_ptr(), words, places, flags, sink, slope, out.data_ptr(), _stream(stream))
         if st != UA_OK:
             raise UAError(st, "ua_forward_tree")
         return out
@@ -810,11 +851,13 @@ class Problem:
         right behind the context.  Out: ``path`` (int32 [num_seqs, n], -1 behind the
         branch), ``accepted`` (its length) and ``seqused_out``."""
         device = k_cache.get_device()
+        self._check_caches(k_cache, v_cache, device)
         stride = _tree_rows(parents, num_seqs, device)
         if parents.shape[1] < max_seqlen_q:
             raise ValueError("parents must have a column per node")
         _check_table(block_table, num_seqs, self.max_blocks_per_seq, device)
-        if path.dim() != 2 or path.shape[0] != num_seqs or path.shape[1] < 1:
+        wide = path.shape
+        if len(wide) != 2 or wide[0] != num_seqs or wide[1] < 1:
             raise ValueError("path must be [num_seqs, n]")
         i32 = _ints()[0]
         for t, n, name in ((path, 1, "path"), (cu_seqlens_q, num_seqs + 1, "cu_seqlens_q"),
@@ -825,7 +868,7 @@ class Problem:
         st = load_library().ua_cache_accept(
             self.handle, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), cu_seqlens_q.data_ptr(),
             seqused_k.data_ptr(), parents.data_ptr(), stride, last.data_ptr(), num_seqs, total_q, max_seqlen_q,
-            max_seqlen_k, path.data_ptr(), path.shape[1], accepted.data_ptr(), seqused_out.data_ptr(), _stream(stream))
+            max_seqlen_k, path.data_ptr(), wide[1], accepted.data_ptr(), seqused_out.data_ptr(), _stream(stream))
         if st != UA_OK:
             raise UAError(st, "ua_cache_accept")
 
