@@ -574,6 +574,7 @@ class Problem:
         self.flags = flags
         self.kv_dtype = kv_dtype
         self._cache_shape = cache_shape(num_blocks, num_kv_heads, head_size, block_size, kv_dtype)
+        self._cache_bytes = math.prod(self._cache_shape) * (2 if kv_dtype == UA_DTYPE_BF16 else 1)
         self.head_size = head_size
         self.block_size = block_size
         self.num_blocks = num_blocks
@@ -597,6 +598,18 @@ class Problem:
                 raise ValueError("k_cache and v_cache must be contiguous %s of %s, on the device of the other tensors" % (
                     list(shape), " or ".join(map(str, types))))
 
+    _cache_bytes = 0
+
+    def _check_room(self, k_cache, v_cache):
+        """Refuse tensors that are shorter than the problem's caches, or not contiguous: kernels
+        would read or write past them.  (Addresses are taken as they are.)"""
+        n = self._cache_bytes
+        for t in (k_cache, v_cache):
+            if t is None or isinstance(t, int):
+                continue
+            if t.nbytes < n or not t.is_contiguous():
+                raise ValueError("k_cache and v_cache must be contiguous, with %d bytes at least" % n)
+
     @classmethod
     def for_workload(cls, w, max_total_q=None, max_num_seqs=None, extra_flags=0,
                      path=UA_PATH_AUTO, split_partials=UA_PARTIALS_F32):
@@ -611,6 +624,7 @@ class Problem:
     def forward(self, q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, num_seqs,
                 total_q, max_seqlen_q, max_seqlen_k, flags, sinks=None, alibi_slopes=None,
                 out=None, stream=None):
+        self._check_room(k_cache, v_cache)
         if out is None:
             out = _empty_like(q, stream)
         st = ua_forward(self.handle, q, k_cache, v_cache, block_table, cu_seqlens_q,
@@ -623,6 +637,7 @@ class Problem:
     def forward_topk(self, q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k,
                      num_seqs, total_q, max_seqlen_q, max_seqlen_k, topk_idx, topk_len, flags,
                      sinks=None, alibi_slopes=None, out=None, stream=None):
+        self._check_room(k_cache, v_cache)
         if out is None:
             out = _empty_like(q, stream)
         if topk_idx.dim() != 2 or topk_idx.stride(1) != 1:
@@ -641,6 +656,7 @@ class Problem:
         """``forward`` that also writes decay * weights_in plus this call's
         attention weights to ``weights_out`` (fp32 [num_seqs, H_k, n >= max_seqlen_k];
         ``weights_in`` may be the same tensor, or None for zeros)."""
+        self._check_room(k_cache, v_cache)
         rows = num_seqs, self.num_kv_heads, max_seqlen_k, q
         stride = _weight_rows(weights_out, "weights_out", *rows)
         if weights_in is not None and _weight_rows(weights_in, "weights_in", *rows) != stride:
@@ -659,6 +675,7 @@ class Problem:
                     num_seqs, total_q, max_seqlen_q, max_seqlen_k, stream=None):
         """Write a chunk's rows (bf16 [total_q, H_k, d]; tokens may be strided)
         to the positions ``forward`` expects them at."""
+        self._check_room(k_cache, v_cache)
         stride = _token_stride(k_new, "k_new", total_q, self.num_kv_heads, self.head_size)
         device = k_cache.get_device()
         _check(k_new, "k_new", "torch.bfloat16", device)
@@ -677,6 +694,7 @@ class Problem:
                      v_out, out_block_table, begin=None, stream=None):
         """Expand the keys from ``begin`` (or 0) on into the bf16 pages
         ``k_out`` / ``v_out`` [blocks, b, H_k, d]."""
+        self._check_room(k_cache, v_cache)
         step, device = out_block_table.stride(), k_cache.get_device()
         if len(step) != 2 or step[1] != 1 or out_block_table.shape[0] < num_seqs:
             raise ValueError("out_block_table must be [num_seqs, n] with unit inner stride")
@@ -705,6 +723,7 @@ class Problem:
         """Keep ``budget`` keys of every (sequence, KV head) by weight, in place
         or into ``dst_block_table`` (rows as far apart as block_table's); ``kept``
         int32 [num_seqs, H_k, budget]."""
+        self._check_room(k_cache, v_cache)
         rows = num_seqs, self.num_kv_heads, max_seqlen_k, block_table
         stride = _weight_rows(weights_in, "weights_in", *rows)
         if _weight_rows(weights_out, "weights_out", *rows) != stride:

@@ -1,6 +1,8 @@
-"""What the step calls of ``Problem`` refuse of caches, sinks and slopes that the kernels
-would read or write past.  CPU only: the problem has no handle, so that a call whose arguments
+"""What the calls of ``Problem`` refuse of caches, and the step calls of sinks and slopes, that
+the kernels would read or write past.  CPU only: the problem has no handle, so that a call whose arguments
 pass ends in the library's "invalid argument"."""
+import math
+
 import pytest
 import torch
 
@@ -19,6 +21,7 @@ def problem(kind, known=True):
     x.block_size, x.max_blocks_per_seq, x.num_blocks = B, WIDTH, BLOCKS
     if known:
         x._cache_shape = ua.cache_shape(BLOCKS, HK, D, B, kind)
+        x._cache_bytes = math.prod(x._cache_shape) * KINDS[kind].itemsize
     return x
 
 
@@ -86,3 +89,42 @@ def test_sinks_and_slopes_of_tree_calls():
         for name in ("sinks", "alibi_slopes"):
             with pytest.raises(ValueError):
                 call(**{name: bad})
+
+
+def other_calls(p):
+    rows = i32(N, WIDTH), i32(N + 1), i32(N)
+    w, pages = torch.zeros(N, HK, 50), bf(4, B, HK, D)
+    return [
+        lambda k, v: p.forward(bf(T, HQ, D), k, v, *rows, N, T, 5, 50, ua.UA_FLAG_CAUSAL, stream=0),
+        lambda k, v: p.forward_topk(bf(T, HQ, D), k, v, *rows, N, T, 5, 50, i32(T, 8), i32(T), ua.UA_FLAG_CAUSAL, stream=0),
+        lambda k, v: p.forward_weights(bf(T, HQ, D), k, v, *rows, N, T, 5, 50, ua.UA_FLAG_CAUSAL, None, w, stream=0),
+        lambda k, v: p.cache_store(bf(T, HK, D), bf(T, HK, D), k, v, *rows, N, T, 5, 50, stream=0),
+        lambda k, v: p.cache_expand(k, v, rows[0], rows[2], N, 50, pages, pages, rows[0], stream=0),
+        lambda k, v: p.cache_evict(k, v, rows[0], rows[2], N, 50, w, w, 10, 2, i32(N, HK, 10), i32(N), stream=0),
+    ]
+
+
+@pytest.mark.parametrize("kind", list(KINDS))
+def test_caches_of_the_other_calls(kind):
+    """Whatever their shape, they are as long as the problem's."""
+    p = problem(kind)
+    shape, dtype = ua.cache_shape(BLOCKS, HK, D, B, kind), KINDS[kind]
+    good = torch.zeros(*shape, dtype=dtype)
+    for call in other_calls(p):
+        for k, v in ((good, good), (good.flatten(), good.view(torch.uint8)), (torch.cat([good, good]), good)):
+            reaches_the_library(lambda: call(k, v))
+        for bad in (good[1:], good.flatten()[1:], torch.cat([good, good], -1)[..., ::2], torch.cat([good, good], 1)[:, ::2]):
+            for k, v in ((bad, good), (good, bad)):
+                with pytest.raises(ValueError):
+                    call(k, v)
+    # Addresses say nothing about what is behind them.
+    a = 1 << 12
+    reaches_the_library(lambda: p.forward(a, a, a, a, a, a, N, T, 5, 50, ua.UA_FLAG_CAUSAL, out=a, stream=0))
+
+
+def test_what_a_problem_knows_of_its_caches(monkeypatch):
+    monkeypatch.setattr(ua.binding, "ua_problem_create", lambda *a: None)
+    for kind, bits in ((ua.UA_DTYPE_BF16, 16), (ua.UA_DTYPE_FP8_E4M3, 8), (ua.UA_DTYPE_FP4_E2M1, 4.5)):
+        p = ua.Problem(HQ, HK, D, B, BLOCKS, N, WIDTH, T, ua.UA_FLAG_CAUSAL, 0.1, kv_dtype=kind)
+        assert p.kv_dtype == kind and p._cache_shape == ua.cache_shape(BLOCKS, HK, D, B, kind)
+        assert p._cache_bytes == BLOCKS * B * HK * D * bits / 8
