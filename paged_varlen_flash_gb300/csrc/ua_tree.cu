@@ -126,10 +126,12 @@ __device__ __forceinline__ void store32b(void* dst, const uint32_t* v) {
                  : "memory");
 }
 
+// (Not to be moved in front of the wait for the kernel in front, which may write what it reads.)
 __device__ __forceinline__ void load32b(uint32_t* v, const void* src) {
-    asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "l"(src));
+                 : "l"(src)
+                 : "memory");
 }
 
 // Values that are not finite among a row's visible V of keys [beg, end): the sum of

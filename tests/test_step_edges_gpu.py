@@ -51,3 +51,34 @@ def test_alibi_positions_outside_the_chunk_are_reported(kind, d, at, moved):
     bt.pos[0][2] = at
     bt.check(bt.run(p, ua.UA_FLAG_CAUSAL))
     assert p.check_device_error() == 0
+
+
+# ---------------------------------------------------------------- early starts
+@pytest.mark.parametrize("d,words", [(64, 16), (128, 16), (256, 16), (256, 8)])
+def test_q_that_the_kernel_in_front_writes(d, words):
+    """The same q buffer, written anew in front of every call (words: its alignment in 16-bit
+    words, whole or half sectors): each call reads what was written last."""
+    bt = Trees(2700 + d, 16, 2, d, 16, (64, 20), (200, 90)).device()
+    p = bt.problem()
+    mask = torch.from_numpy(bt.mask.view(np.int32)).cuda()
+    room = torch.zeros(bt.d_q.numel() + 64, dtype=torch.bfloat16, device="cuda")
+    q = room[words:words + bt.d_q.numel()].view(bt.d_q.shape)
+    assert q.data_ptr() % 32 == 2 * words % 32
+    rows = [torch.randn(bt.d_q.shape, device="cuda").to(torch.bfloat16) for _ in range(16)]
+    outs = [torch.empty_like(bt.d_q) for _ in rows]
+
+    def call(out):
+        p.forward_tree(q, bt.d_k, bt.d_v, bt.d_table, bt.d_cu, bt.d_sk, 2, 84, 64, 200, ua.UA_FLAG_CAUSAL, mask, out=out)
+
+    for x, out in zip(rows, outs):
+        q.copy_(x)
+        call(out)
+    torch.cuda.synchronize()
+    want = torch.empty_like(bt.d_q)
+    for x, out in zip(rows, outs):
+        q.copy_(x)
+        torch.cuda.synchronize()
+        call(want)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert p.check_device_error() == 0
