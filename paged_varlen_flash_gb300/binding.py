@@ -436,29 +436,40 @@ def _refuse_vector(t, name, n, kind, device):
     raise ValueError("%s must be %s, on the device of the other tensors" % (name, kind))
 
 
-_element_types = None
-
-
-def _types():
-    """int32, int64, bf16, fp32, and those of the caches by kv_dtype (torch is not imported
-    with this module)."""
-    global _element_types
-    if _element_types is None:
-        import torch
-        codes = torch.uint8, torch.float8_e4m3fn
-        _element_types = (torch.int32, torch.int64, torch.bfloat16, torch.float32,
-                          {UA_DTYPE_BF16: (torch.bfloat16,), UA_DTYPE_FP8_E4M3: codes, UA_DTYPE_FP4_E2M1: codes[:1]})
-    return _element_types
+_int_types = _row_types = _cache_types = None
 
 
 def _ints():
-    """torch.int32 and torch.int64."""
-    return _types()[:2]
+    """torch.int32 and torch.int64 (torch is not imported with this module)."""
+    global _int_types
+    if _int_types is None:
+        import torch
+        _int_types = torch.int32, torch.int64
+    return _int_types
+
+
+def _rows():
+    """torch.bfloat16 and torch.float32."""
+    global _row_types
+    if _row_types is None:
+        import torch
+        _row_types = torch.bfloat16, torch.float32
+    return _row_types
+
+
+def _types_of(kv_dtype):
+    """The element types of a cache of that kv_dtype."""
+    global _cache_types
+    if _cache_types is None:
+        import torch
+        codes = torch.uint8, torch.float8_e4m3fn
+        _cache_types = {UA_DTYPE_BF16: (torch.bfloat16,), UA_DTYPE_FP8_E4M3: codes, UA_DTYPE_FP4_E2M1: codes[:1]}
+    return _cache_types[kv_dtype]
 
 
 def _head_terms(t, name, num_q_heads, device):
     """The address of sinks or slopes, a contiguous fp32 [H_q]."""
-    if (t.dtype is not _types()[3] or t.numel() < num_q_heads or not t.is_contiguous() or
+    if (t.dtype is not _rows()[1] or t.numel() < num_q_heads or not t.is_contiguous() or
             t.get_device() != device):
         _refuse_vector(t, name, num_q_heads, "float32", device)
     return t.data_ptr()
@@ -473,14 +484,14 @@ def _check_table(table, num_seqs, width, device):
 
 
 def _tree_rows(parents, num_seqs, device):
-    """Elements between the rows of the trees' parents [num_seqs, n]."""
+    """Elements between the rows of the trees' parents [num_seqs, n], and n."""
     shape, stride = parents.shape, parents.stride()
     if len(shape) != 2 or shape[0] < num_seqs or shape[1] < 1 or (shape[1] > 1 and stride[1] != 1) or (
             shape[0] > 1 and stride[0] < shape[1]):
         raise ValueError("parents must be [num_seqs, nodes] with unit inner stride")
     if parents.dtype is not _ints()[0] or parents.get_device() != device:
         raise ValueError("parents must be int32, on the device of the other tensors")
-    return stride[0] if shape[0] > 1 else shape[1]
+    return stride[0] if shape[0] > 1 else shape[1], shape[1]
 
 
 def _mask_stride(mask, tokens, device):
@@ -586,7 +597,7 @@ class Problem:
 
     def _check_caches(self, k_cache, v_cache, device):
         """Refuse caches that are not the problem's: kernels would read or write past them."""
-        shape, types = self._cache_shape, _types()[4][self.kv_dtype]
+        shape, types = self._cache_shape, _types_of(self.kv_dtype)
         kind = types[0]
         if (k_cache.shape == shape and v_cache.shape == shape and k_cache.dtype is kind and v_cache.dtype is kind and
                 k_cache.is_contiguous() and v_cache.is_contiguous() and k_cache.get_device() == v_cache.get_device() == device):
@@ -605,10 +616,12 @@ class Problem:
         would read or write past them.  (Addresses are taken as they are.)"""
         n = self._cache_bytes
         for t in (k_cache, v_cache):
-            if t is None or isinstance(t, int):
+            try:
+                if t.nbytes >= n and t.is_contiguous():
+                    continue
+            except AttributeError:
                 continue
-            if t.nbytes < n or not t.is_contiguous():
-                raise ValueError("k_cache and v_cache must be contiguous, with %d bytes at least" % n)
+            raise ValueError("k_cache and v_cache must be contiguous, with %d bytes at least" % n)
 
     @classmethod
     def for_workload(cls, w, max_total_q=None, max_num_seqs=None, extra_flags=0,
@@ -772,7 +785,7 @@ class Problem:
         tree = mask = None
         stride = words = 0
         if parents is not None:
-            tree, stride = parents.data_ptr(), _tree_rows(parents, num_seqs, device)
+            tree, stride = parents.data_ptr(), _tree_rows(parents, num_seqs, device)[0]
         if tree_mask is not None:
             mask, words = tree_mask.data_ptr(), _mask_stride(tree_mask, max_tokens, device)
         st = load_library().ua_plan_step(
@@ -795,7 +808,8 @@ class Problem:
         """Rotate q and k (bf16 [total_q, heads, d]; tokens may be strided) by
         ``positions`` and write k and v to ``slots`` (int64; negative: not stored).
         Returns the rotated q (``q_out``, which may be q)."""
-        i32, i64, bf16 = _types()[:3]
+        i32, i64 = _ints()
+        bf16 = _rows()[0]
         device, heads, kv_heads, d = k_cache.get_device(), self.num_q_heads, self.num_kv_heads, self.head_size
         self._check_caches(k_cache, v_cache, device)
         if q_out is None:
@@ -871,8 +885,8 @@ class Problem:
         branch), ``accepted`` (its length) and ``seqused_out``."""
         device = k_cache.get_device()
         self._check_caches(k_cache, v_cache, device)
-        stride = _tree_rows(parents, num_seqs, device)
-        if parents.shape[1] < max_seqlen_q:
+        stride, nodes = _tree_rows(parents, num_seqs, device)
+        if nodes < max_seqlen_q:
             raise ValueError("parents must have a column per node")
         _check_table(block_table, num_seqs, self.max_blocks_per_seq, device)
         wide = path.shape
