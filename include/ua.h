@@ -94,8 +94,8 @@ enum {
 /* Element types.  Q, O: bf16.  K/V caches: bf16, or fp8 e4m3 codes (one byte
  * each; OCP e4m3: bias 7, subnormals, no infinities, 0x7f / 0xff NaN) with one
  * scale per tensor, K = code * k_scale, V = code * v_scale (gfx950 page,
- * section 7.3 "fp8 KV cache (bf16-Q + fp8-KV)").  The fp8 cache is read by
- * the DECODE_TC path only.
+ * section 7.3 "fp8 KV cache (bf16-Q + fp8-KV)").  ua_forward reads an fp8
+ * cache on its DECODE_TC path only; the other calls say what they need.
  *
  * UA_DTYPE_FP4_E2M1: caches in 4 bits, uint8 [num_blocks, H_k, P] with
  * P = b * (d / 2 + d / 16) bytes for one (block, KV head): first b rows of
@@ -158,8 +158,8 @@ typedef struct ua_problem_desc {
     int32_t window;             /* W >= 1 when UA_FLAG_WINDOW, else ignored */
     uint32_t path;              /* UA_PATH_*: which kernel family serves the calls */
     int32_t kv_dtype;           /* UA_DTYPE_BF16, or UA_DTYPE_FP8_E4M3 (needs d = 128 and
-                                   path AUTO or DECODE_TC; a call whose shape the
-                                   decode kernel does not take returns
+                                   path AUTO or DECODE_TC; a ua_forward call whose
+                                   shape the decode kernel does not take returns
                                    UA_ERR_UNSUPPORTED), or UA_DTYPE_FP4_E2M1 (needs
                                    path AUTO) */
     float k_scale;              /* fp8 / fp4 caches: factor of every K value, > 0; else ignored */
@@ -173,11 +173,12 @@ typedef struct ua_problem ua_problem;
  * Validate *desc and create a problem bound to the current CUDA device.  The
  * problem owns a device workspace (split-KV partials of fp32 (m, l, o), the
  * device error word) that is allocated here, once; ua_forward allocates
- * nothing.  (Of a bf16 cache it has room for the partials of ua_forward_tree: two
- * tiles of up to 128 rows per share of the work, about 41 MB at most.)  Returns UA_ERR_INVALID_ARG for malformed fields (e.g. H_q % H_k !=
- * 0, WINDOW without CAUSAL), UA_ERR_UNSUPPORTED for d or b outside the sets
- * above or a non-bf16 dtype, UA_ERR_OUT_OF_MEMORY if the workspace cannot be
- * allocated.  *out is set only on UA_OK; free it with ua_destroy.
+ * nothing.  (Of a bf16 cache it has room for the partials of ua_forward_tree, whether
+ * it is called or not: two tiles of up to 128 rows per share of the work, about 41 MB
+ * at most.)  Returns UA_ERR_INVALID_ARG for malformed fields (e.g. H_q % H_k != 0,
+ * WINDOW without CAUSAL), UA_ERR_UNSUPPORTED for d or b outside the sets above or a
+ * non-bf16 dtype, UA_ERR_OUT_OF_MEMORY if the workspace cannot be allocated.  *out is
+ * set only on UA_OK; free it with ua_destroy.
  */
 ua_status ua_problem_create(const ua_problem_desc *desc, ua_problem **out);
 

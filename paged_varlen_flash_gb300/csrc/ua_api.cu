@@ -162,7 +162,7 @@ ua_status ua_problem_create(const ua_problem_desc* d, ua_problem** out) {
     if (d->kv_dtype == UA_DTYPE_FP4_E2M1 && d->path != UA_PATH_AUTO)
         return d->path > UA_PATH_DECODE_TC ? UA_ERR_INVALID_ARG : UA_ERR_UNSUPPORTED;
     if (d->kv_dtype == UA_DTYPE_FP8_E4M3) {
-        // Only the decode tensor-core kernel reads an fp8 cache.
+        // The decode tensor-core kernel and the one of draft trees read an fp8 cache, at d = 128.
         if (d->head_size != 128) return UA_ERR_UNSUPPORTED;
         if (d->path != UA_PATH_AUTO && d->path != UA_PATH_DECODE_TC) return UA_ERR_UNSUPPORTED;
     }
@@ -439,8 +439,9 @@ ua_status run_combine(const ua::FwdParams& fp, cudaStream_t st) {
     return UA_ERR_CUDA;
 }
 
-// Attention over a 4-bit cache, or of draft trees over an fp8 one.  With fp->scores the rows' final (m, l) go to
-// the front of the workspace, laid out like the partials of one segment.
+// Attention over a 4-bit cache, or of draft trees over an fp8 one.  With fp->scores the
+// rows' final (m, l) go to the front of the workspace, laid out like the partials of one
+// segment.
 ua_status run_fp4(ua_problem* p, ua::FwdParams* fp, cudaStream_t st) {
     const size_t rows = (size_t)fp->total_q * p->desc.num_q_heads;
     ua::Fp4RowsPlan tiles;

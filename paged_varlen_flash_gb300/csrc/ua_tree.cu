@@ -798,9 +798,8 @@ tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     tc::wait_st();
                 }
                 if (live && j > 0 && __any_sync(0xffffffffu, reanchor)) {
-                    // O holds the P V of the tiles up to j - 1.  With one S tile that product
-                    // was issued in front of this tile's Q K^T, which is complete.
-                    if (C::kBufs == 2 && !(ok = wwait(o_done0 + 8 * ((kt - 1) & 1), ((kt - 1) >> 1) & 1))) break;
+                    // O holds the P V of the tiles up to j - 1, once the last of them is complete.
+                    if (!(ok = wwait(o_done0 + 8 * ((kt - 1) & 1), ((kt - 1) >> 1) & 1))) break;
                     tc::fence_after_sync();
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
