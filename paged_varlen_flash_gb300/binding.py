@@ -615,13 +615,14 @@ class Problem:
         """Refuse tensors that are shorter than the problem's caches, or not contiguous: kernels
         would read or write past them.  (Addresses are taken as they are.)"""
         n = self._cache_bytes
+        try:
+            if k_cache.nbytes >= n and v_cache.nbytes >= n and k_cache.is_contiguous() and v_cache.is_contiguous():
+                return
+        except AttributeError:
+            pass
         for t in (k_cache, v_cache):
-            try:
-                if t.nbytes >= n and t.is_contiguous():
-                    continue
-            except AttributeError:
-                continue
-            raise ValueError("k_cache and v_cache must be contiguous, with %d bytes at least" % n)
+            if hasattr(t, "nbytes") and (t.nbytes < n or not t.is_contiguous()):
+                raise ValueError("k_cache and v_cache must be contiguous, with %d bytes at least" % n)
 
     @classmethod
     def for_workload(cls, w, max_total_q=None, max_num_seqs=None, extra_flags=0,
