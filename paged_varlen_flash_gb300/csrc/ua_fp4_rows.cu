@@ -33,7 +33,7 @@
 // Draft trees (TREE) differ in what a row sees: chunk keys by its row of the mask, the
 // window and ALiBi by the nodes' positions; every tile that reaches past the context is
 // looked at key by key.  64 requests of 16 to 32 nodes, 512 to 8192 keys, 32 / 8 heads,
-// d = 128: 285 us (causal chunks 288); one of 8 nodes, 999 keys, 8 / 2 heads, d = 64: 14.
+// d = 128: 288 us (causal chunks the same); one of 8 nodes, 999 keys, 8 / 2 heads, d = 64: 14.
 //
 // An fp8 cache (F8, trees at d = 128) comes through the tensor maps of its pages, rows of
 // 128 bytes swizzled; its codes are exact in f16 too, and NaN stands in single values. The

@@ -39,7 +39,8 @@
 // Measured: 64 requests of 16 to 32 nodes, 512 to 8192 keys, 32 / 8 heads, d = 128: 205 us,
 // 196 of them this kernel (1.2 GB of K and V, 6.1 TB/s, 0.90 of a plain copy); bound by HBM,
 // then by the ramp at both ends.  4 requests of 64 nodes and 30,000 to 65,535 keys, 16 / 2
-// heads, d = 256: 155 us (1,270 TFLOP/s); about 1,700 cycles a tile of MMAs of 1,024, bound
+// heads, d = 256: 154 us with the same inputs again and again, 166 with others every time
+// (1,280 and 1,180 TFLOP/s); about 1,630 cycles a tile of MMAs of 1,024, bound
 // by the chain softmax -> P V -> Q K^T and L2 (four row tiles read every key, from HBM once).
 // 48 trees of up to 64 nodes, softcap, window 1024, d = 64: 30 us, and one of 8 nodes over
 // 999 keys 12 us: starting, one tile's latency, the epilogue and the merge.
