@@ -1,5 +1,5 @@
-"""Tree calls at the edges of what their documentation allows: batches without rows and
-positions out of range.  Tolerances: tests/test_step_ops_gpu.py."""
+"""Tree calls at the edges of what their documentation allows: batches without rows, positions
+out of range, q written by the kernel in front.  Tolerances: tests/test_step_ops_gpu.py."""
 import numpy as np
 import pytest
 import torch
